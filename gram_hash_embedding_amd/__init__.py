@@ -24,6 +24,13 @@ an exception is raised.
     engram_gather_mx       -- the gather + dequant writing its rows as MX fp8 (no bf16 tensor)
     engram_wkv_mx          -- the wkv projection on MX fp8 operands (fp8 matrix cores with block scales)
     engram_wkv_mx_gate     -- engram_wkv_mx fused with the gate dot (keys reduced in the projection)
+
+and the gradients that train the module and its embeddings (training.py):
+
+    engram_embed           -- rows of a trainable table by id, scaled
+    engram_embed_grad, engram_embed_grad_rows -- its gradient by sorted ids, dense or as the distinct rows
+    engram_gate_output_backward, engram_wkv_backward -- the gradients of engram_gate_output and engram_wkv
+    engram_grad_norm, engram_clip_grads -- the norm of many gradients together, and clipping by it
 """
 from __future__ import annotations
 
@@ -86,6 +93,9 @@ def lib() -> ctypes.CDLL:
         L.engram_status_string.restype = ctypes.c_char_p
         L.engram_last_error.argtypes = []
         L.engram_last_error.restype = ctypes.c_char_p
+        from .training import declare
+
+        declare(L)
         _lib = L
     return _lib
 
@@ -706,8 +716,11 @@ def engram_gate_residual(x, value, dot, token_mask=None, out=None, stream=None):
     return out
 
 
+from . import training as _training  # noqa: E402  (it uses the helpers above)
+from .training import *  # noqa: E402,F401,F403
+
 __all__ = ["engram_hash", "engram_hash_gather_packed", "engram_gather_dequant", "engram_wkv", "engram_gate_dot", "engram_gate_output",
            "engram_wkv_gate", "engram_wkv_gate_layers", "engram_wkv_gate_layers_noalloc", "NOALLOC_SCRATCH_BYTES",
            "engram_wkv_gate_workspace_bytes", "engram_gather_dequant_fmt", "SCALE_FORMATS", "engram_mx_quant", "engram_gather_mx", "engram_wkv_mx", "engram_wkv_mx_gate", "engram_mx_scale_bytes", "engram_gate_residual", "engram_pack_table",
            "engram_gather_dequant_packed", "EngramError", "lib",
-           "LIB_PATH"]
+           "LIB_PATH"] + _training.__all__

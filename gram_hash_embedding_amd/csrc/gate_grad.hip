@@ -1,0 +1,374 @@
+// engram_gate_output_backward: the gradient of engram_gate_output (the gate pre-activation, the sigmoid gate and the
+// residual) with respect to the stream, the keys, the value and the two gate weights.
+//
+// With h = x[t,c], key = kv[t,c], v the token's value row, w = q * k, d = the pre-activation the forward gave,
+// rh = rsqrt(mean h^2 + eps), rk = rsqrt(mean key^2 + eps), s = rh rk dim^-1/2 and up the gradient of the output:
+//   z = sqrt(max(|d|, 1e-6)) with d's sign,  g = sigmoid(z)  (0 for a masked token)
+//   dd   = (sum_j up v) g (1 - g) / (2 |z|)      (0 where |d| < 1e-6: the clamp is flat; 0 for a masked token)
+//   dx   = up + dd (s w key - d rh^2 h / dim)
+//   dkey = dd (s w h - d rk^2 key / dim)
+//   dv   = sum_c g up
+//   dq   = k sum_t dd s h key,  dk = q sum_t dd s h key
+// The second term of dx and dkey is the derivative of the two norms: sum(h w key) s = d.
+//
+// HBM-bound: per token (3 hc + 1) rows of dim are read and 2 hc + 1 written, every one once.  A workgroup holds a
+// whole token, one 16-byte piece of every row per thread: the rows stay in registers between the sums that need all
+// of a row and the outputs that need the sums, and the sum over tokens of dq and dk stays in registers over all of
+// the workgroup's tokens.  One barrier per token (the sums of the waves, in two LDS buffers taken in turn).  A second
+// launch adds the workgroups' sums in their order, so the same call gives the same bits.
+#include "rows.h"
+
+namespace engram {
+namespace {
+
+constexpr int kMaxWaves = 16;
+constexpr int kMaxDim = 8192;
+constexpr int kCUs = 256;
+constexpr int kWavesPerCU = 20;
+
+struct GateGradArgs {
+    const uint16_t* x;
+    const uint16_t* kv;
+    int64_t ld_kv;
+    const uint16_t* q;
+    const uint16_t* k;
+    const float* dot;
+    const uint16_t* up;
+    const uint8_t* mask;
+    uint16_t* dx;
+    uint16_t* dkv;
+    float* part;  // [gridDim.x][hc * dim] sums over the workgroup's tokens of dd s h key
+    int64_t T;
+    int hc, dim;
+    float eps, inv_dim, rsqrt_dim;
+};
+
+__device__ inline float wave_sum(float v) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+    return v;
+}
+
+// the scalars of one (token, copy)
+struct Coef {
+    float g;   // the gate
+    float a;   // dd s
+    float bh;  // dd d rh^2 / dim
+    float bk;  // dd d rk^2 / dim
+};
+__device__ inline Coef coef_of(const GateGradArgs& p, float hh, float kk, float dg, float d) {
+    const float rh = rsqrtf(hh * p.inv_dim + p.eps), rk = rsqrtf(kk * p.inv_dim + p.eps);
+    const float z = sqrtf(fmaxf(fabsf(d), 1e-6f));
+    Coef c;
+    c.g = 1.0f / (1.0f + expf(-copysignf(z, d)));
+    const float dd = fabsf(d) < 1e-6f ? 0.f : dg * c.g * (1.0f - c.g) / (2.0f * z);
+    c.a = c.bh = c.bk = 0.f;
+    if (dd != 0.f) {  // (a zero gradient stays zero next to the large norms of zero rows; NaN goes on)
+        c.a = dd * (rh * rk * p.rsqrt_dim);
+        c.bh = dd * (d * rh * rh * p.inv_dim);
+        c.bk = dd * (d * rk * rk * p.inv_dim);
+    }
+    return c;
+}
+
+// A masked token: the gate is shut, so the stream's gradient passes and nothing else does.
+__device__ inline void masked_token(const GateGradArgs& p, int64_t t, int piece) {
+    const Piece<Bf16> zero = {u32x4{0, 0, 0, 0}};
+    for (int c = 0; c < p.hc; ++c) {
+        Piece<Bf16> u;
+        u.load_nt(p.up + (t * p.hc + c) * p.dim, piece);
+        u.store_nt(p.dx + (t * p.hc + c) * p.dim, piece);
+    }
+    for (int c = 0; c <= p.hc; ++c) zero.store_nt(p.dkv + (t * (p.hc + 1) + c) * p.dim, piece);
+}
+
+template <int HC, int kMaxThreads>
+__global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) {
+    __shared__ float sums[2][kMaxWaves][3 * HC];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int piece = threadIdx.x;
+    const bool live = piece < p.dim / 8;
+    float acc[HC][8] = {};
+    int turn = 0;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        if (p.mask && p.mask[t] == 0) {  // the whole workgroup
+            if (live) masked_token(p, t, piece);
+            continue;
+        }
+        Piece<Bf16> hr[HC], kr[HC], ur[HC], vr;
+        const uint16_t* row = p.kv + t * p.ld_kv;
+        if (live) {
+            vr.load(row + static_cast<int64_t>(HC) * p.dim, piece);
+#pragma unroll
+            for (int c = 0; c < HC; ++c) {
+                hr[c].load_nt(p.x + (t * HC + c) * p.dim, piece);
+                kr[c].load_nt(row + static_cast<int64_t>(c) * p.dim, piece);
+                ur[c].load_nt(p.up + (t * HC + c) * p.dim, piece);
+            }
+        } else {
+            vr.v = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < HC; ++c) hr[c].v = kr[c].v = ur[c].v = u32x4{0, 0, 0, 0};
+        }
+        float v[8];
+        vr.to(v);
+#pragma unroll
+        for (int c = 0; c < HC; ++c) {
+            float h[8], key[8], u[8], hh = 0.f, kk = 0.f, dg = 0.f;
+            hr[c].to(h);
+            kr[c].to(key);
+            ur[c].to(u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                hh += h[e] * h[e];
+                kk += key[e] * key[e];
+                dg += u[e] * v[e];
+            }
+            hh = wave_sum(hh);
+            kk = wave_sum(kk);
+            dg = wave_sum(dg);
+            if (lane == 0) {
+                sums[turn][wave][3 * c] = hh;
+                sums[turn][wave][3 * c + 1] = kk;
+                sums[turn][wave][3 * c + 2] = dg;
+            }
+        }
+        __syncthreads();
+        float dv[8] = {};
+#pragma unroll
+        for (int c = 0; c < HC; ++c) {
+            float hh = 0.f, kk = 0.f, dg = 0.f;
+            for (int w = 0; w < waves; ++w) {
+                hh += sums[turn][w][3 * c];
+                kk += sums[turn][w][3 * c + 1];
+                dg += sums[turn][w][3 * c + 2];
+            }
+            const Coef k = coef_of(p, hh, kk, dg, p.dot[t * HC + c]);
+            if (!live) continue;
+            Piece<Bf16> qr, kw;
+            qr.load(p.q + static_cast<int64_t>(c) * p.dim, piece);
+            kw.load(p.k + static_cast<int64_t>(c) * p.dim, piece);
+            float h[8], key[8], u[8], qf[8], kf[8], ox[8], ok[8];
+            hr[c].to(h);
+            kr[c].to(key);
+            ur[c].to(u);
+            qr.to(qf);
+            kw.to(kf);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float aw = k.a * (qf[e] * kf[e]);
+                ox[e] = u[e] + (aw * key[e] - k.bh * h[e]);
+                ok[e] = aw * h[e] - k.bk * key[e];
+                dv[e] += k.g * u[e];
+                acc[c][e] += k.a * (h[e] * key[e]);
+            }
+            Piece<Bf16> o;
+            o.from(ox);
+            o.store_nt(p.dx + (t * HC + c) * p.dim, piece);
+            o.from(ok);
+            o.store_nt(p.dkv + (t * (HC + 1) + c) * p.dim, piece);
+        }
+        if (live) {
+            Piece<Bf16> o;
+            o.from(dv);
+            o.store_nt(p.dkv + (t * (HC + 1) + HC) * p.dim, piece);
+        }
+        turn ^= 1;
+    }
+    if (!live) return;
+#pragma unroll
+    for (int c = 0; c < HC; ++c) {
+        Piece<F32> o;
+        o.from(acc[c]);
+        o.store(p.part + (static_cast<int64_t>(blockIdx.x) * HC + c) * p.dim, piece);
+    }
+}
+
+// Any other number of copies: one copy after the other, the sums over tokens in the workgroup's own row of `part`
+// (each thread reads and writes only its piece).
+__global__ __launch_bounds__(1024) void gate_grad_any_kernel(GateGradArgs p) {
+    __shared__ float sums[2][kMaxWaves][3];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int piece = threadIdx.x;
+    const bool live = piece < p.dim / 8;
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.hc * p.dim;
+    Piece<F32> a;
+    const float zero[8] = {};
+    a.from(zero);
+    if (live)
+        for (int c = 0; c < p.hc; ++c) a.store(part + static_cast<int64_t>(c) * p.dim, piece);
+    int turn = 0;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        if (p.mask && p.mask[t] == 0) {
+            if (live) masked_token(p, t, piece);
+            continue;
+        }
+        const uint16_t* row = p.kv + t * p.ld_kv;
+        Piece<Bf16> r = {u32x4{0, 0, 0, 0}};
+        float v[8], dv[8] = {};
+        if (live) r.load(row + static_cast<int64_t>(p.hc) * p.dim, piece);
+        r.to(v);
+        for (int c = 0; c < p.hc; ++c) {
+            float h[8] = {}, key[8] = {}, u[8] = {}, hh = 0.f, kk = 0.f, dg = 0.f;
+            if (live) {
+                r.load(p.x + (t * p.hc + c) * p.dim, piece);
+                r.to(h);
+                r.load(row + static_cast<int64_t>(c) * p.dim, piece);
+                r.to(key);
+                r.load(p.up + (t * p.hc + c) * p.dim, piece);
+                r.to(u);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                hh += h[e] * h[e];
+                kk += key[e] * key[e];
+                dg += u[e] * v[e];
+            }
+            hh = wave_sum(hh);
+            kk = wave_sum(kk);
+            dg = wave_sum(dg);
+            if (lane == 0) {
+                sums[turn][wave][0] = hh;
+                sums[turn][wave][1] = kk;
+                sums[turn][wave][2] = dg;
+            }
+            __syncthreads();
+            hh = kk = dg = 0.f;
+            for (int w = 0; w < waves; ++w) {
+                hh += sums[turn][w][0];
+                kk += sums[turn][w][1];
+                dg += sums[turn][w][2];
+            }
+            turn ^= 1;
+            const Coef k = coef_of(p, hh, kk, dg, p.dot[t * p.hc + c]);
+            if (!live) continue;
+            float qf[8], kf[8], ox[8], ok[8], sum[8];
+            r.load(p.q + static_cast<int64_t>(c) * p.dim, piece);
+            r.to(qf);
+            r.load(p.k + static_cast<int64_t>(c) * p.dim, piece);
+            r.to(kf);
+            a.load(part + static_cast<int64_t>(c) * p.dim, piece);
+            a.to(sum);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float aw = k.a * (qf[e] * kf[e]);
+                ox[e] = u[e] + (aw * key[e] - k.bh * h[e]);
+                ok[e] = aw * h[e] - k.bk * key[e];
+                dv[e] += k.g * u[e];
+                sum[e] += k.a * (h[e] * key[e]);
+            }
+            a.from(sum);
+            a.store(part + static_cast<int64_t>(c) * p.dim, piece);
+            r.from(ox);
+            r.store(p.dx + (t * p.hc + c) * p.dim, piece);
+            r.from(ok);
+            r.store(p.dkv + (t * (p.hc + 1) + c) * p.dim, piece);
+        }
+        if (live) {
+            r.from(dv);
+            r.store(p.dkv + (t * (p.hc + 1) + p.hc) * p.dim, piece);
+        }
+    }
+}
+
+// dq = k * sum, dk = q * sum over the workgroups' sums: 64 columns per workgroup, 16 runs of rows.
+__global__ __launch_bounds__(1024) void gate_grad_sum_kernel(const float* part, int rows, int cols, const uint16_t* q,
+                                                             const uint16_t* k, float* dq, float* dk) {
+    __shared__ float run_sum[16][64];
+    const int col = blockIdx.x * 64 + (threadIdx.x & 63);
+    const int run = threadIdx.x >> 6;
+    const int per = (rows + 15) / 16;
+    const int r0 = min(run * per, rows), r1 = min(r0 + per, rows);
+    float s = 0.f;
+    if (col < cols)
+        for (int r = r0; r < r1; ++r) s += part[static_cast<int64_t>(r) * cols + col];
+    run_sum[run][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (run != 0 || col >= cols) return;
+    s = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s += run_sum[r][threadIdx.x];
+    dq[col] = s * __uint_as_float(static_cast<uint32_t>(k[col]) << 16);
+    dk[col] = s * __uint_as_float(static_cast<uint32_t>(q[col]) << 16);
+}
+
+int threads_of(int dim) { return (dim / 8 + 63) / 64 * 64; }
+
+// workgroups of a launch: as many as kWavesPerCU waves on every CU hold, and no more than there are tokens
+int64_t groups_of(int64_t T, int dim) {
+    const int waves = threads_of(dim) / 64;
+    const int64_t per_cu = kWavesPerCU / waves > 1 ? kWavesPerCU / waves : 1;
+    return T < per_cu * kCUs ? T : per_cu * kCUs;
+}
+
+bool shape_ok(int64_t T, int32_t hc, int32_t dim) {
+    return T >= 0 && hc >= 1 && hc <= 64 && dim >= 8 && dim % 8 == 0 && dim <= kMaxDim;
+}
+
+}  // namespace
+}  // namespace engram
+
+using namespace engram;
+
+extern "C" int64_t engram_gate_output_backward_workspace_bytes(int64_t T, int32_t hc, int32_t dim) {
+    return shape_ok(T, hc, dim) ? groups_of(T, dim) * hc * dim * 4 : -1;
+}
+
+extern "C" int engram_gate_output_backward(const uint16_t* x, const uint16_t* kv, int64_t ld_kv, const uint16_t* q_weight,
+                                           const uint16_t* k_weight, float eps, const float* dot, const uint16_t* dout,
+                                           const uint8_t* token_mask, uint16_t* dx, uint16_t* dkv, float* dq, float* dk,
+                                           void* workspace, int64_t workspace_bytes, int64_t T, int32_t hc, int32_t dim,
+                                           void* stream) {
+    const char* what = "engram_gate_output_backward";
+    if (T < 0) return fail(ENGRAM_EINVAL, "%s: T < 0", what);
+    if (hc < 1 || hc > 64) return fail(ENGRAM_EINVAL, "%s: hc=%d outside [1, 64]", what, hc);
+    if (dim < 8 || dim % 8 != 0 || dim > kMaxDim)
+        return fail(ENGRAM_EINVAL, "%s: dim=%d must be a multiple of 8 in [8, %d]", what, dim, kMaxDim);
+    if (ld_kv < static_cast<int64_t>(hc + 1) * dim || ld_kv % 8 != 0)
+        return fail(ENGRAM_EINVAL, "%s: ld_kv=%lld must be >= (hc+1)*dim and a multiple of 8", what, (long long)ld_kv);
+    if (!q_weight || !k_weight || !dq || !dk) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
+    if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(dq, 4) || !aligned(dk, 4))
+        return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
+    if (T > 0) {
+        if (!x || !kv || !dot || !dout || !dx || !dkv || !workspace) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
+        if (!aligned(x, 16) || !aligned(kv, 16) || !aligned(dout, 16) || !aligned(dx, 16) || !aligned(dkv, 16) ||
+            !aligned(dot, 4) || !aligned(workspace, 16))
+            return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
+    }
+    const int64_t groups = groups_of(T, dim);
+    if (T > 0 && workspace_bytes < groups * hc * dim * 4)
+        return fail(ENGRAM_ERANGE, "%s: workspace of %lld bytes, needs %lld", what, (long long)workspace_bytes,
+                    (long long)(groups * hc * dim * 4));
+    hipStream_t s = as_stream(stream);
+    GateGradArgs p = {};
+    p.x = x;
+    p.kv = kv;
+    p.ld_kv = ld_kv;
+    p.q = q_weight;
+    p.k = k_weight;
+    p.dot = dot;
+    p.up = dout;
+    p.mask = token_mask;
+    p.dx = dx;
+    p.dkv = dkv;
+    p.part = static_cast<float*>(workspace);
+    p.T = T;
+    p.hc = hc;
+    p.dim = dim;
+    p.eps = eps;
+    p.inv_dim = 1.0f / static_cast<float>(dim);
+    p.rsqrt_dim = static_cast<float>(1.0 / __builtin_sqrt(static_cast<double>(dim)));
+    const int threads = threads_of(dim);
+    if (T > 0) {
+        const dim3 grid(static_cast<unsigned>(groups)), block(threads);
+        if (hc == 4 && threads <= 640) hipLaunchKernelGGL((gate_grad_kernel<4, 640>), grid, block, 0, s, p);
+        else if (hc == 4) hipLaunchKernelGGL((gate_grad_kernel<4, 1024>), grid, block, 0, s, p);
+        else if (hc == 2) hipLaunchKernelGGL((gate_grad_kernel<2, 1024>), grid, block, 0, s, p);
+        else if (hc == 1) hipLaunchKernelGGL((gate_grad_kernel<1, 1024>), grid, block, 0, s, p);
+        else hipLaunchKernelGGL(gate_grad_any_kernel, grid, block, 0, s, p);
+    }
+    const int cols = hc * dim;
+    hipLaunchKernelGGL(gate_grad_sum_kernel, dim3((cols + 63) / 64), dim3(1024), 0, s, p.part, static_cast<int>(groups), cols,
+                       q_weight, k_weight, dq, dk);
+    return check_launch(what);
+}

@@ -1,0 +1,342 @@
+// engram_wkv_backward: the gradient of the projection kv = a W^T (engram_wkv).
+//
+//   da [T, K]    = dkv [T, Nout] W [Nout, K]        (over Nout)
+//   dW [Nout, K] = dkv^T [Nout, T] a [T, K]         (over T)
+//
+// Both are products on v_mfma_f32_16x16x32_bf16 with fp32 accumulation.  Neither has both operands contiguous along
+// the reduced axis, which is what the instruction's lanes take: W of da and both operands of dW have it as their rows.
+// Such an operand's slab (64 rows of the reduced axis, 256 columns) goes into LDS as it lies in memory and is turned
+// on the way to the registers by ds_read_b64_tr_b16 (within 16 lanes, lane i supplies the address of four elements,
+// row i / 4, columns 4 (i % 4) .. + 3, and receives column i of the four rows: lane layout measured on gfx950), so
+// nothing is transposed in memory.  Its rows of 512 bytes are swizzled by 32-byte blocks (block b of row k at b XOR
+// (k % 4 + 4 ((k / 8) % 4))): the sixteen rows that one read touches then lie in sixteen different blocks.
+//
+// A workgroup (eight waves) makes a 256 x 256 tile of the output, 128 x 64 per wave, from slabs of 64 of the reduced
+// axis in two stages of LDS filled by direct-to-LDS loads.  Where the tiles are fewer than the CUs the reduced axis is
+// split over workgroups, whose fp32 partial tiles a second launch adds in order.  da and dW of a call are one launch.
+#include "rows.h"
+
+namespace engram {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int BM = 256, BN = 256, BK = 64;
+constexpr int kThreads = 512;
+constexpr int kOpBytes = 256 * 128;  // one operand's slab: 32 KB
+constexpr int kStageBytes = 2 * kOpBytes;
+constexpr int kCUs = 256;
+constexpr int kBufferWord3 = 0x00020000;
+constexpr int kWaitVm0 = 0x0F70;
+constexpr int kWaitLgkm0 = 0xC07F;
+constexpr uint32_t kOutside = 0x80000000u;  // a buffer offset past every resource: the load gives zeros
+
+// One product out [M, N] = sum over r < R of P[m, r] Q[r, n].
+struct Prod {
+    const uint16_t* p;  // da: dkv [M, R]; dW: dkv [R, M]
+    const uint16_t* q;  // [R, N]
+    int64_t M, N, R;
+    void* out;          // [M, N]
+    float* part;        // [splits][M, N] when splits > 1
+    int out_f32, accumulate;
+    int tiles_m, tiles_n, splits, slabs;
+    int64_t units() const { return static_cast<int64_t>(tiles_m) * tiles_n * splits; }
+};
+struct GradArgs {
+    Prod da, dw;
+    int first_dw;           // dW's workgroups come first
+    int64_t first_units;    // workgroups of the product that comes first
+};
+
+__device__ inline uint32_t pack_bf16(float lo, float hi) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+template <bool kRowsP>  // P's slab holds rows of the reduced axis (dW), else rows of the output (da)
+__device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* lds) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave & 1, wn = wave >> 1;
+    const int tn = static_cast<int>(unit % g.tiles_n);
+    const int64_t rest = unit / g.tiles_n;
+    const int tm = static_cast<int>(rest % g.tiles_m);
+    const int split = static_cast<int>(rest / g.tiles_m);
+    const int64_t m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
+    const int s0 = static_cast<int>(static_cast<int64_t>(g.slabs) * split / g.splits);
+    const int s1 = static_cast<int>(static_cast<int64_t>(g.slabs) * (split + 1) / g.splits);
+
+    auto sync = [&]() {
+        __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+
+    // ---- slab loads: every wave 4 KB of each operand, 1 KB per instruction.  A slab of reduced rows: two rows of
+    // 512 bytes per instruction; a slab of output rows: eight rows of 128 bytes, 16-byte pieces swizzled by row / 2.
+    const uint32_t t_row = wave * 8 + (lane >> 5);  // + 2 q
+    auto t_voff = [&](int q, int64_t ld) {
+        const uint32_t k = t_row + 2 * q;
+        const uint32_t f = (k & 3) | (((k >> 3) & 3) << 2);
+        return k * static_cast<uint32_t>(ld * 2) + (((lane & 31) ^ (f << 1)) << 4);
+    };
+    auto t_rsrc = [&](const uint16_t* base, int64_t ld, int64_t c0, int64_t r0) {
+        const int64_t rows = min<int64_t>(BK, g.R - r0);
+        const int64_t bytes = rows > 0 ? rows * ld * 2 - c0 * 2 : 0;
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (rows > 0 ? r0 * ld + c0 : 0)), 0,
+                                                 static_cast<int>(bytes), kBufferWord3);
+    };
+    auto issue = [&](int slab, int stage) {
+        uint8_t* st = lds + stage * kStageBytes;
+        const int64_t r0 = static_cast<int64_t>(slab) * BK;
+        if constexpr (kRowsP) {
+            const auto rp = t_rsrc(g.p, g.M, m0, r0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, st + (wave * 8 + 2 * q) * 512, 16, t_voff(q, g.M), 0, 0, 0);
+        } else {
+            const int64_t rows = min<int64_t>(BM, g.M - m0);
+            const auto rp = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(g.p + m0 * g.R), 0,
+                                                              static_cast<int>(rows * g.R * 2), kBufferWord3);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t row = wave * 32 + 8 * q + (lane >> 3);
+                const uint32_t piece = (lane & 7) ^ ((row >> 1) & 7);
+                const uint32_t voff = r0 + 8 * piece < g.R ? row * static_cast<uint32_t>(g.R * 2) + (piece << 4) : kOutside;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, st + (wave * 32 + 8 * q) * 128, 16, voff,
+                                                         static_cast<int>(r0 * 2), 0, 0);
+            }
+        }
+        const auto rq = t_rsrc(g.q, g.N, n0, r0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, st + kOpBytes + (wave * 8 + 2 * q) * 512, 16, t_voff(q, g.N), 0, 0,
+                                                     0);
+    };
+
+    // ---- fragments of k-step s (32 of the slab's 64): lane l holds row or column l % 16, reduced 8 (l / 16) .. + 7
+    const uint32_t t_lane = (8 * (lane >> 4) + ((lane >> 2) & 3)) * 512 + (lane & 3) * 8 + ((lane >> 2) << 5);
+    const uint32_t r_lane = (lane & 15) * 128 + (((lane >> 4) ^ ((lane >> 1) & 7)) << 4);
+    auto read_t = [&](const uint8_t* op, int s, int block) {
+        typedef __attribute__((address_space(3))) s16x4* lds4;
+        const uint8_t* at = op + s * 32 * 512 + (t_lane ^ (block << 5));
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + 4 * 512));
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        return __builtin_bit_cast(bf16x8, v);
+    };
+    auto read_p = [&](int stage, int s, int i) -> bf16x8 {
+        const uint8_t* op = lds + stage * kStageBytes;
+        if constexpr (kRowsP) return read_t(op, s, wm * 8 + i);
+        else return *reinterpret_cast<const bf16x8*>(op + (wm * 128 + 16 * i) * 128 + (r_lane ^ (s << 6)));
+    };
+    auto read_q = [&](int stage, int s, int j) { return read_t(lds + stage * kStageBytes + kOpBytes, s, wn * 4 + j); };
+
+    f32x4 acc[8][4] = {};
+    if (s0 < s1) issue(s0, 0);
+    for (int kt = s0; kt < s1; ++kt) {
+        const int stage = (kt - s0) & 1;
+        __builtin_amdgcn_s_waitcnt(kWaitVm0);
+        sync();  // the slab has landed, and everyone is done with the other stage
+        if (kt + 1 < s1) issue(kt + 1, stage ^ 1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            bf16x8 fp[8], fq[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) fq[j] = read_q(stage, s, j);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) fp[i] = read_p(stage, s, i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fp[i], acc[i][j], 0, 0, 0);
+        }
+    }
+
+    // ---- lane l holds, per block, output row l % 16 and the columns 4 (l / 16) .. + 3
+    const int64_t mrow = m0 + wm * 128 + (lane & 15), ncol = n0 + wn * 64 + 4 * (lane >> 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t m = mrow + 16 * i;
+        if (m >= g.M) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t n = ncol + 16 * j;
+            if (n >= g.N) continue;
+            const int64_t at = m * g.N + n;
+            f32x4 v = acc[i][j];
+            if (g.splits > 1) {
+                *reinterpret_cast<f32x4*>(g.part + split * g.M * g.N + at) = v;
+            } else if (g.out_f32) {
+                f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + at);
+                if (g.accumulate) v += *o;
+                *o = v;
+            } else {
+                u32x2* o = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(g.out) + at);
+                if (g.accumulate) {
+                    const u32x2 w = *o;
+                    v += f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u),
+                               __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u)};
+                }
+                *o = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+            }
+        }
+    }
+}
+
+__global__ __launch_bounds__(kThreads, 1) void wkv_grad_kernel(GradArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStageBytes];
+    const int64_t b = blockIdx.x;
+    const bool first = b < a.first_units;
+    const int64_t unit = first ? b : b - a.first_units;
+    if (first == (a.first_dw != 0)) product<true>(a.dw, unit, lds);
+    else product<false>(a.da, unit, lds);
+}
+
+// The partial tiles of a split reduction, added in order: eight outputs per thread.
+__global__ __launch_bounds__(256) void wkv_grad_join_kernel(const float* part, int splits, int64_t n8, void* out,
+                                                            int out_f32, int accumulate) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n8) return;
+    float s[8] = {};
+    for (int k = 0; k < splits; ++k) {
+        Piece<F32> p;
+        float f[8];
+        p.load_nt(part, k * n8 + i);
+        p.to(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += f[e];
+    }
+    if (out_f32) {
+        Piece<F32> o;
+        if (accumulate) {
+            float f[8];
+            o.load(out, i);
+            o.to(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += f[e];
+        }
+        o.from(s);
+        o.store(out, i);
+    } else {
+        Piece<Bf16> o;
+        if (accumulate) {
+            float f[8];
+            o.load(out, i);
+            o.to(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += f[e];
+        }
+        o.from(s);
+        o.store(out, i);
+    }
+}
+
+int splits_of(int64_t tiles, int64_t slabs) {
+    if (tiles >= kCUs) return 1;
+    int64_t s = kCUs / tiles;
+    if (s > slabs / 4) s = slabs / 4;
+    return static_cast<int>(s < 1 ? 1 : s);
+}
+
+Prod prod_of(int64_t M, int64_t N, int64_t R) {
+    Prod p = {};
+    p.M = M;
+    p.N = N;
+    p.R = R;
+    p.tiles_m = static_cast<int>((M + BM - 1) / BM);
+    p.tiles_n = static_cast<int>((N + BN - 1) / BN);
+    p.slabs = static_cast<int>((R + BK - 1) / BK);
+    p.splits = splits_of(static_cast<int64_t>(p.tiles_m) * p.tiles_n, p.slabs);
+    return p;
+}
+
+int64_t part_bytes(const Prod& p) { return p.splits > 1 ? p.splits * p.M * p.N * 4 : 0; }
+
+bool shape_ok(int64_t T, int32_t K, int32_t Nout) {
+    return T >= 0 && T <= (1ll << 30) && K >= 8 && K % 8 == 0 && K <= (1 << 20) && Nout >= 8 && Nout % 8 == 0 &&
+           Nout <= (1 << 21);
+}
+
+}  // namespace
+}  // namespace engram
+
+using namespace engram;
+
+extern "C" int64_t engram_wkv_backward_workspace_bytes(int64_t T, int32_t K, int32_t Nout) {
+    if (!shape_ok(T, K, Nout)) return -1;
+    if (T == 0) return 0;
+    return part_bytes(prod_of(T, K, Nout)) + part_bytes(prod_of(Nout, K, T));
+}
+
+extern "C" int engram_wkv_backward(const uint16_t* dkv, const uint16_t* a, const uint16_t* w, uint16_t* da, void* dw,
+                                   int32_t dw_dtype, int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                                   int64_t T, int32_t K, int32_t Nout, void* stream) {
+    const char* what = "engram_wkv_backward";
+    if (T < 0 || T > (1ll << 30)) return fail(ENGRAM_EINVAL, "%s: T outside [0, 2^30]", what);
+    if (K < 8 || K % 8 != 0 || K > (1 << 20))
+        return fail(ENGRAM_EINVAL, "%s: K=%d must be a multiple of 8 in [8, 2^20]", what, K);
+    if (Nout < 8 || Nout % 8 != 0 || Nout > (1 << 21))
+        return fail(ENGRAM_EINVAL, "%s: Nout=%d must be a multiple of 8 in [8, 2^21]", what, Nout);
+    if (!known_dtype(dw_dtype)) return fail(ENGRAM_EINVAL, "%s: unknown dtype", what);
+    if (!da && !dw) return fail(ENGRAM_EINVAL, "%s: neither da nor dw is asked for", what);
+    if (T > 0) {
+        if (!dkv || (dw && !a) || (da && !w)) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
+        if (!aligned(dkv, 16) || (dw && !aligned(a, 16)) || (da && !aligned(w, 16)) || !aligned(da, 16))
+            return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
+    }
+    if (!aligned(dw, 16)) return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
+    hipStream_t s = as_stream(stream);
+    if (T == 0) {
+        if (!dw || accumulate) return ENGRAM_OK;
+        return launch_zero(dw, static_cast<int64_t>(Nout) * K * (dw_dtype == ENGRAM_F32 ? 4 : 2), s, what);
+    }
+    GradArgs g = {};
+    int64_t need = 0;
+    float* part = static_cast<float*>(workspace);
+    if (da) {
+        g.da = prod_of(T, K, Nout);
+        g.da.p = dkv;
+        g.da.q = w;
+        g.da.out = da;
+        g.da.part = part;
+        need += part_bytes(g.da);
+    }
+    if (dw) {
+        g.dw = prod_of(Nout, K, T);
+        g.dw.p = dkv;
+        g.dw.q = a;
+        g.dw.out = dw;
+        g.dw.out_f32 = dw_dtype == ENGRAM_F32;
+        g.dw.accumulate = accumulate != 0;
+        g.dw.part = part + need / 4;
+        need += part_bytes(g.dw);
+    }
+    if (need > 0) {
+        if (!workspace || !aligned(workspace, 16)) return fail(ENGRAM_EINVAL, "%s: workspace is null or misaligned", what);
+        if (workspace_bytes < need)
+            return fail(ENGRAM_ERANGE, "%s: workspace of %lld bytes, needs %lld", what, (long long)workspace_bytes,
+                        (long long)need);
+    }
+    const int64_t u_da = da ? g.da.units() : 0, u_dw = dw ? g.dw.units() : 0;
+    if (u_da + u_dw > 0x7FFFFFFF) return fail(ENGRAM_EINVAL, "%s: too many tiles", what);
+    // the longer reductions first: the shorter ones fill in behind them
+    g.first_dw = !da || (dw && g.dw.slabs / g.dw.splits > g.da.slabs / g.da.splits);
+    g.first_units = g.first_dw ? u_dw : u_da;
+    hipLaunchKernelGGL(wkv_grad_kernel, dim3(static_cast<unsigned>(u_da + u_dw)), dim3(kThreads), 0, s, g);
+    for (const Prod* p : {&g.da, &g.dw}) {
+        if (!p->out || p->splits <= 1) continue;
+        const int64_t n8 = p->M * p->N / 8;
+        hipLaunchKernelGGL(wkv_grad_join_kernel, dim3(static_cast<unsigned>((n8 + 255) / 256)), dim3(256), 0, s, p->part,
+                           p->splits, n8, p->out, p->out_f32, p->accumulate);
+    }
+    return check_launch(what);
+}

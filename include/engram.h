@@ -41,6 +41,17 @@
  *   engram_wkv_mx          -- the projection on MX fp8 operands
  *   engram_wkv_mx_gate     -- engram_wkv_mx fused with the gate pre-activation
  *
+ * and the gradients that train the module and its embeddings:
+ *
+ *   engram_embed           -- rows of a trainable (bf16 or float32) table by id, scaled
+ *   engram_embed_grad, engram_embed_grad_rows
+ *                          -- its gradient by sorted ids: a row per table row, or the
+ *                             distinct rows only (hashed tables)
+ *   engram_gate_output_backward -- the gradient of engram_gate_output
+ *   engram_wkv_backward    -- the gradient of engram_wkv
+ *   engram_grad_norm, engram_clip_grads
+ *                          -- the 2-norm of many gradients together, and clipping by it
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - Every array argument is a DEVICE pointer (memory the caller allocated on
@@ -531,6 +542,163 @@ int engram_wkv_gate_layers_noalloc(int32_t layers, const uint16_t* const* a, con
                                    const uint16_t* const* k_weight, float eps, uint16_t* const* value,
                                    int64_t ld_value, float* const* dot, int64_t T, int32_t K, int32_t hc,
                                    int32_t dim, void* stream);
+
+/*
+ * The gradients that train the module (stack-hashes page: Engram.forward and
+ * ParallelEngramEmbedding.forward, whose weights are trained; the pages show the
+ * forward only).  Element types of their arguments:
+ */
+#define ENGRAM_BF16 0 /* bf16 bits, 2 bytes */
+#define ENGRAM_F32 1  /* float32 */
+
+/*
+ * engram_embed -- rows of a trainable table by id, times a scalar (a token
+ * embedding, or the master copy of a hashed table):
+ *   out[i,:] = round(fp32(table[ids[i] - row_start, :]) * scale), or zeros where
+ *   ids[i] lies outside [row_start, row_start + R).
+ *
+ * ids    [n] int64 (id_bytes 8) or int32 (id_bytes 4), aligned to its size
+ * table  [R, D] of table_dtype; 16-byte aligned
+ * out    [n, D] of out_dtype, out; 16-byte aligned
+ * Limits: n >= 0; R >= 1; D a multiple of 8 in [8, 65536].
+ */
+int engram_embed(const void* ids, int32_t id_bytes, int64_t n, const void* table, int32_t table_dtype, int64_t R,
+                 int64_t row_start, int32_t D, float scale, void* out, int32_t out_dtype, void* stream);
+
+/*
+ * engram_embed_grad -- the gradient of such a lookup, a row per table row:
+ *   grad[r,:] = round(scale * sum over the positions i with id_i - row_start = r of
+ *               fp32(up[i,:])  [+ grad[r,:] if accumulate])
+ * where position i = t*C + c has the id ids[t*id_token_stride + c], and ids outside
+ * [row_start, row_start + R) take no part.  Sums in fp32, in an order set by the
+ * ids alone: the same call gives the same bits.  Without `accumulate` every row
+ * is written (zeros where no id points); with it, rows no id points at are not
+ * touched.
+ *
+ * ids        [T, id_token_stride] int64 or int32 (engram_hash's output for one layer, or
+ *            token ids with C = id_token_stride = 1); aligned to its size
+ * up         [T*C, D] of up_dtype, the gradient of the looked-up rows; 16-byte aligned
+ * grad       [R, D] of grad_dtype, out (in/out with accumulate); 16-byte aligned
+ * workspace  engram_embed_grad_workspace_bytes(T*C, D, R) bytes, 16-byte aligned,
+ *            caller-owned scratch (no initialisation needed)
+ * Limits: T >= 0, 1 <= C <= 1024, T*C <= 2^30; 1 <= R < 2^31; D a multiple of 8 in
+ * [8, 65536].  Too small a workspace -> ENGRAM_ERANGE.
+ */
+int engram_embed_grad(const void* ids, int32_t id_bytes, int64_t T, int64_t id_token_stride, int32_t C, const void* up,
+                      int32_t up_dtype, int64_t R, int64_t row_start, int32_t D, float scale, void* grad,
+                      int32_t grad_dtype, int32_t accumulate, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace engram_embed_grad and engram_embed_grad_rows need for n = T*C ids, or -1 outside their limits. */
+int64_t engram_embed_grad_workspace_bytes(int64_t n, int32_t D, int64_t R);
+
+/*
+ * engram_embed_grad_rows -- the same gradient as its distinct rows (a hashed table
+ * has far more rows than a step touches): with u_0 < u_1 < ... the `count` distinct
+ * ids inside [row_start, row_start + R),
+ *   unique[k] = u_k and rows[k,:] = the gradient row of u_k, for k < count;
+ *   unique[k] = -1 and rows[k,:] = 0 for count <= k < T*C.
+ *
+ * unique  int64 [T*C], out; 8-byte aligned
+ * rows    [T*C, D] of rows_dtype, out; 16-byte aligned
+ * count   int32 [1], out
+ * Other arguments and limits: as engram_embed_grad.
+ */
+int engram_embed_grad_rows(const void* ids, int32_t id_bytes, int64_t T, int64_t id_token_stride, int32_t C,
+                           const void* up, int32_t up_dtype, int64_t R, int64_t row_start, int32_t D, float scale,
+                           int64_t* unique, void* rows, int32_t rows_dtype, int32_t* count, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/*
+ * engram_gate_output_backward -- the gradient of engram_gate_output (stack-hashes
+ * page: the gate, the token mask and the returned sum of Engram.forward).  With
+ * h = x[t,c,:], key and v the key and value columns of kv, w = q_weight * k_weight,
+ * d = dot[t,c] (as the forward wrote it), up = dout[t,c,:], rh = rsqrt(mean h^2 + eps),
+ * rk = rsqrt(mean key^2 + eps), s = rh rk dim^-1/2, z = copysign(sqrt(max(|d|, 1e-6)), d),
+ * g = sigmoid(z), dd = (sum up v) g (1 - g) / (2 |z|), 0 where |d| < 1e-6:
+ *   dx[t,c,:]  = bf16(up + dd (s w key - d rh^2 h / dim))
+ *   dkv[t, key columns of c] = bf16(dd (s w h - d rk^2 key / dim))
+ *   dkv[t, value columns]    = bf16(sum_c g up)
+ *   dq[c,:] = k_weight sum_t dd s h key,   dk[c,:] = q_weight sum_t dd s h key
+ * A masked token passes dout to dx bit for bit and contributes nothing else (its dkv
+ * row is zero), whatever its x and kv hold.  Sums in fp32, in a fixed order.
+ *
+ * x, dout    uint16 [T, hc, dim] bf16 bits; 16-byte aligned
+ * kv         uint16, row stride ld_kv >= (hc+1)*dim, ld_kv % 8 == 0 (engram_wkv's
+ *            output); 16-byte aligned
+ * q_weight, k_weight  uint16 [hc, dim] bf16 bits; 16-byte aligned
+ * dot        float32 [T, hc]: engram_gate_output's or engram_wkv_gate's
+ * token_mask uint8 [T] (nonzero = takes part) or NULL = every token
+ * dx         uint16 [T, hc, dim] bf16 bits, out; 16-byte aligned; may be dout itself
+ * dkv        uint16 [T, (hc+1)*dim] bf16 bits, out; 16-byte aligned; no overlap with an input
+ * dq, dk     float32 [hc, dim], out
+ * workspace  engram_gate_output_backward_workspace_bytes(T, hc, dim) bytes, 16-byte aligned,
+ *            caller-owned scratch (no initialisation needed)
+ * Limits: T >= 0; 1 <= hc <= 64; 8 <= dim <= 8192 and dim % 8 == 0 (hc 1, 2 and 4
+ * keep a token's sums in registers; other counts go through the workspace).
+ * Too small a workspace -> ENGRAM_ERANGE.
+ */
+int engram_gate_output_backward(const uint16_t* x, const uint16_t* kv, int64_t ld_kv, const uint16_t* q_weight,
+                                const uint16_t* k_weight, float eps, const float* dot, const uint16_t* dout,
+                                const uint8_t* token_mask, uint16_t* dx, uint16_t* dkv, float* dq, float* dk,
+                                void* workspace, int64_t workspace_bytes, int64_t T, int32_t hc, int32_t dim,
+                                void* stream);
+
+/* Bytes of workspace engram_gate_output_backward needs, or -1 outside its limits. */
+int64_t engram_gate_output_backward_workspace_bytes(int64_t T, int32_t hc, int32_t dim);
+
+/*
+ * engram_wkv_backward -- the gradient of engram_wkv, kv = a * w^T:
+ *   da = bf16(dkv * w);   dw = round(dkv^T * a [+ dw if accumulate]);  fp32 accumulation.
+ *
+ * dkv   uint16 [T, Nout] bf16 bits; 16-byte aligned
+ * a     uint16 [T, K] bf16 bits (unused if dw is NULL); 16-byte aligned
+ * w     uint16 [Nout, K] bf16 bits (unused if da is NULL); 16-byte aligned
+ * da    uint16 [T, K] bf16 bits, out, or NULL = not computed; 16-byte aligned
+ * dw    [Nout, K] of dw_dtype, out (in/out with accumulate), or NULL = not computed; 16-byte aligned
+ * workspace  engram_wkv_backward_workspace_bytes(T, K, Nout) bytes, 16-byte aligned, caller-owned
+ *       scratch (no initialisation needed; NULL where it needs none)
+ * Limits: 0 <= T <= 2^30; K a multiple of 8 in [8, 2^20]; Nout a multiple of 8 in
+ * [8, 2^21].  Too small a workspace -> ENGRAM_ERANGE.
+ */
+int engram_wkv_backward(const uint16_t* dkv, const uint16_t* a, const uint16_t* w, uint16_t* da, void* dw,
+                        int32_t dw_dtype, int32_t accumulate, void* workspace, int64_t workspace_bytes, int64_t T,
+                        int32_t K, int32_t Nout, void* stream);
+
+/* Bytes of workspace engram_wkv_backward needs, or -1 outside its limits. */
+int64_t engram_wkv_backward_workspace_bytes(int64_t T, int32_t K, int32_t Nout);
+
+/*
+ * engram_grad_norm -- the 2-norm of `tensors` gradients taken as one vector:
+ *   norm = sqrt(sum of the squares of all their elements), summed in fp32 and fp64 in a
+ *   fixed order; 0 for no elements.
+ *
+ * grads  host array of device pointers to contiguous elements (aligned to their
+ *        size; 16-byte aligned ones are read 16 bytes at a time)
+ * n      host array of element counts, each in [0, 2^40]
+ * dtype  host array of element types
+ * norm   float32 [1], out (device)
+ * workspace  engram_grad_norm_workspace_bytes(tensors, n, dtype) bytes, 8-byte aligned
+ * The host arrays are read during the call only.
+ */
+int engram_grad_norm(int32_t tensors, const void* const* grads, const int64_t* n, const int32_t* dtype, float* norm,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace engram_grad_norm needs, or -1 for bad arguments. */
+int64_t engram_grad_norm_workspace_bytes(int32_t tensors, const int64_t* n, const int32_t* dtype);
+
+/*
+ * engram_clip_grads -- out = round(grad * min(1, max_norm / (norm + 1e-6))) for every
+ * tensor, `norm` being a device float32 (engram_grad_norm's, or one combined over
+ * ranks).  A NaN norm gives NaN.
+ *
+ * grads, n, dtype  as engram_grad_norm
+ * out    host array of device pointers, each of its gradient's type and size, aligned to
+ *        its element; out[i] may be grads[i] (in place: nothing is written where the
+ *        factor is 1), no other overlap
+ * max_norm >= 0
+ */
+int engram_clip_grads(int32_t tensors, const void* const* grads, void* const* out, const int64_t* n,
+                      const int32_t* dtype, const float* norm, float max_norm, void* stream);
 
 #ifdef __cplusplus
 }

@@ -10,14 +10,13 @@
 //
 // Sort: least significant digit first, 8 bytes (row, position) per element, digits of at most kMaxDigitBits bits over
 // the bits that rows actually have, so the fewest passes (17 bits of a token vocabulary: two, 29 bits of a 384 M row
-// table: three).  A pass is one launch: every workgroup ranks a tile of kSortTile elements (per wave by ballots over
-// the digit's bits, so stable), adds the tiles before it from the table of per-tile digit counts, and scatters.  The
-// counts of the next pass are gathered by the scatter itself with integer atomics (their order does not matter).
+// table: three).  A pass counts the digits per tile, then every workgroup ranks a tile of kSortTile elements (per wave by ballots over
+// the digit's bits, so stable), adds the tiles before it from the table of per-tile digit counts, and scatters.
 //
-// Fold: the sorted positions are cut into chunks of kChunk; a group of lanes walks a chunk with the row sum in
-// registers and writes a table row where its segment ends.  A segment that crosses chunks leaves fp32 partial sums
-// (one leaving a chunk, one entering) which a last launch adds in chunk order, so that one hot row costs no more than
-// many cold ones.
+// Fold: the sorted positions are cut into chunks of kChunk; a group of lanes adds a segment's positions within a chunk
+// in registers and writes the table row if the segment ends there.  A segment that crosses chunks leaves fp32 partial
+// sums (one leaving a chunk, one entering) which a last launch adds in a fixed order, so that one hot row costs no more
+// than many cold ones.
 #include "rows.h"
 
 namespace engram {
@@ -28,13 +27,15 @@ constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortItems = 8;
 constexpr int kSortTile = kSortThreads * kSortItems;
-constexpr int kMaxDigitBits = 10;
+constexpr int kMaxDigitBits = 11;
 constexpr int kMaxDigits = 1 << kMaxDigitBits;
 // up to this many tiles every scattering workgroup adds the digit counts of the tiles before it by itself; past it a
 // launch of its own turns the counts into prefixes
 constexpr int kDirectTiles = 64;
 constexpr int kChunk = 16;   // sorted positions per chunk of the fold
 constexpr int64_t kMaxIds = 1ll << 30;
+constexpr int64_t kMaxGridX = 1ll << 23;  // workgroups along x: x * threads stays below 2^32
+constexpr int kSmall = 1024;              // up to this many ids one launch sorts and folds
 
 // ---------------------------------------------------------------------------------------------------------------------
 // lookup
@@ -109,6 +110,25 @@ int launch_embed(EmbedArgs& a, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------------------------------------------------
+// zeros
+// ---------------------------------------------------------------------------------------------------------------------
+// A run of 16-byte pieces.  One store per thread, the workgroups in memory order: 2.65 GB in 385 us (6.9 TB/s), against
+// 441 us with four stores per thread, 489 us with a grid that walks the memory and 470-480 us with a row per wave (non-
+// temporal stores are slower in every form).
+struct Zeros {
+    u32x4* p;
+    int64_t n16;
+    __device__ inline void run(int64_t block) const {
+        const int64_t i = block * blockDim.x + threadIdx.x;
+        if (i < n16) p[i] = u32x4{0, 0, 0, 0};
+    }
+};
+
+__global__ __launch_bounds__(kThreads) void zero_kernel(Zeros z) {
+    z.run(static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x);
+}
+
+// ---------------------------------------------------------------------------------------------------------------------
 // sort
 // ---------------------------------------------------------------------------------------------------------------------
 struct Pair {
@@ -126,9 +146,8 @@ struct SortArgs {
     uint32_t n;
     const Pair* in;    // later passes
     Pair* out;
-    uint32_t* hist;       // [tiles][digits] this pass's digit counts per tile (or their prefixes over the tiles)
-    uint32_t* totals;     // [digits], with prefixes
-    uint32_t* hist_next;  // [tiles][digits] of the next pass, zeroed, or null
+    uint32_t* hist;    // [tiles][digits] this pass's digit counts per tile (or their prefixes over the tiles)
+    uint32_t* totals;  // [digits], with prefixes
     int shift, bits;      // this pass's digit
     int tiles;
 };
@@ -143,18 +162,24 @@ __device__ inline uint32_t load_key(const SortArgs& a, uint32_t i) {
     return r >= 0 && r < static_cast<int64_t>(a.R) ? static_cast<uint32_t>(r) : a.R;
 }
 
-// The first pass's digit counts per tile, and the later passes' count tables zeroed.
-__global__ __launch_bounds__(kSortThreads) void hist_kernel(SortArgs a, uint32_t* zero, uint32_t zero_n) {
+// A pass's digit counts per tile; the first pass's workgroups behind the tiles write the dense form's zeros (skipping the
+// rows that will be written costs more than it saves: a byte per row looked up before each store took 520 us for the
+// 385 us of stores).
+template <bool kFirst>
+__global__ __launch_bounds__(kSortThreads) void hist_kernel(SortArgs a, Zeros z) {
     __shared__ uint32_t h[kMaxDigits];
+    if (kFirst && static_cast<int>(blockIdx.x) >= a.tiles) {
+        z.run(blockIdx.x - a.tiles);
+        return;
+    }
     const int digits = 1 << a.bits;
     for (int d = threadIdx.x; d < digits; d += kSortThreads) h[d] = 0;
-    for (uint32_t z = blockIdx.x * kSortThreads + threadIdx.x; z < zero_n; z += gridDim.x * kSortThreads) zero[z] = 0;
     __syncthreads();
     const uint32_t base = blockIdx.x * kSortTile + threadIdx.x;
 #pragma unroll
     for (int u = 0; u < kSortItems; ++u) {
         const uint32_t i = base + u * kSortThreads;
-        if (i < a.n) atomicAdd(&h[load_key(a, i) & (digits - 1)], 1u);
+        if (i < a.n) atomicAdd(&h[((kFirst ? load_key(a, i) : a.in[i].key) >> a.shift) & (digits - 1)], 1u);
     }
     __syncthreads();
     for (int d = threadIdx.x; d < digits; d += kSortThreads) a.hist[blockIdx.x * digits + d] = h[d];
@@ -169,8 +194,10 @@ __global__ __launch_bounds__(1024) void prefix_kernel(SortArgs a) {
     const int per = (a.tiles + 15) / 16;
     const int t0 = min(run * per, a.tiles), t1 = min(t0 + per, a.tiles);
     uint32_t sum = 0;
-    if (d < digits)
+    if (d < digits) {
+#pragma unroll 8
         for (int t = t0; t < t1; ++t) sum += a.hist[t * digits + d];
+    }
     part[run][threadIdx.x & 63] = sum;
     __syncthreads();
     uint32_t base = 0, total = 0;
@@ -181,22 +208,44 @@ __global__ __launch_bounds__(1024) void prefix_kernel(SortArgs a) {
         total += v;
     }
     if (d >= digits) return;
-    for (int t = t0; t < t1; ++t) {
-        const uint32_t v = a.hist[t * digits + d];
-        a.hist[t * digits + d] = base;
-        base += v;
+    for (int t = t0; t < t1; t += 8) {
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = t + j < t1 ? a.hist[(t + j) * digits + d] : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (t + j < t1) a.hist[(t + j) * digits + d] = base;
+            base += v[j];
+        }
     }
     if (run == 0) a.totals[d] = total;
 }
 
-template <bool kFirst>
+// kPer consecutive counts, as one load
+template <int kPer>
+__device__ inline void load_counts(const uint32_t* p, uint32_t (&v)[kPer]) {
+    typedef uint32_t vec __attribute__((ext_vector_type(kPer)));
+    if constexpr (kPer == 1) {
+        v[0] = *p;
+    } else {
+        const vec x = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[j] = x[j];
+    }
+}
+
+// kPer: digits per thread (digits = kPer * kSortThreads, or fewer than kSortThreads with kPer 1)
+template <bool kFirst, int kPer>
 __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
-    __shared__ uint32_t cnt[kSortWaves][kMaxDigits];
-    __shared__ uint32_t wave_sum[kSortWaves];
+    constexpr int kDigits = kPer * kSortThreads;
+    __shared__ uint16_t cnt[kSortWaves][kDigits];
+    __shared__ uint32_t move[kDigits];  // a digit's elements: their place in the output less that in the tile
+    __shared__ Pair tile[kSortTile];    // the tile in order of the digit
+    __shared__ uint32_t wave_sum[kSortWaves], wave_local[kSortWaves];
     const int digits = 1 << a.bits;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t mask_bits = static_cast<uint32_t>(digits - 1);
-    for (int d = threadIdx.x; d < digits * kSortWaves; d += kSortThreads) cnt[d / digits][d % digits] = 0;
+    for (int d = threadIdx.x; d < kSortWaves * kDigits / 2; d += kSortThreads) reinterpret_cast<uint32_t*>(cnt)[d] = 0;
 
     // the wave's kSortItems * 64 consecutive elements
     Pair e[kSortItems];
@@ -211,8 +260,32 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
             else e[u] = a.in[i];
         }
     }
+    // each thread owns the digits [own, own + kPer): how many elements have it, and how many of them lie in the tiles
+    // before this one
+    const int own = threadIdx.x * kPer;
+    uint32_t total[kPer] = {}, prior[kPer] = {};
+    if (own < digits) {
+        if (a.totals) {
+            load_counts(a.totals + own, total);
+            load_counts(a.hist + blockIdx.x * digits + own, prior);
+        } else {
+            constexpr int kBatch = 16;
+            for (int t = 0; t < a.tiles; t += kBatch) {
+                uint32_t v[kBatch][kPer];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) load_counts(a.hist + min(t + i, a.tiles - 1) * digits + own, v[i]);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) {
+                        total[j] += t + i < a.tiles ? v[i][j] : 0;
+                        prior[j] += t + i < static_cast<int>(blockIdx.x) ? v[i][j] : 0;
+                    }
+            }
+        }
+    }
     __syncthreads();
-    volatile uint32_t* mine = cnt[wave];  // this wave's counters: its LDS accesses stay in program order
+    volatile uint16_t* mine = cnt[wave];  // this wave's counters: its LDS accesses stay in program order
     const uint64_t below = (1ull << lane) - 1;
 #pragma unroll
     for (int u = 0; u < kSortItems; ++u) {
@@ -227,74 +300,76 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
         const uint32_t before = __popcll(same & below);
         const uint32_t have = live ? mine[d] : 0;
         rank[u] = have + before;
-        if (live && before == 0) mine[d] = have + __popcll(same);
+        if (live && before == 0) mine[d] = static_cast<uint16_t>(have + __popcll(same));
     }
     __syncthreads();
 
-    // each thread owns the digits [own, own + per): the elements with a smaller digit, the tiles before this one and
-    // the waves before each wave
-    constexpr int kPer = kMaxDigits / kSortThreads;
-    const int per = digits >= kSortThreads ? digits / kSortThreads : 1;
-    const int own = threadIdx.x * per;
-    uint32_t total[kPer] = {}, prior[kPer] = {};
-    if (own < digits) {
-        if (a.totals) {
+    // exclusive sums over the digits, of all elements and of the tile's
+    uint32_t sum = 0, local = 0, have[kPer];
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                if (j < per) {
-                    total[j] = a.totals[own + j];
-                    prior[j] = a.hist[blockIdx.x * digits + own + j];
-                }
-        } else {
-            for (int t = 0; t < a.tiles; ++t) {
+    for (int j = 0; j < kPer; ++j) {
+        uint32_t at = 0;
 #pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    if (j < per) {
-                        const uint32_t v = a.hist[t * digits + own + j];
-                        total[j] += v;
-                        prior[j] += t < static_cast<int>(blockIdx.x) ? v : 0;
-                    }
-            }
+        for (int w = 0; w < kSortWaves; ++w) {  // each wave's elements of the digit begin after those of the waves before
+            const uint32_t c = cnt[w][own + j];
+            cnt[w][own + j] = static_cast<uint16_t>(at);
+            at += c;
         }
+        have[j] = at;
+        local += at;
+        sum += total[j];
     }
-    uint32_t sum = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) sum += total[j];
-    uint32_t scan = sum;  // inclusive over the wave's threads
+    uint32_t scan = sum, scan_local = local;  // inclusive over the wave's threads
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-        const uint32_t o = __shfl_up(scan, off, 64);
+        const uint32_t o = __shfl_up(scan, off, 64), l = __shfl_up(scan_local, off, 64);
         scan += lane >= off ? o : 0;
+        scan_local += lane >= off ? l : 0;
     }
-    if (lane == 63) wave_sum[wave] = scan;
-    __syncthreads();
-    uint32_t base = scan - sum;
-    for (int w = 0; w < wave; ++w) base += wave_sum[w];
-    if (own < digits) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            if (j < per) {
-                uint32_t at = base + prior[j];
-#pragma unroll
-                for (int w = 0; w < kSortWaves; ++w) {
-                    const uint32_t c = cnt[w][own + j];
-                    cnt[w][own + j] = at;
-                    at += c;
-                }
-                base += total[j];
-            }
+    if (lane == 63) {
+        wave_sum[wave] = scan;
+        wave_local[wave] = scan_local;
     }
     __syncthreads();
+    uint32_t base = scan - sum, base_local = scan_local - local;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+        base += w < wave ? wave_sum[w] : 0;
+        base_local += w < wave ? wave_local[w] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        move[own + j] = base + prior[j] - base_local;
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) cnt[w][own + j] = static_cast<uint16_t>(cnt[w][own + j] + base_local);
+        base += total[j];
+        base_local += have[j];
+    }
+    __syncthreads();
+    // through LDS in the digit's order, so that the stores of neighbouring lanes fall into the same lines
 #pragma unroll
     for (int u = 0; u < kSortItems; ++u) {
         if (first + u * 64 >= a.n) continue;
-        const uint32_t to = cnt[wave][(e[u].key >> a.shift) & mask_bits] + rank[u];
-        a.out[to] = e[u];
-        if (a.hist_next) {
-            const uint32_t d2 = (e[u].key >> (a.shift + a.bits)) & mask_bits;
-            atomicAdd(&a.hist_next[to / kSortTile * digits + d2], 1u);
-        }
+        tile[cnt[wave][(e[u].key >> a.shift) & mask_bits] + rank[u]] = e[u];
     }
+    __syncthreads();
+    const uint32_t here = min(a.n - blockIdx.x * kSortTile, static_cast<uint32_t>(kSortTile));
+#pragma unroll
+    for (int u = 0; u < kSortItems; ++u) {
+        const uint32_t i = threadIdx.x + u * kSortThreads;
+        if (i >= here) continue;
+        const Pair x = tile[i];
+        a.out[move[(x.key >> a.shift) & mask_bits] + i] = x;
+    }
+}
+
+template <bool kFirst>
+void launch_scatter(const SortArgs& a, hipStream_t stream) {
+    const dim3 grid(a.tiles), block(kSortThreads);
+    const int digits = 1 << a.bits;
+    if (digits > 2 * kSortThreads) hipLaunchKernelGGL((scatter_kernel<kFirst, 4>), grid, block, 0, stream, a);
+    else if (digits > kSortThreads) hipLaunchKernelGGL((scatter_kernel<kFirst, 2>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((scatter_kernel<kFirst, 1>), grid, block, 0, stream, a);
 }
 
 // ---------------------------------------------------------------------------------------------------------------------
@@ -317,6 +392,7 @@ struct FoldArgs {
     uint32_t* chunk_base;  // [chunks] of those, the ones before the chunk
     int tiles;
     uint32_t chunks;
+    uint32_t* leave_to;  // rows form: [chunks] the distinct row that leaves the chunk
     float* leave;       // [chunks][D] sum of a segment that begins in the chunk and goes on after it
     float* enter;       // [chunks][D] sum of the chunk's share of a segment that began before it
 };
@@ -347,13 +423,13 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(FoldArgs a) {
     }
     if (lane == 63) wsum[wave] = scan;
     __syncthreads();
-    uint32_t base = 0, all = 0;
+    uint32_t base = scan - c, all = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 64; ++w) {
         base += w < wave ? wsum[w] : 0;
         all += wsum[w];
     }
-    if (chunk < a.chunks) a.chunk_base[chunk] = base + scan - c;
+    if (chunk < a.chunks) a.chunk_base[chunk] = base;
     if (threadIdx.x == 0) a.heads[blockIdx.x] = all;
 }
 
@@ -385,45 +461,40 @@ __device__ inline void put_row(const FoldArgs& a, uint32_t key, uint32_t u, int 
     if (a.unique && piece == 0) a.unique[u] = static_cast<int64_t>(key) + a.row_start;
 }
 
-// One group of LPR lanes per (chunk, column block).
+// One group of LPR lanes per (chunk, column block), with all of the chunk's rows in flight at once (a group per sorted
+// position instead, most of them a single row, keeps too few bytes in flight: 241 us against 134 us for 1.57 M rows of
+// 64 bf16).
 template <class GT, class OT, int LPR>
 __global__ __launch_bounds__(kThreads) void fold_kernel(FoldArgs a) {
-    constexpr int kGroups = kThreads / LPR;
-    constexpr int kBatch = GT::kBytes == 2 ? 8 : 4;  // upstream pieces in flight per lane
+    constexpr int kGroups = kThreads / LPR, kPerTile = kSortTile / kChunk;
+    constexpr int kBatch = GT::kBytes == 2 ? kChunk : kChunk / 2;  // rows in flight
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / LPR;
     const uint32_t chunk = static_cast<uint32_t>(unit / a.cols);
     const int piece = static_cast<int>(unit % a.cols) * LPR + threadIdx.x % LPR;
-    uint32_t u = 0;
+    uint32_t u = 0;  // the distinct rows before the chunk
     if (a.unique) {
-        // a workgroup's chunks lie in one or two tiles: the distinct rows before the first, then on by its own count
         const uint32_t c0 = static_cast<uint32_t>(static_cast<int64_t>(blockIdx.x) * kGroups / a.cols);
-        constexpr int kPerTile = kSortTile / kChunk;
         const uint32_t t0 = min(c0, a.chunks - 1) / kPerTile;
         u = heads_before(a, static_cast<int>(t0));
-        if (chunk < a.chunks) {
+        if (chunk < a.chunks) {  // (the workgroup's chunks lie in one tile or two)
             for (uint32_t t = t0; t < chunk / kPerTile; ++t) u += a.heads[t];
             u += a.chunk_base[chunk];
         }
     }
-    if (chunk >= a.chunks) return;
-    const bool live = piece < a.D / 8;
+    if (chunk >= a.chunks || piece >= a.D / 8) return;
     const uint32_t s = chunk * kChunk, e = min(s + kChunk, a.n);
-    uint32_t prev = s ? a.sorted[s - 1].key : 0xFFFFFFFFu;
+    uint32_t cur = s ? a.sorted[s - 1].key : 0xFFFFFFFFu;  // the running segment's row
     const uint32_t after = e < a.n ? a.sorted[e].key : a.R;  // R: nothing goes on
     float acc[8] = {};
-    bool entered = true;   // the running segment began before the chunk
-    bool open = false;     // a segment is running
-    uint32_t cur = prev;
+    bool entered = true;  // the running segment began before the chunk
+    bool open = false;    // it has positions in the chunk
     auto close = [&](bool goes_on) {
-        if (!open || !live) return;
-        if (entered) {
+        if (!open) return;
+        if (entered || goes_on) {
             Piece<F32> p;
             p.from(acc);
-            p.store(a.enter + static_cast<int64_t>(chunk) * a.D, piece);
-        } else if (goes_on) {
-            Piece<F32> p;
-            p.from(acc);
-            p.store(a.leave + static_cast<int64_t>(chunk) * a.D, piece);
+            p.store((entered ? a.enter : a.leave) + static_cast<int64_t>(chunk) * a.D, piece);
+            if (!entered && a.unique && piece == 0) a.leave_to[chunk] = u - 1;
         } else {
             put_row<OT>(a, cur, u - 1, piece, acc);
         }
@@ -435,22 +506,22 @@ __global__ __launch_bounds__(kThreads) void fold_kernel(FoldArgs a) {
         for (int j = 0; j < kBatch; ++j) pr[j] = b + j < e ? a.sorted[b + j] : Pair{a.R, 0};
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
-            if (pr[j].key < a.R && live) v[j].load(a.up + static_cast<int64_t>(pr[j].pos) * a.D * GT::kBytes, piece);
+            if (pr[j].key < a.R) v[j].load(a.up + static_cast<int64_t>(pr[j].pos) * a.D * GT::kBytes, piece);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            if (b + j >= e || pr[j].key >= a.R) continue;
+            if (pr[j].key >= a.R) continue;
             float f[8];
-            if (live) v[j].to(f);
+            v[j].to(f);
             if (pr[j].key != cur) {
                 close(false);
                 cur = pr[j].key;
                 entered = false;
                 ++u;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) acc[q] = live ? f[q] : 0.f;
+                for (int q = 0; q < 8; ++q) acc[q] = f[q];
             } else {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) acc[q] += live ? f[q] : 0.f;
+                for (int q = 0; q < 8; ++q) acc[q] += f[q];
             }
             open = true;
         }
@@ -458,65 +529,227 @@ __global__ __launch_bounds__(kThreads) void fold_kernel(FoldArgs a) {
     close(after == cur);
 }
 
-// Segments that cross chunks: the chunk where one begins adds its own partial sum and those of the chunks it enters,
-// in order.  In the rows form also the rows past the last distinct one: zeros, and -1 for their ids.
+// Segments that cross chunks: the chunk where one begins adds its own partial sum and those of the chunks it enters.
+// A workgroup looks at kJoinChunks chunks of one column block, a wave at a quarter of them; the 64 / LPR groups of lanes
+// of the wave take a segment's chunks in turn and their sums are added by shuffles.  A segment of kLong chunks or more
+// (a hot row) is taken by the whole workgroup, kBatch chunks per group at a time.  Every order is fixed.  In the rows
+// form also the rows past the last distinct one: zeros, and -1 for their ids.
+constexpr int kJoinChunks = 16;
+constexpr int kLong = 16;
+
+template <int LPR>
+__device__ inline void add_groups(float (&acc)[8]) {
+#pragma unroll
+    for (int off = LPR; off < 64; off <<= 1)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[q] += __shfl_xor(acc[q], off, 64);
+}
+
 template <class OT, int LPR>
 __global__ __launch_bounds__(kThreads) void join_kernel(FoldArgs a) {
-    constexpr int kGroups = kThreads / LPR;
-    constexpr int kPerTile = kSortTile / kChunk;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / LPR;
-    const uint32_t chunk = static_cast<uint32_t>(unit / a.cols);
-    const int piece = static_cast<int>(unit % a.cols) * LPR + threadIdx.x % LPR;
-    uint32_t before = 0, all = 0, t0 = 0;
-    if (a.unique) {
-        const uint32_t c0 = static_cast<uint32_t>(static_cast<int64_t>(blockIdx.x) * kGroups / a.cols);
-        t0 = min(c0, a.chunks - 1) / kPerTile;
-        before = heads_before(a, static_cast<int>(t0));
-        all = heads_before(a, a.tiles);
-        if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = static_cast<int32_t>(all);
-    }
-    if (chunk >= a.chunks || piece >= a.D / 8) return;
-    const uint32_t s = chunk * kChunk, e = min(s + kChunk, a.n);
-    if (a.unique) {
-        Piece<OT> z;
-        const float zero[8] = {};
-        z.from(zero);
-        for (uint32_t k = max(s, all); k < e; ++k) {
-            z.store(a.out + static_cast<int64_t>(k) * a.D * OT::kBytes, piece);
-            if (piece == 0) a.unique[k] = -1;
+    constexpr int kWaves = kThreads / 64, kGroups = 64 / LPR, kBatch = 4;
+    __shared__ float sums[kWaves][LPR][9];
+    const int cb = blockIdx.x % a.cols;
+    const uint32_t c0 = blockIdx.x / a.cols * kJoinChunks;
+    const uint32_t c1 = min(c0 + kJoinChunks, a.chunks);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int group = lane / LPR, piece = cb * LPR + lane % LPR;
+    const bool live = piece < a.D / 8;
+    // which chunks a segment that began in them leaves, and which of those are long: the same in every wave
+    bool crosses = false, goes_far = false;
+    uint32_t my_key = a.R;
+    if (lane < kJoinChunks && c0 + lane < c1) {
+        const uint32_t s = (c0 + lane) * kChunk, e = min(s + kChunk, a.n);
+        if (e < a.n) {
+            const uint32_t far = c0 + lane + kLong;
+            my_key = a.sorted[e].key;
+            const uint32_t last = a.sorted[e - 1].key, prev = s ? a.sorted[s - 1].key : a.R;
+            const uint32_t far_key = far < a.chunks ? a.sorted[far * kChunk].key : a.R;
+            crosses = my_key < a.R && last == my_key && prev != my_key;
+            goes_far = crosses && far_key == my_key;
         }
     }
-    if (e >= a.n) return;
-    const uint32_t key = a.sorted[e].key;
-    if (key >= a.R || a.sorted[e - 1].key != key) return;                                  // nothing crosses the end
-    if (s && a.sorted[s - 1].key == key) return;                                           // it began before
-    float acc[8];
-    Piece<F32> p;
-    p.load(a.leave + static_cast<int64_t>(chunk) * a.D, piece);
-    p.to(acc);
-    for (uint32_t c = chunk + 1; c < a.chunks && a.sorted[c * kChunk].key == key; ++c) {
+    const uint64_t all_crossing = __ballot(crosses), far = __ballot(goes_far);
+    if (a.unique) {
+        const uint32_t all = heads_before(a, a.tiles);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = static_cast<int32_t>(all);
+        const uint32_t e = min(c1 * kChunk, a.n);
+        if (live && e > all) {
+            Piece<OT> z;
+            const float zero[8] = {};
+            z.from(zero);
+            for (uint32_t k = max(c0 * kChunk, all) + threadIdx.x / LPR; k < e; k += kThreads / LPR) {
+                z.store(a.out + static_cast<int64_t>(k) * a.D * OT::kBytes, piece);
+                if (piece == 0) a.unique[k] = -1;
+            }
+        }
+    }
+    auto add = [&](float (&acc)[8], uint32_t chunk) {
         float f[8];
-        p.load(a.enter + static_cast<int64_t>(c) * a.D, piece);
+        Piece<F32> p;
+        p.load(a.enter + static_cast<int64_t>(chunk) * a.D, piece);
         p.to(f);
 #pragma unroll
         for (int q = 0; q < 8; ++q) acc[q] += f[q];
+    };
+    auto first = [&](float (&acc)[8], uint32_t chunk) {
+        Piece<F32> p;
+        p.load(a.leave + static_cast<int64_t>(chunk) * a.D, piece);
+        p.to(acc);
+    };
+    constexpr int kQuarter = kJoinChunks / kWaves;
+    for (uint64_t todo = all_crossing & ~far & (((1ull << kQuarter) - 1) << (wave * kQuarter)); todo; todo &= todo - 1) {
+        const int bit = __builtin_ctzll(todo);
+        const uint32_t chunk = c0 + bit, key = __shfl(my_key, bit, 64);
+        float acc[8] = {};
+        if (group == 0 && live) first(acc, chunk);
+        for (uint32_t c = chunk + 1 + group; c < a.chunks && a.sorted[c * kChunk].key == key; c += kGroups)
+            if (live) add(acc, c);
+        add_groups<LPR>(acc);
+        if (group == 0 && live) put_row<OT>(a, key, a.unique ? a.leave_to[chunk] : 0, piece, acc);
     }
-    uint32_t u = 0;
-    if (a.unique) {  // the segment is the last that begins in its chunk
-        u = before;
-        for (uint32_t t = t0; t < (chunk + 1) / kPerTile; ++t) u += a.heads[t];
-        if ((chunk + 1) % kPerTile) u += a.chunk_base[chunk + 1];
-        u -= 1;
+    for (uint64_t todo = far; todo; todo &= todo - 1) {
+        const int bit = __builtin_ctzll(todo);
+        const uint32_t chunk = c0 + bit, key = __shfl(my_key, bit, 64);
+        float acc[8] = {};
+        if (wave == 0 && group == 0 && live) first(acc, chunk);
+        constexpr int kStep = kWaves * kGroups * kBatch;
+        for (uint32_t c = chunk + 1 + (wave * kGroups + group) * kBatch; c < a.chunks; c += kStep) {
+            uint32_t k[kBatch];
+            Piece<F32> p[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                k[j] = c + j < a.chunks ? a.sorted[(c + j) * kChunk].key : a.R;
+                // (a chunk that is not entered holds anything: loaded, not used)
+                if (live && c + j < a.chunks) p[j].load(a.enter + static_cast<int64_t>(c + j) * a.D, piece);
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (k[j] != key || !live) continue;
+                float f[8];
+                p[j].to(f);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) acc[q] += f[q];
+            }
+            if (k[kBatch - 1] != key) break;
+        }
+        add_groups<LPR>(acc);
+        if (group == 0)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) sums[wave][lane][q] = acc[q];
+        __syncthreads();
+        if (wave == 0 && group == 0 && live) {
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) acc[q] += sums[w][lane][q];
+            put_row<OT>(a, key, a.unique ? a.leave_to[chunk] : 0, piece, acc);
+        }
+        __syncthreads();
     }
-    put_row<OT>(a, key, u, piece, acc);
 }
 
-// zeros over 16-byte pieces
-__global__ __launch_bounds__(kThreads) void zero_kernel(u32x4* p, int64_t n16) {
-    const u32x4 z = {};
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n16;
-         i += static_cast<int64_t>(gridDim.x) * kThreads)
-        p[i] = z;
+// Up to kSmall ids: every workgroup sorts them in LDS (a bitonic network over (row, position)) and folds its share of
+// (distinct row, column block) units, one group of LPR lanes each; the units past the last distinct row are the rows
+// form's tail.  One launch instead of six or more: at these sizes the launches are the time.
+struct SmallArgs {
+    SortArgs ids;
+    FoldArgs fold;
+};
+
+template <class GT, class OT, int LPR>
+__global__ __launch_bounds__(kThreads) void small_kernel(SmallArgs a) {
+    constexpr int kBatch = GT::kBytes == 2 ? 8 : 4;
+    __shared__ uint64_t s[kSmall];
+    __shared__ uint16_t start[kSmall + 1];
+    __shared__ uint32_t wsum[kThreads / 64];
+    const int n = static_cast<int>(a.fold.n), tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int size = 64;
+    while (size < n) size <<= 1;
+    for (int i = tid; i < size; i += kThreads)
+        s[i] = (static_cast<uint64_t>(i < n ? load_key(a.ids, i) : 0xFFFFFFFFu) << 32) | static_cast<uint32_t>(i);
+    for (int k = 2; k <= size; k <<= 1)
+        for (int j = k >> 1; j >= 1; j >>= 1) {
+            __syncthreads();
+            for (int i = tid; i < size / 2; i += kThreads) {
+                const int lo = (i / j) * 2 * j + i % j, hi = lo + j;  // j is a power of two
+                const uint64_t x = s[lo], y = s[hi];
+                if ((x > y) == ((lo & k) == 0)) {
+                    s[lo] = y;
+                    s[hi] = x;
+                }
+            }
+        }
+    __syncthreads();
+    // where each distinct row begins: four positions per thread
+    constexpr int kPer = kSmall / kThreads;
+    auto key_at = [&](int i) { return i < n ? static_cast<uint32_t>(s[i] >> 32) : 0xFFFFFFFFu; };
+    bool head[kPer];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = tid * kPer + j;
+        const uint32_t key = key_at(i);
+        head[j] = key < a.fold.R && (i == 0 || key_at(i - 1) != key);
+        mine += head[j];
+    }
+    uint32_t scan = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const uint32_t o = __shfl_up(scan, off, 64);
+        scan += lane >= off ? o : 0;
+    }
+    if (lane == 63) wsum[wave] = scan;
+    __syncthreads();
+    uint32_t u = scan - mine, count = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) {
+        u += w < wave ? wsum[w] : 0;
+        count += wsum[w];
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+        if (head[j]) start[u++] = static_cast<uint16_t>(tid * kPer + j);
+    __syncthreads();
+    const FoldArgs& f = a.fold;
+    if (f.unique && blockIdx.x == 0 && tid == 0) *f.count = static_cast<int32_t>(count);
+
+    const uint32_t unit = blockIdx.x * (kThreads / LPR) + tid / LPR;
+    const uint32_t seg = unit / f.cols;
+    const int piece = static_cast<int>(unit % f.cols) * LPR + tid % LPR;
+    if (seg >= f.n || piece >= f.D / 8) return;
+    if (seg >= count) {
+        if (f.unique) {
+            Piece<OT> z;
+            const float zero[8] = {};
+            z.from(zero);
+            z.store(f.out + static_cast<int64_t>(seg) * f.D * OT::kBytes, piece);
+            if (piece == 0) f.unique[seg] = -1;
+        }
+        return;
+    }
+    const int b0 = start[seg];
+    const uint32_t key = static_cast<uint32_t>(s[b0] >> 32);
+    float acc[8] = {};
+    for (int b = b0; b < n && static_cast<uint32_t>(s[b] >> 32) == key; b += kBatch) {
+        Piece<GT> v[kBatch];
+        bool in[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const uint64_t e = b + j < n ? s[b + j] : ~0ull;
+            in[j] = static_cast<uint32_t>(e >> 32) == key;
+            if (in[j]) v[j].load(f.up + static_cast<int64_t>(static_cast<uint32_t>(e)) * f.D * GT::kBytes, piece);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (!in[j]) continue;
+            float x[8];
+            v[j].to(x);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) acc[q] += x[q];
+        }
+    }
+    put_row<OT>(f, key, seg, piece, acc);
 }
 
 __global__ void zero_count_kernel(int32_t* count) { *count = 0; }
@@ -530,7 +763,7 @@ struct Plan {
     int bits, passes;      // digit bits and passes
     int tiles;
     uint32_t chunks;
-    int64_t pairs, hist, totals, heads, chunk_base, leave, enter, bytes;  // offsets
+    int64_t pairs, hist, totals, heads, chunk_base, leave_to, leave, enter, bytes;  // offsets
 };
 
 int64_t up16(int64_t v) { return (v + 15) & ~15ll; }
@@ -546,12 +779,14 @@ Plan plan_of(int64_t n, int32_t D, int64_t R) {
     p.pairs = at;
     at += up16(2 * n * static_cast<int64_t>(sizeof(Pair)));
     p.hist = at;
-    at += up16(static_cast<int64_t>(p.passes) * p.tiles * (4ll << p.bits));
+    at += up16(static_cast<int64_t>(p.tiles) * (4ll << p.bits));
     p.totals = at;
     at += up16(4ll << p.bits);
     p.heads = at;
     at += up16(4ll * p.tiles);
     p.chunk_base = at;
+    at += up16(4ll * p.chunks);
+    p.leave_to = at;
     at += up16(4ll * p.chunks);
     p.leave = at;
     at += up16(4ll * p.chunks * D);
@@ -561,12 +796,10 @@ Plan plan_of(int64_t n, int32_t D, int64_t R) {
     return p;
 }
 
-// sorted (row, position) pairs of the ids, in the workspace
+// sorted (row, position) pairs of the ids, in the workspace; `zeros` bytes at `zero` are written on the way
 const Pair* sort_ids(const Plan& p, const void* ids, int id_bytes, int64_t n, int C, int64_t stride, int64_t R,
-                     int64_t row_start, uint8_t* ws, hipStream_t stream) {
+                     int64_t row_start, uint8_t* ws, void* zero, int64_t zeros, hipStream_t stream) {
     Pair* buf[2] = {reinterpret_cast<Pair*>(ws + p.pairs), reinterpret_cast<Pair*>(ws + p.pairs) + n};
-    const uint32_t table = static_cast<uint32_t>(p.tiles) << p.bits;
-    uint32_t* hist = reinterpret_cast<uint32_t*>(ws + p.hist);
     SortArgs a = {};
     a.ids = ids;
     a.id_bytes = id_bytes;
@@ -577,56 +810,62 @@ const Pair* sort_ids(const Plan& p, const void* ids, int id_bytes, int64_t n, in
     a.n = static_cast<uint32_t>(n);
     a.bits = p.bits;
     a.tiles = p.tiles;
-    a.hist = hist;
-    hipLaunchKernelGGL(hist_kernel, dim3(p.tiles), dim3(kSortThreads), 0, stream, a, hist + table,
-                       table * (p.passes - 1));
+    a.hist = reinterpret_cast<uint32_t*>(ws + p.hist);
+    // (what a grid does not hold, 1 TB and more, in a launch of its own)
+    const int64_t n16 = zeros / 16, most = (kMaxGridX / 2 - p.tiles) * kSortThreads;
+    const Zeros z = {static_cast<u32x4*>(zero), n16 < most ? n16 : most};
+    const dim3 grid(static_cast<unsigned>(p.tiles + (z.n16 + kSortThreads - 1) / kSortThreads));
+    if (n16 > most) launch_zero(z.p + most, (n16 - most) * 16, stream, "engram_embed_grad");
     for (int q = 0; q < p.passes; ++q) {
         a.shift = q * p.bits;
-        a.hist = hist + static_cast<int64_t>(table) * q;
-        a.hist_next = q + 1 < p.passes ? a.hist + table : nullptr;
         a.in = buf[(q + 1) & 1];
         a.out = buf[q & 1];
-        a.totals = nullptr;
+        if (q == 0) hipLaunchKernelGGL(hist_kernel<true>, grid, dim3(kSortThreads), 0, stream, a, z);
+        else hipLaunchKernelGGL(hist_kernel<false>, dim3(p.tiles), dim3(kSortThreads), 0, stream, a, Zeros{});
         if (p.tiles > kDirectTiles) {
             a.totals = reinterpret_cast<uint32_t*>(ws + p.totals);
             hipLaunchKernelGGL(prefix_kernel, dim3(((1 << p.bits) + 63) / 64), dim3(1024), 0, stream, a);
         }
-        if (q == 0)
-            hipLaunchKernelGGL(scatter_kernel<true>, dim3(p.tiles), dim3(kSortThreads), 0, stream, a);
-        else
-            hipLaunchKernelGGL(scatter_kernel<false>, dim3(p.tiles), dim3(kSortThreads), 0, stream, a);
+        if (q == 0) launch_scatter<true>(a, stream);
+        else launch_scatter<false>(a, stream);
     }
     return buf[(p.passes - 1) & 1];
 }
 
 template <class GT, class OT, int LPR>
-int launch_fold_as(FoldArgs& a, hipStream_t stream, const char* what) {
+int launch_fold_as(FoldArgs& a, const SortArgs* small, hipStream_t stream, const char* what) {
     a.cols = (a.D / 8 + LPR - 1) / LPR;
-    const int64_t groups = static_cast<int64_t>(a.chunks) * a.cols;
-    const int64_t blocks = (groups + kThreads / LPR - 1) / (kThreads / LPR);
+    if (small) {
+        const int64_t blocks = (static_cast<int64_t>(a.n) * a.cols + kThreads / LPR - 1) / (kThreads / LPR);
+        hipLaunchKernelGGL((small_kernel<GT, OT, LPR>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream,
+                           SmallArgs{*small, a});
+        return check_launch(what);
+    }
+    const int64_t blocks = (static_cast<int64_t>(a.chunks) * a.cols + kThreads / LPR - 1) / (kThreads / LPR);
     if (blocks > 0x7FFFFFFF) return fail(ENGRAM_EINVAL, "%s: too many ids for the row width", what);
     hipLaunchKernelGGL((fold_kernel<GT, OT, LPR>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a);
-    hipLaunchKernelGGL((join_kernel<OT, LPR>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a);
+    const int64_t joins = static_cast<int64_t>((a.chunks + kJoinChunks - 1) / kJoinChunks) * a.cols;
+    hipLaunchKernelGGL((join_kernel<OT, LPR>), dim3(static_cast<unsigned>(joins)), dim3(kThreads), 0, stream, a);
     return check_launch(what);
 }
 
 template <class GT, class OT>
-int launch_fold(FoldArgs& a, hipStream_t stream, const char* what) {
+int launch_fold(FoldArgs& a, const SortArgs* small, hipStream_t stream, const char* what) {
     const int pieces = a.D / 8;
-    if (pieces <= 4) return launch_fold_as<GT, OT, 4>(a, stream, what);
-    if (pieces <= 8) return launch_fold_as<GT, OT, 8>(a, stream, what);
-    if (pieces <= 16) return launch_fold_as<GT, OT, 16>(a, stream, what);
-    if (pieces <= 32) return launch_fold_as<GT, OT, 32>(a, stream, what);
-    return launch_fold_as<GT, OT, 64>(a, stream, what);
+    if (pieces <= 4) return launch_fold_as<GT, OT, 4>(a, small, stream, what);
+    if (pieces <= 8) return launch_fold_as<GT, OT, 8>(a, small, stream, what);
+    if (pieces <= 16) return launch_fold_as<GT, OT, 16>(a, small, stream, what);
+    if (pieces <= 32) return launch_fold_as<GT, OT, 32>(a, small, stream, what);
+    return launch_fold_as<GT, OT, 64>(a, small, stream, what);
 }
 
-int launch_fold_types(FoldArgs& a, int32_t gd, int32_t od, hipStream_t stream, const char* what) {
+int launch_fold_types(FoldArgs& a, const SortArgs* small, int32_t gd, int32_t od, hipStream_t stream, const char* what) {
     if (gd == ENGRAM_BF16) {
-        if (od == ENGRAM_BF16) return launch_fold<Bf16, Bf16>(a, stream, what);
-        return launch_fold<Bf16, F32>(a, stream, what);
+        if (od == ENGRAM_BF16) return launch_fold<Bf16, Bf16>(a, small, stream, what);
+        return launch_fold<Bf16, F32>(a, small, stream, what);
     }
-    if (od == ENGRAM_BF16) return launch_fold<F32, Bf16>(a, stream, what);
-    return launch_fold<F32, F32>(a, stream, what);
+    if (od == ENGRAM_BF16) return launch_fold<F32, Bf16>(a, small, stream, what);
+    return launch_fold<F32, F32>(a, small, stream, what);
 }
 
 int check_ids(const char* what, int32_t id_bytes, int64_t T, int64_t stride, int32_t C, int64_t R) {
@@ -648,11 +887,12 @@ int check_width(const char* what, int32_t D) {
 }  // namespace
 
 int launch_zero(void* p, int64_t bytes, hipStream_t stream, const char* what) {
-    const int64_t n16 = bytes / 16;
-    if (n16 == 0) return ENGRAM_OK;
-    const int64_t blocks = (n16 + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL(zero_kernel, dim3(static_cast<unsigned>(blocks < 16384 ? blocks : 16384)), dim3(kThreads), 0, stream,
-                       static_cast<u32x4*>(p), n16);
+    const Zeros z = {static_cast<u32x4*>(p), bytes / 16};
+    if (z.n16 == 0) return ENGRAM_OK;
+    const int64_t blocks = (z.n16 + kThreads - 1) / kThreads;
+    const int64_t x = blocks < kMaxGridX ? blocks : kMaxGridX;
+    hipLaunchKernelGGL(zero_kernel, dim3(static_cast<unsigned>(x), static_cast<unsigned>((blocks + x - 1) / x)),
+                       dim3(kThreads), 0, stream, z);
     return check_launch(what);
 }
 
@@ -698,6 +938,56 @@ extern "C" int64_t engram_embed_grad_workspace_bytes(int64_t n, int32_t D, int64
     return n == 0 ? 0 : plan_of(n, D, R).bytes;
 }
 
+namespace engram {
+namespace {
+
+// What both forms of the gradient do once their arguments are checked (n > 0 ids): `f` holds the outputs.
+int embed_grad(FoldArgs& f, const void* ids, int32_t id_bytes, int64_t n, int64_t stride, int32_t C, const void* up,
+               int32_t up_dtype, int64_t R, int64_t row_start, int32_t D, float scale, int32_t out_dtype, void* workspace,
+               int64_t workspace_bytes, hipStream_t s, const char* what) {
+    const Plan p = plan_of(n, D, R);
+    if (workspace_bytes < p.bytes)
+        return fail(ENGRAM_ERANGE, "%s: workspace of %lld bytes, needs %lld", what, (long long)workspace_bytes,
+                    (long long)p.bytes);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    f.n = static_cast<uint32_t>(n);
+    f.R = static_cast<uint32_t>(R);
+    f.up = static_cast<const uint8_t*>(up);
+    f.D = D;
+    f.scale = scale;
+    f.row_start = row_start;
+    const bool fill = !f.unique && !f.accumulate;
+    const int64_t bytes = R * D * (out_dtype == ENGRAM_BF16 ? 2 : 4);
+    if (n <= kSmall) {
+        if (fill) {
+            const int rc = launch_zero(f.out, bytes, s, what);
+            if (rc != ENGRAM_OK) return rc;
+        }
+        SortArgs a = {};
+        a.ids = ids;
+        a.id_bytes = id_bytes;
+        a.C = C;
+        a.stride = stride;
+        a.row_start = row_start;
+        a.R = f.R;
+        a.n = f.n;
+        return launch_fold_types(f, &a, up_dtype, out_dtype, s, what);
+    }
+    f.sorted = sort_ids(p, ids, id_bytes, n, C, stride, R, row_start, ws, f.out, fill ? bytes : 0, s);
+    f.tiles = p.tiles;
+    f.chunks = p.chunks;
+    f.heads = reinterpret_cast<uint32_t*>(ws + p.heads);
+    f.chunk_base = reinterpret_cast<uint32_t*>(ws + p.chunk_base);
+    f.leave_to = reinterpret_cast<uint32_t*>(ws + p.leave_to);
+    f.leave = reinterpret_cast<float*>(ws + p.leave);
+    f.enter = reinterpret_cast<float*>(ws + p.enter);
+    if (f.unique) hipLaunchKernelGGL(heads_kernel, dim3(p.tiles), dim3(kThreads), 0, s, f);
+    return launch_fold_types(f, nullptr, up_dtype, out_dtype, s, what);
+}
+
+}  // namespace
+}  // namespace engram
+
 extern "C" int engram_embed_grad(const void* ids, int32_t id_bytes, int64_t T, int64_t id_token_stride, int32_t C,
                                  const void* up, int32_t up_dtype, int64_t R, int64_t row_start, int32_t D,
                                  float scale, void* grad, int32_t grad_dtype, int32_t accumulate, void* workspace,
@@ -717,32 +1007,12 @@ extern "C" int engram_embed_grad(const void* ids, int32_t id_bytes, int64_t T, i
             return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
     }
     hipStream_t s = as_stream(stream);
-    Plan p = {};
-    if (n) {
-        p = plan_of(n, D, R);
-        if (workspace_bytes < p.bytes)
-            return fail(ENGRAM_ERANGE, "%s: workspace of %lld bytes, needs %lld", what, (long long)workspace_bytes,
-                        (long long)p.bytes);
-    }
-    if (!accumulate) {
-        rc = launch_zero(grad, R * D * (grad_dtype == ENGRAM_BF16 ? 2 : 4), s, what);
-        if (rc != ENGRAM_OK || n == 0) return rc;
-    }
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if (n == 0) return launch_zero(grad, R * D * (grad_dtype == ENGRAM_BF16 ? 2 : 4), s, what);
     FoldArgs f = {};
-    f.sorted = sort_ids(p, ids, id_bytes, n, C, id_token_stride, R, row_start, ws, s);
-    f.n = static_cast<uint32_t>(n);
-    f.R = static_cast<uint32_t>(R);
-    f.up = static_cast<const uint8_t*>(up);
-    f.D = D;
-    f.scale = scale;
     f.out = static_cast<uint8_t*>(grad);
     f.accumulate = accumulate != 0;
-    f.tiles = p.tiles;
-    f.chunks = p.chunks;
-    f.leave = reinterpret_cast<float*>(ws + p.leave);
-    f.enter = reinterpret_cast<float*>(ws + p.enter);
-    return launch_fold_types(f, up_dtype, grad_dtype, s, what);
+    return embed_grad(f, ids, id_bytes, n, id_token_stride, C, up, up_dtype, R, row_start, D, scale, grad_dtype, workspace,
+                      workspace_bytes, s, what);
 }
 
 extern "C" int engram_embed_grad_rows(const void* ids, int32_t id_bytes, int64_t T, int64_t id_token_stride, int32_t C,
@@ -764,28 +1034,10 @@ extern "C" int engram_embed_grad_rows(const void* ids, int32_t id_bytes, int64_t
     if (!ids || !up || !workspace || !unique || !rows) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
     if (!aligned(ids, id_bytes) || !aligned(up, 16) || !aligned(workspace, 16) || !aligned(unique, 8) || !aligned(rows, 16))
         return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
-    const Plan p = plan_of(n, D, R);
-    if (workspace_bytes < p.bytes)
-        return fail(ENGRAM_ERANGE, "%s: workspace of %lld bytes, needs %lld", what, (long long)workspace_bytes,
-                    (long long)p.bytes);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
     FoldArgs f = {};
-    f.sorted = sort_ids(p, ids, id_bytes, n, C, id_token_stride, R, row_start, ws, s);
-    f.n = static_cast<uint32_t>(n);
-    f.R = static_cast<uint32_t>(R);
-    f.up = static_cast<const uint8_t*>(up);
-    f.D = D;
-    f.scale = scale;
     f.out = static_cast<uint8_t*>(rows);
     f.unique = unique;
     f.count = count;
-    f.row_start = row_start;
-    f.tiles = p.tiles;
-    f.chunks = p.chunks;
-    f.heads = reinterpret_cast<uint32_t*>(ws + p.heads);
-    f.chunk_base = reinterpret_cast<uint32_t*>(ws + p.chunk_base);
-    f.leave = reinterpret_cast<float*>(ws + p.leave);
-    f.enter = reinterpret_cast<float*>(ws + p.enter);
-    hipLaunchKernelGGL(heads_kernel, dim3(p.tiles), dim3(kThreads), 0, s, f);
-    return launch_fold_types(f, up_dtype, rows_dtype, s, what);
+    return embed_grad(f, ids, id_bytes, n, id_token_stride, C, up, up_dtype, R, row_start, D, scale, rows_dtype, workspace,
+                      workspace_bytes, s, what);
 }

@@ -16,6 +16,8 @@
 // of a row and the outputs that need the sums, and the sum over tokens of dq and dk stays in registers over all of
 // the workgroup's tokens.  One barrier per token (the sums of the waves, in two LDS buffers taken in turn).  A second
 // launch adds the workgroups' sums in their order, so the same call gives the same bits.
+#include <type_traits>
+
 #include "rows.h"
 
 namespace engram {
@@ -24,7 +26,6 @@ namespace {
 constexpr int kMaxWaves = 16;
 constexpr int kMaxDim = 8192;
 constexpr int kCUs = 256;
-constexpr int kWavesPerCU = 20;
 
 struct GateGradArgs {
     const uint16_t* x;
@@ -82,91 +83,135 @@ __device__ inline void masked_token(const GateGradArgs& p, int64_t t, int piece)
     for (int c = 0; c <= p.hc; ++c) zero.store_nt(p.dkv + (t * (p.hc + 1) + c) * p.dim, piece);
 }
 
+// A wave's sum, in its last lane.
+__device__ inline float wave_sum_last(float v) {
+    auto add = [&](auto ctrl, auto rows) {
+        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, decltype(rows)::value,
+                                                        0xF, false));
+    };
+    using std::integral_constant;
+    integral_constant<int, 0xF> all;
+    add(integral_constant<int, 0x111>{}, all);  // row_shr 1, 2, 4, 8: lane 15 of each row of 16 has the row's sum
+    add(integral_constant<int, 0x112>{}, all);
+    add(integral_constant<int, 0x114>{}, all);
+    add(integral_constant<int, 0x118>{}, all);
+    add(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});  // row_bcast 15 into rows 1 and 3
+    add(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});  // row_bcast 31 into rows 2 and 3
+    return v;
+}
+
 template <int HC, int kMaxThreads>
 __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) {
-    __shared__ float sums[2][kMaxWaves][3 * HC];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    constexpr int kSums = 3 * HC, kReads = (kSums + 3) / 4;
+    __shared__ float sums[2][4 * kReads][kMaxWaves];  // [sum][wave]; waves the workgroup lacks hold zeros
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int piece = threadIdx.x;
     const bool live = piece < p.dim / 8;
+    for (int i = threadIdx.x; i < 2 * 4 * kReads * kMaxWaves; i += blockDim.x) (&sums[0][0][0])[i] = 0.f;
+    __syncthreads();
     float acc[HC][8] = {};
-    int turn = 0;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        if (p.mask && p.mask[t] == 0) {  // the whole workgroup
+    Piece<Bf16> hr[HC], kr[HC], ur[HC], vr;
+    auto load_copy = [&](int64_t t, int c) {
+        hr[c].load_nt(p.x + (t * HC + c) * p.dim, piece);
+        kr[c].load_nt(p.kv + t * p.ld_kv + static_cast<int64_t>(c) * p.dim, piece);
+        ur[c].load_nt(p.up + (t * HC + c) * p.dim, piece);
+    };
+    auto load_value = [&](int64_t t) { vr.load_nt(p.kv + t * p.ld_kv + static_cast<int64_t>(HC) * p.dim, piece); };
+    // the first token from t on that takes part; the masked ones before it are done with on the way
+    auto next = [&](int64_t t) {
+        for (; t < p.T && p.mask && p.mask[t] == 0; t += gridDim.x)
             if (live) masked_token(p, t, piece);
-            continue;
-        }
-        Piece<Bf16> hr[HC], kr[HC], ur[HC], vr;
-        const uint16_t* row = p.kv + t * p.ld_kv;
-        if (live) {
-            vr.load(row + static_cast<int64_t>(HC) * p.dim, piece);
+        return t;
+    };
+    int turn = 0;
+    int64_t t = next(blockIdx.x);
+    vr.v = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < HC; ++c) hr[c].v = kr[c].v = ur[c].v = u32x4{0, 0, 0, 0};
+    if (live && t < p.T) {
+        load_value(t);
+#pragma unroll
+        for (int c = 0; c < HC; ++c) load_copy(t, c);
+    }
+    while (t < p.T) {
+        {
+            float v[8];
+            vr.to(v);
 #pragma unroll
             for (int c = 0; c < HC; ++c) {
-                hr[c].load_nt(p.x + (t * HC + c) * p.dim, piece);
-                kr[c].load_nt(row + static_cast<int64_t>(c) * p.dim, piece);
-                ur[c].load_nt(p.up + (t * HC + c) * p.dim, piece);
-            }
-        } else {
-            vr.v = u32x4{0, 0, 0, 0};
+                float h[8], key[8], u[8], hh = 0.f, kk = 0.f, dg = 0.f;
+                hr[c].to(h);
+                kr[c].to(key);
+                ur[c].to(u);
 #pragma unroll
-            for (int c = 0; c < HC; ++c) hr[c].v = kr[c].v = ur[c].v = u32x4{0, 0, 0, 0};
-        }
-        float v[8];
-        vr.to(v);
-#pragma unroll
-        for (int c = 0; c < HC; ++c) {
-            float h[8], key[8], u[8], hh = 0.f, kk = 0.f, dg = 0.f;
-            hr[c].to(h);
-            kr[c].to(key);
-            ur[c].to(u);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                hh += h[e] * h[e];
-                kk += key[e] * key[e];
-                dg += u[e] * v[e];
-            }
-            hh = wave_sum(hh);
-            kk = wave_sum(kk);
-            dg = wave_sum(dg);
-            if (lane == 0) {
-                sums[turn][wave][3 * c] = hh;
-                sums[turn][wave][3 * c + 1] = kk;
-                sums[turn][wave][3 * c + 2] = dg;
+                for (int e = 0; e < 8; ++e) {
+                    hh += h[e] * h[e];
+                    kk += key[e] * key[e];
+                    dg += u[e] * v[e];
+                }
+                hh = wave_sum_last(hh);
+                kk = wave_sum_last(kk);
+                dg = wave_sum_last(dg);
+                if (lane == 63) {
+                    sums[turn][3 * c][wave] = hh;
+                    sums[turn][3 * c + 1][wave] = kk;
+                    sums[turn][3 * c + 2][wave] = dg;
+                }
             }
         }
         __syncthreads();
+        // the rows as they were loaded: widened again below rather than held as floats over the barrier
+#pragma unroll
+        for (int c = 0; c < HC; ++c) asm volatile("" : "+v"(hr[c].v), "+v"(kr[c].v), "+v"(ur[c].v));
+        // each 16 lanes add one sum over the waves: read j of lane l is sum 4 j + l / 16 of wave l % 16
+        float part[kReads];
+#pragma unroll
+        for (int j = 0; j < kReads; ++j) {
+            part[j] = sums[turn][4 * j + (lane >> 4)][lane & 15];
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1) part[j] += __shfl_xor(part[j], off, 64);
+        }
+        auto total = [&](int i) {
+            return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(part[i / 4]), (i % 4) * 16));
+        };
+        auto uniform = [](float f) { return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(f))); };
+        // the next token's rows are asked for as soon as this one's are used up
+        const int64_t ahead = next(t + gridDim.x);
+        const bool more = live && ahead < p.T;
+        if (more) load_value(ahead);
         float dv[8] = {};
 #pragma unroll
         for (int c = 0; c < HC; ++c) {
-            float hh = 0.f, kk = 0.f, dg = 0.f;
-            for (int w = 0; w < waves; ++w) {
-                hh += sums[turn][w][3 * c];
-                kk += sums[turn][w][3 * c + 1];
-                dg += sums[turn][w][3 * c + 2];
-            }
-            const Coef k = coef_of(p, hh, kk, dg, p.dot[t * HC + c]);
-            if (!live) continue;
-            Piece<Bf16> qr, kw;
-            qr.load(p.q + static_cast<int64_t>(c) * p.dim, piece);
-            kw.load(p.k + static_cast<int64_t>(c) * p.dim, piece);
-            float h[8], key[8], u[8], qf[8], kf[8], ox[8], ok[8];
-            hr[c].to(h);
-            kr[c].to(key);
-            ur[c].to(u);
-            qr.to(qf);
-            kw.to(kf);
+            Coef k = coef_of(p, total(3 * c), total(3 * c + 1), total(3 * c + 2), p.dot[t * HC + c]);
+            k = Coef{uniform(k.g), uniform(k.a), uniform(k.bh), uniform(k.bk)};
+            if (live) {
+                Piece<Bf16> qr, kw;
+                int at = c * (p.dim / 8) + piece;
+                asm volatile("" : "+v"(at));  // read anew for every token (from L2), not held in registers over them
+                qr.load(p.q, at);
+                kw.load(p.k, at);
+                float h[8], key[8], u[8], qf[8], kf[8], ox[8], ok[8];
+                hr[c].to(h);
+                kr[c].to(key);
+                ur[c].to(u);
+                qr.to(qf);
+                kw.to(kf);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float aw = k.a * (qf[e] * kf[e]);
-                ox[e] = u[e] + (aw * key[e] - k.bh * h[e]);
-                ok[e] = aw * h[e] - k.bk * key[e];
-                dv[e] += k.g * u[e];
-                acc[c][e] += k.a * (h[e] * key[e]);
+                for (int e = 0; e < 8; ++e) {
+                    const float aw = k.a * (qf[e] * kf[e]);
+                    ox[e] = u[e] + (aw * key[e] - k.bh * h[e]);
+                    ok[e] = aw * h[e] - k.bk * key[e];
+                    dv[e] += k.g * u[e];
+                    acc[c][e] += k.a * (h[e] * key[e]);
+                }
+                Piece<Bf16> o;
+                o.from(ox);
+                o.store_nt(p.dx + (t * HC + c) * p.dim, piece);
+                o.from(ok);
+                o.store_nt(p.dkv + (t * (HC + 1) + c) * p.dim, piece);
+                if (more) load_copy(ahead, c);
             }
-            Piece<Bf16> o;
-            o.from(ox);
-            o.store_nt(p.dx + (t * HC + c) * p.dim, piece);
-            o.from(ok);
-            o.store_nt(p.dkv + (t * (HC + 1) + c) * p.dim, piece);
+            __builtin_amdgcn_sched_barrier(0);  // one copy's floats at a time
         }
         if (live) {
             Piece<Bf16> o;
@@ -174,6 +219,7 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) 
             o.store_nt(p.dkv + (t * (HC + 1) + HC) * p.dim, piece);
         }
         turn ^= 1;
+        t = ahead;
     }
     if (!live) return;
 #pragma unroll
@@ -280,8 +326,15 @@ __global__ __launch_bounds__(1024) void gate_grad_sum_kernel(const float* part, 
     const int per = (rows + 15) / 16;
     const int r0 = min(run * per, rows), r1 = min(r0 + per, rows);
     float s = 0.f;
-    if (col < cols)
-        for (int r = r0; r < r1; ++r) s += part[static_cast<int64_t>(r) * cols + col];
+    if (col < cols) {
+        for (int r = r0; r < r1; r += 8) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = r + j < r1 ? part[static_cast<int64_t>(r + j) * cols + col] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += v[j];
+        }
+    }
     run_sum[run][threadIdx.x & 63] = s;
     __syncthreads();
     if (run != 0 || col >= cols) return;
@@ -294,11 +347,13 @@ __global__ __launch_bounds__(1024) void gate_grad_sum_kernel(const float* part, 
 
 int threads_of(int dim) { return (dim / 8 + 63) / 64 * 64; }
 
-// workgroups of a launch: as many as kWavesPerCU waves on every CU hold, and no more than there are tokens
-int64_t groups_of(int64_t T, int dim) {
-    const int waves = threads_of(dim) / 64;
-    const int64_t per_cu = kWavesPerCU / waves > 1 ? kWavesPerCU / waves : 1;
-    return T < per_cu * kCUs ? T : per_cu * kCUs;
+// Workgroups of a launch: as many as the CUs hold (the kernels' registers leave 12 waves a CU for hc 4, 16 for most, 20
+// for hc 1), yet four tokens or more for each once every CU has one: every workgroup leaves a row of sums to be added.
+int64_t groups_of(int64_t T, int hc, int dim) {
+    const int waves = threads_of(dim) / 64, fit = hc == 4 ? 12 : hc == 1 ? 20 : 16;
+    const int64_t per_cu = fit / waves > 1 ? fit / waves : 1;
+    const int64_t few = T < kCUs ? T : (T + 3) / 4 > kCUs ? (T + 3) / 4 : kCUs;
+    return few < per_cu * kCUs ? few : per_cu * kCUs;
 }
 
 bool shape_ok(int64_t T, int32_t hc, int32_t dim) {
@@ -311,7 +366,7 @@ bool shape_ok(int64_t T, int32_t hc, int32_t dim) {
 using namespace engram;
 
 extern "C" int64_t engram_gate_output_backward_workspace_bytes(int64_t T, int32_t hc, int32_t dim) {
-    return shape_ok(T, hc, dim) ? groups_of(T, dim) * hc * dim * 4 : -1;
+    return shape_ok(T, hc, dim) ? groups_of(T, hc, dim) * hc * dim * 4 : -1;
 }
 
 extern "C" int engram_gate_output_backward(const uint16_t* x, const uint16_t* kv, int64_t ld_kv, const uint16_t* q_weight,
@@ -335,7 +390,7 @@ extern "C" int engram_gate_output_backward(const uint16_t* x, const uint16_t* kv
             !aligned(dot, 4) || !aligned(workspace, 16))
             return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
     }
-    const int64_t groups = groups_of(T, dim);
+    const int64_t groups = groups_of(T, hc, dim);
     if (T > 0 && workspace_bytes < groups * hc * dim * 4)
         return fail(ENGRAM_ERANGE, "%s: workspace of %lld bytes, needs %lld", what, (long long)workspace_bytes,
                     (long long)(groups * hc * dim * 4));

@@ -1,11 +1,12 @@
 // engram_grad_norm: the 2-norm of many tensors taken as one vector.
 // engram_clip_grads: every tensor times min(1, max_norm / (norm + 1e-6)).
 //
-// Both stream each gradient once.  A launch takes up to kTensors tensors, cut into runs of kRunBytes; a workgroup finds
-// its tensor by binary search in the kernel's arguments.  The squares of a thread are added in fp32 eight at a time and
-// then in fp64: fp32 running sums over a run would lose digits against the one rounding of the result, and squares
-// past fp32's range (gradients over 1.8e19) would give infinity where the norm is finite.  The runs' sums are added in
-// their order by one workgroup, so the norm has the same bits from every call.
+// Both stream each gradient once.  A launch takes up to kTensors tensors, cut into runs, one per workgroup, which finds
+// its tensor by binary search in the kernel's arguments.  Squares are added in fp64: fp32 running sums over a run would
+// lose digits against the one rounding of the result, and squares past fp32's range (gradients over 1.8e19) would give
+// infinity where the norm is finite.  The runs' sums are added in their order by one workgroup, so the norm has the
+// same bits from every call.  The clipping takes the runs last to first: what the norm read last is still in the
+// Infinity Cache.
 #include "rows.h"
 
 namespace engram {
@@ -13,7 +14,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTensors = 96;         // per launch: 96 * 28 bytes of kernel arguments
-constexpr int64_t kRunBytes = 65536;
+constexpr int kNormPieces = 16;       // 16-byte pieces per thread and run
+constexpr int kClipPieces = 1;
 
 struct NormList {
     const void* in[kTensors];
@@ -54,39 +56,79 @@ __device__ inline float element(const void* p, bool f32, int64_t i) {
     return f32 ? static_cast<const float*>(p)[i] : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
 }
 
-template <class T>
-__device__ inline double run_squares(const void* in, int64_t n, int64_t i0, int64_t i1) {
+// 16 bytes of a gradient: eight bf16 or four fp32
+__device__ inline double squares(u32x4 v, bool f32) {
     double s = 0.0;
-    const int64_t p1 = i1 / 8;
-#pragma unroll 4
-    for (int64_t p = i0 / 8 + threadIdx.x; p < p1; p += kThreads) {
-        Piece<T> v;
-        v.load(in, p);
-        float f[8];
-        v.to(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += static_cast<double>(f[e]) * static_cast<double>(f[e]);
+    for (int i = 0; i < 4; ++i) {
+        if (f32) {
+            const double a = __uint_as_float(v[i]);
+            s += a * a;
+        } else {
+            const double a = __uint_as_float(v[i] << 16), b = __uint_as_float(v[i] & 0xFFFF0000u);
+            s += a * a;
+            s += b * b;
+        }
     }
     return s;
+}
+__device__ inline u32x4 scaled(u32x4 v, bool f32, float c) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (f32) {
+            v[i] = __float_as_uint(__uint_as_float(v[i]) * c);
+        } else {
+            const bf16x2 p = {static_cast<__bf16>(__uint_as_float(v[i] << 16) * c),
+                              static_cast<__bf16>(__uint_as_float(v[i] & 0xFFFF0000u) * c)};
+            v[i] = __builtin_bit_cast(uint32_t, p);
+        }
+    }
+    return v;
+}
+
+// a workgroup's run: its tensor, its elements and how many whole 16-byte pieces it may move at once
+struct Run {
+    int t;
+    bool f32;
+    int64_t i0, i1;   // elements
+    int64_t p0, p1;   // 16-byte pieces of the tensor, none if it is not aligned to them
+    int64_t rest;     // first element after the pieces
+};
+template <int kPieces>
+__device__ inline Run run_of(const NormList& l, uint32_t block, int t, bool pieces) {
+    Run r;
+    r.t = t;
+    r.f32 = (l.f32[r.t >> 5] >> (r.t & 31)) & 1;
+    const int per = r.f32 ? 4 : 8;
+    r.i0 = static_cast<int64_t>(block - l.first[r.t]) * (per * kPieces * kThreads);
+    r.i1 = min(r.i0 + per * kPieces * kThreads, l.n[r.t]);
+    r.p0 = r.i0 / per;
+    r.p1 = pieces ? r.i1 / per : r.p0;
+    r.rest = r.p1 * per;
+    return r;
 }
 
 __global__ __launch_bounds__(kThreads) void norm_kernel(NormList l, double* part) {
     __shared__ double lds[kThreads / 64];
     const int t = tensor_of(l, blockIdx.x);
-    const bool f32 = (l.f32[t >> 5] >> (t & 31)) & 1;
-    const int64_t run = kRunBytes / (f32 ? 4 : 2);
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x - l.first[t]) * run;
-    const int64_t i1 = min(i0 + run, l.n[t]);
+    const Run r = run_of<kNormPieces>(l, blockIdx.x, t, (reinterpret_cast<uintptr_t>(l.in[t]) & 15) == 0);
+    constexpr int kBatch = 8;
     double s = 0.0;
-    int64_t done = i0;
-    if ((reinterpret_cast<uintptr_t>(l.in[t]) & 15) == 0) {
-        s = f32 ? run_squares<F32>(l.in[t], l.n[t], i0, i1) : run_squares<Bf16>(l.in[t], l.n[t], i0, i1);
-        done = i1 / 8 * 8;
-        if (done < i0) done = i0;
+#pragma unroll
+    for (int b = 0; b < kNormPieces; b += kBatch) {
+        u32x4 v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t p = r.p0 + (b + u) * kThreads + threadIdx.x;
+            v[u] = p < r.p1 ? static_cast<const u32x4*>(l.in[t])[p] : u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) s += squares(v[u], r.f32);
     }
-    for (int64_t i = done + threadIdx.x; i < i1; i += kThreads) {
-        const double v = element(l.in[t], f32, i);
-        s += v * v;
+    for (int64_t i = r.rest + threadIdx.x; i < r.i1; i += kThreads) {
+        const double x = element(l.in[t], r.f32, i);
+        s += x * x;
     }
     s = block_sum(s, lds);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
@@ -95,56 +137,49 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormList l, double* part
 __global__ __launch_bounds__(1024) void norm_sum_kernel(const double* part, int64_t n, float* norm) {
     __shared__ double lds[16];
     double s = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) s += part[i];
+    for (int64_t i = threadIdx.x; i < n; i += 8 * 1024) {
+        double v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = i + u * 1024 < n ? part[i + u * 1024] : 0.0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += v[u];
+    }
     s = block_sum(s, lds);
     if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(s));
-}
-
-template <class T>
-__device__ inline void run_scale(const void* in, void* out, int64_t i0, int64_t i1, float coef) {
-    const int64_t p1 = i1 / 8;
-#pragma unroll 4
-    for (int64_t p = i0 / 8 + threadIdx.x; p < p1; p += kThreads) {
-        Piece<T> v;
-        v.load(in, p);
-        float f[8];
-        v.to(f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= coef;
-        v.from(f);
-        v.store(out, p);
-    }
 }
 
 __global__ __launch_bounds__(kThreads) void clip_kernel(NormList l, const float* norm, float max_norm) {
     const float c = max_norm / (*norm + 1e-6f);
     const float coef = c > 1.0f ? 1.0f : c;  // NaN stays NaN
-    const int t = tensor_of(l, blockIdx.x);
+    const uint32_t block = gridDim.x - 1 - blockIdx.x;
+    const int t = tensor_of(l, block);
     if (coef == 1.0f && l.in[t] == l.out[t]) return;  // in place and nothing to clip
-    const bool f32 = (l.f32[t >> 5] >> (t & 31)) & 1;
-    const int64_t run = kRunBytes / (f32 ? 4 : 2);
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x - l.first[t]) * run;
-    const int64_t i1 = min(i0 + run, l.n[t]);
-    int64_t done = i0;
-    if (((reinterpret_cast<uintptr_t>(l.in[t]) | reinterpret_cast<uintptr_t>(l.out[t])) & 15) == 0) {
-        if (f32) run_scale<F32>(l.in[t], l.out[t], i0, i1, coef);
-        else run_scale<Bf16>(l.in[t], l.out[t], i0, i1, coef);
-        done = i1 / 8 * 8;
-        if (done < i0) done = i0;
+    const Run r = run_of<kClipPieces>(l, block, t,
+                               ((reinterpret_cast<uintptr_t>(l.in[t]) | reinterpret_cast<uintptr_t>(l.out[t])) & 15) == 0);
+    u32x4 v[kClipPieces];
+#pragma unroll
+    for (int u = 0; u < kClipPieces; ++u) {
+        const int64_t p = r.p0 + u * kThreads + threadIdx.x;
+        if (p < r.p1) v[u] = static_cast<const u32x4*>(l.in[t])[p];
     }
-    for (int64_t i = done + threadIdx.x; i < i1; i += kThreads) {
-        const float v = element(l.in[t], f32, i) * coef;
-        if (f32) {
-            static_cast<float*>(l.out[t])[i] = v;
+#pragma unroll
+    for (int u = 0; u < kClipPieces; ++u) {
+        const int64_t p = r.p0 + u * kThreads + threadIdx.x;
+        if (p < r.p1) __builtin_nontemporal_store(scaled(v[u], r.f32, coef), static_cast<u32x4*>(l.out[t]) + p);
+    }
+    for (int64_t i = r.rest + threadIdx.x; i < r.i1; i += kThreads) {
+        const float x = element(l.in[t], r.f32, i) * coef;
+        if (r.f32) {
+            static_cast<float*>(l.out[t])[i] = x;
         } else {
-            const __bf16 b = static_cast<__bf16>(v);
+            const __bf16 b = static_cast<__bf16>(x);
             static_cast<uint16_t*>(l.out[t])[i] = __builtin_bit_cast(uint16_t, b);
         }
     }
 }
 
-int64_t runs_of(int64_t n, int32_t dtype) {
-    const int64_t run = kRunBytes / (dtype == ENGRAM_F32 ? 4 : 2);
+int64_t runs_of(int64_t n, int32_t dtype, int pieces) {
+    const int64_t run = static_cast<int64_t>(pieces) * kThreads * (dtype == ENGRAM_F32 ? 4 : 8);
     return (n + run - 1) / run;
 }
 
@@ -166,7 +201,7 @@ int check_list(const char* what, int32_t tensors, const void* const* in, const i
 // The tensors in lists of kTensors, each with its workgroups; `launch(list, blocks, runs before)`.
 template <class F>
 void for_lists(int32_t tensors, const void* const* in, void* const* out, const int64_t* n, const int32_t* dtype,
-               F&& launch) {
+               int pieces, F&& launch) {
     NormList l = {};
     int64_t blocks = 0, before = 0;
     auto flush = [&]() {
@@ -177,7 +212,7 @@ void for_lists(int32_t tensors, const void* const* in, void* const* out, const i
     };
     for (int i = 0; i < tensors; ++i) {
         if (n[i] == 0) continue;
-        const int64_t r = runs_of(n[i], dtype[i]);
+        const int64_t r = runs_of(n[i], dtype[i], pieces);
         if (l.tensors == kTensors || blocks + r > 0x7FFFFFFF) flush();
         const int at = l.tensors++;
         l.in[at] = in[i];
@@ -200,7 +235,7 @@ extern "C" int64_t engram_grad_norm_workspace_bytes(int32_t tensors, const int64
     int64_t runs = 0;
     for (int i = 0; i < tensors; ++i) {
         if (!known_dtype(dtype[i]) || n[i] < 0 || n[i] > (1ll << 40)) return -1;
-        runs += runs_of(n[i], dtype[i]);
+        runs += runs_of(n[i], dtype[i], kNormPieces);
     }
     return runs * 8;
 }
@@ -219,7 +254,7 @@ extern "C" int engram_grad_norm(int32_t tensors, const void* const* grads, const
                     (long long)need);
     hipStream_t s = as_stream(stream);
     double* part = static_cast<double*>(workspace);
-    for_lists(tensors, grads, nullptr, n, dtype, [&](const NormList& l, unsigned blocks, int64_t before) {
+    for_lists(tensors, grads, nullptr, n, dtype, kNormPieces, [&](const NormList& l, unsigned blocks, int64_t before) {
         hipLaunchKernelGGL(norm_kernel, dim3(blocks), dim3(kThreads), 0, s, l, part + before);
     });
     hipLaunchKernelGGL(norm_sum_kernel, dim3(1), dim3(1024), 0, s, part, need / 8, norm);
@@ -242,7 +277,7 @@ extern "C" int engram_clip_grads(int32_t tensors, const void* const* grads, void
             return fail(ENGRAM_EINVAL, "%s: output %d: misaligned pointer", what, i);
     }
     hipStream_t s = as_stream(stream);
-    for_lists(tensors, grads, out, n, dtype, [&](const NormList& l, unsigned blocks, int64_t) {
+    for_lists(tensors, grads, out, n, dtype, kClipPieces, [&](const NormList& l, unsigned blocks, int64_t) {
         hipLaunchKernelGGL(clip_kernel, dim3(blocks), dim3(kThreads), 0, s, l, norm, max_norm);
     });
     return check_launch(what);

@@ -232,8 +232,9 @@ def test_embed_grad_refusals(gpu_device):
         g.engram_embed_grad(ids, up, 4, layer=0)
     with pytest.raises(TypeError):
         g.engram_embed_grad(ids, up.half(), 4)
-    with pytest.raises(g.EngramError) as e:
-        g.engram_embed_grad(ids, up, 4, workspace=torch.zeros(16, dtype=torch.uint8, device=gpu_device))
+    with pytest.raises(g.EngramError) as e:  # (the first sizes need none)
+        g.engram_embed_grad(ids.repeat(300), up.repeat(300, 1), 4,
+                            workspace=torch.zeros(16, dtype=torch.uint8, device=gpu_device))
     assert e.value.status == g.ENGRAM_ERANGE
     with pytest.raises(ValueError):
         g.engram_embed_grad_rows(ids, up, 4, rows=torch.zeros((5, 16), device=gpu_device))

@@ -74,11 +74,11 @@ def test_embed_validation(args, status, msg):
     (dict(D=12), 1, "multiple of 8"), (dict(T=-1), 1, "T < 0"), (dict(C=0), 1, "C=0"), (dict(C=1025, stride=1025), 1, "C=1025"),
     (dict(stride=5), 1, "stride"), (dict(T=1 << 28), 1, "2^30"), (dict(R=0), 1, "R=0"), (dict(R=1 << 31), 1, "R="),
     (dict(id_bytes=3), 1, "id_bytes"), (dict(gd=7), 1, "dtype"), (dict(od=2), 1, "dtype"), (dict(ids=None), 1, "null"),
-    (dict(up=None), 1, "null"), (dict(out=None), 1, "null"), (dict(ws=None), 1, "null"), (dict(up=ODD), 1, "misaligned"),
+    (dict(up=None), 1, "null"), (dict(out=None), 1, "null"), (dict(ws=None), 1, "workspace"), (dict(up=ODD), 1, "misaligned"),
     (dict(out=ODD), 1, "misaligned"), (dict(ws=ODD), 1, "misaligned"), (dict(wn=100), 2, "workspace"),
 ])
 def test_embed_grad_validation(args, status, msg, rows_form):
-    a = dict(ids=FAKE, id_bytes=8, T=100, stride=6, C=6, up=FAKE, gd=0, R=1000, D=64, out=FAKE, od=1, ws=FAKE, wn=1 << 30)
+    a = dict(ids=FAKE, id_bytes=8, T=1000, stride=6, C=6, up=FAKE, gd=0, R=1000, D=64, out=FAKE, od=1, ws=FAKE, wn=1 << 30)
     a.update(args)
     head = (a["ids"], a["id_bytes"], a["T"], a["stride"], a["C"], a["up"], a["gd"], a["R"], 0, a["D"], 1.0)
     if rows_form:

@@ -38,6 +38,7 @@ HIPCC_FLAGS = [
 FILE_FLAGS = {
     "wkv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "wkv16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "wkv_grad.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

@@ -14,6 +14,8 @@
 // A workgroup (eight waves) makes a 256 x 256 tile of the output, 128 x 64 per wave, from slabs of 64 of the reduced
 // axis in two stages of LDS filled by direct-to-LDS loads.  Where the tiles are fewer than the CUs the reduced axis is
 // split over workgroups, whose fp32 partial tiles a second launch adds in order.  da and dW of a call are one launch.
+#include <type_traits>
+
 #include "rows.h"
 
 namespace engram {
@@ -28,7 +30,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr int BM = 256, BN = 256, BK = 64;
 constexpr int kThreads = 512;
 constexpr int kOpBytes = 256 * 128;  // one operand's slab: 32 KB
-constexpr int kStageBytes = 2 * kOpBytes;
+constexpr int kStageBytes = 2 * kOpBytes;  // an operand's two stages
+constexpr int kXcds = 8;
+constexpr int kBar = 14;  // the slab barrier precedes unit kBar of a slab's second k-step
 constexpr int kCUs = 256;
 constexpr int kBufferWord3 = 0x00020000;
 constexpr int kWaitVm0 = 0x0F70;
@@ -58,15 +62,29 @@ __device__ inline uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// The transposing LDS read.  Its argument is `restrict`, and so is the read marked apart from other memory: without that
+// the compiler takes it for a possible reader of every direct-to-LDS load before it and waits for all of them (ordinary LDS
+// reads it does not).  What orders the reads after the loads they need is the slab's own wait and barrier.
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+__device__ __forceinline__ s16x4 read_transposed(lds_s16x4 __restrict__ p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+}
+
+// pid of n tiles onto an order in which each XCD (workgroups pid % 8) takes a contiguous run
+__device__ inline int64_t xcd_order(int64_t pid, int64_t n) {
+    const int64_t xcd = pid % kXcds, per = n / kXcds, rem = n % kXcds;
+    return xcd * per + min(xcd, rem) + pid / kXcds;
+}
+
 template <bool kRowsP>  // P's slab holds rows of the reduced axis (dW), else rows of the output (da)
 __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* lds) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave & 1, wn = wave >> 1;
-    const int tn = static_cast<int>(unit % g.tiles_n);
-    const int64_t rest = unit / g.tiles_n;
-    const int tm = static_cast<int>(rest % g.tiles_m);
-    const int split = static_cast<int>(rest / g.tiles_m);
+    const int tiles = g.tiles_m * g.tiles_n;
+    const int split = static_cast<int>(unit / tiles);
+    const int tile = static_cast<int>(xcd_order(unit - static_cast<int64_t>(split) * tiles, tiles));
+    const int tm = tile / g.tiles_n, tn = tile - tm * g.tiles_n;
     const int64_t m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
     const int s0 = static_cast<int>(static_cast<int64_t>(g.slabs) * split / g.splits);
     const int s1 = static_cast<int>(static_cast<int64_t>(g.slabs) * (split + 1) / g.splits);
@@ -78,88 +96,164 @@ __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* ld
         asm volatile("" ::: "memory");
     };
 
-    // ---- slab loads: every wave 4 KB of each operand, 1 KB per instruction.  A slab of reduced rows: two rows of
-    // 512 bytes per instruction; a slab of output rows: eight rows of 128 bytes, 16-byte pieces swizzled by row / 2.
-    const uint32_t t_row = wave * 8 + (lane >> 5);  // + 2 q
-    auto t_voff = [&](int q, int64_t ld) {
-        const uint32_t k = t_row + 2 * q;
-        const uint32_t f = (k & 3) | (((k >> 3) & 3) << 2);
-        return k * static_cast<uint32_t>(ld * 2) + (((lane & 31) ^ (f << 1)) << 4);
+    // ---- slab loads, by waves 0-3: 8 KB of each operand per wave, 1 KB per instruction.  A slab of reduced rows: two
+    // rows of 512 bytes per instruction, lane l the piece that belongs at slot l % 32 of row 2 q + l / 32 of the wave's
+    // 16; a slab of output rows: eight rows of 128 bytes, lane l at slot l % 8 of row 8 q + l / 8 of the wave's 64,
+    // 16-byte pieces swizzled by row / 2.  Rows past the reduced axis or past M lie outside the resource and read as
+    // zero (the row term sits in the range-checked offset); columns past M or N read a neighbour's elements, which only
+    // reach outputs that are not stored.
+    const uint32_t t_row = (wave & 3) * 16 + (lane >> 5);
+    const uint32_t t_piece = (lane & 31) ^ (2 * (lane >> 5)) ^ (16 * (wave & 1));
+    const uint32_t ldp = static_cast<uint32_t>((kRowsP ? g.M : g.R) * 2), ldq = static_cast<uint32_t>(g.N * 2);
+    const uint32_t p_row = kRowsP ? t_row * ldp : ((wave & 3) * 64 + (lane >> 3)) * ldp;
+    const uint32_t p_piece = (lane & 7) ^ (lane >> 4);
+    const uint32_t q_row = t_row * ldq;
+    struct Slab {
+        __amdgpu_buffer_rsrc_t p, q;
+        int64_t r0;  // first reduced index
+        int left;    // how many the slab has
     };
-    auto t_rsrc = [&](const uint16_t* base, int64_t ld, int64_t c0, int64_t r0) {
-        const int64_t rows = min<int64_t>(BK, g.R - r0);
-        const int64_t bytes = rows > 0 ? rows * ld * 2 - c0 * 2 : 0;
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (rows > 0 ? r0 * ld + c0 : 0)), 0,
-                                                 static_cast<int>(bytes), kBufferWord3);
-    };
-    auto issue = [&](int slab, int stage) {
-        uint8_t* st = lds + stage * kStageBytes;
-        const int64_t r0 = static_cast<int64_t>(slab) * BK;
+    auto slab_of = [&](int s) {  // s past the unit's last: empty resources
+        Slab b;
+        b.r0 = static_cast<int64_t>(s) * BK;
+        const int64_t rows = s < s1 ? min<int64_t>(BK, g.R - b.r0) : 0;
+        const int64_t at = rows > 0 ? b.r0 : 0;
+        b.left = static_cast<int>(rows);
+        b.q = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(g.q + at * g.N + n0), 0,
+                                                rows > 0 ? static_cast<int>(rows * g.N * 2 - n0 * 2) : 0, kBufferWord3);
         if constexpr (kRowsP) {
-            const auto rp = t_rsrc(g.p, g.M, m0, r0);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, st + (wave * 8 + 2 * q) * 512, 16, t_voff(q, g.M), 0, 0, 0);
+            b.p = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(g.p + at * g.M + m0), 0,
+                                                    rows > 0 ? static_cast<int>(rows * g.M * 2 - m0 * 2) : 0, kBufferWord3);
         } else {
-            const int64_t rows = min<int64_t>(BM, g.M - m0);
-            const auto rp = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(g.p + m0 * g.R), 0,
-                                                              static_cast<int>(rows * g.R * 2), kBufferWord3);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t row = wave * 32 + 8 * q + (lane >> 3);
-                const uint32_t piece = (lane & 7) ^ ((row >> 1) & 7);
-                const uint32_t voff = r0 + 8 * piece < g.R ? row * static_cast<uint32_t>(g.R * 2) + (piece << 4) : kOutside;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, st + (wave * 32 + 8 * q) * 128, 16, voff,
-                                                         static_cast<int>(r0 * 2), 0, 0);
-            }
+            const int64_t outs = min<int64_t>(BM, g.M - m0);
+            b.p = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(g.p + m0 * g.R), 0,
+                                                    rows > 0 ? static_cast<int>(outs * g.R * 2) : 0, kBufferWord3);
         }
-        const auto rq = t_rsrc(g.q, g.N, n0, r0);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, st + kOpBytes + (wave * 8 + 2 * q) * 512, 16, t_voff(q, g.N), 0, 0,
-                                                     0);
+        return b;
+    };
+    // part q (0..7) of a slab into stage st; the offsets are formed here from four held values (opaque, so that they are
+    // not hoisted out of the slab loop as 16 registers)
+    auto issue_part = [&](const Slab& b, int st, int q) {
+        uint32_t tp = t_piece, pr = p_row, qr = q_row;
+        asm volatile("" : "+v"(tp), "+v"(pr), "+v"(qr));
+        const uint32_t piece = (tp ^ (4 * (q & 1)) ^ (8 * (q >> 2))) << 4;
+        uint8_t* to = lds + st * kOpBytes + ((wave & 3) * 16 + 2 * q) * 512;
+        if constexpr (kRowsP) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(b.p, to, 16, pr + 2 * q * ldp + piece, 0, 0, 0);
+        } else {
+            uint32_t pp = p_piece;
+            asm volatile("" : "+v"(pp));
+            const uint32_t pc = pp ^ (4 * (q & 1));
+            const uint32_t voff = static_cast<int>(pc) * 8 < b.left ? pr + 8 * q * ldp + (pc << 4) : kOutside;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(b.p, lds + st * kOpBytes + ((wave & 3) * 64 + 8 * q) * 128, 16, voff,
+                                                     static_cast<int>(b.r0 * 2), 0, 0);
+        }
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(b.q, to + kStageBytes, 16, qr + 2 * q * ldq + piece, 0, 0, 0);
     };
 
-    // ---- fragments of k-step s (32 of the slab's 64): lane l holds row or column l % 16, reduced 8 (l / 16) .. + 7
+    // ---- fragments of k-step s (32 of the slab's 64): lane l holds row or column l % 16, reduced 8 (l / 16) .. + 7.
+    // LDS: P's two stages, then Q's; k-step and half lie in the instruction's offset, the stage in the address.
     const uint32_t t_lane = (8 * (lane >> 4) + ((lane >> 2) & 3)) * 512 + (lane & 3) * 8 + ((lane >> 2) << 5);
-    const uint32_t r_lane = (lane & 15) * 128 + (((lane >> 4) ^ ((lane >> 1) & 7)) << 4);
-    auto read_t = [&](const uint8_t* op, int s, int block) {
-        typedef __attribute__((address_space(3))) s16x4* lds4;
-        const uint8_t* at = op + s * 32 * 512 + (t_lane ^ (block << 5));
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + 4 * 512));
+    const uint32_t r_lane = (wm * 128 + (lane & 15)) * 128 + (((lane >> 4) ^ ((lane >> 1) & 7)) << 4);
+    uint32_t p_at[kRowsP ? 8 : 2], q_at[4];
+    if constexpr (kRowsP) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p_at[i] = t_lane ^ ((wm * 8 + i) << 5);
+    } else {
+        p_at[0] = r_lane;
+        p_at[1] = r_lane ^ 64;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q_at[j] = kStageBytes + (t_lane ^ ((wn * 4 + j) << 5));
+    // opaque: one register each, the rest of an address in the instruction's 16-bit offset
+#pragma unroll
+    for (uint32_t& a : p_at) asm volatile("" : "+v"(a));
+#pragma unroll
+    for (uint32_t& a : q_at) asm volatile("" : "+v"(a));
+    auto read_t = [&](uint32_t at) {
         typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const s16x4 lo = read_transposed((lds_s16x4)(lds + at));
+        const s16x4 hi = read_transposed((lds_s16x4)(lds + at + 4 * 512));
         const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         return __builtin_bit_cast(bf16x8, v);
     };
-    auto read_p = [&](int stage, int s, int i) -> bf16x8 {
-        const uint8_t* op = lds + stage * kStageBytes;
-        if constexpr (kRowsP) return read_t(op, s, wm * 8 + i);
-        else return *reinterpret_cast<const bf16x8*>(op + (wm * 128 + 16 * i) * 128 + (r_lane ^ (s << 6)));
+    auto read_p = [&](int s, int i) -> bf16x8 {
+        if constexpr (kRowsP) return read_t(p_at[i] + s * 32 * 512);
+        else return *reinterpret_cast<const bf16x8*>(lds + p_at[s] + i * 16 * 128);
     };
-    auto read_q = [&](int stage, int s, int j) { return read_t(lds + stage * kStageBytes + kOpBytes, s, wn * 4 + j); };
+    auto read_q = [&](int s, int j) { return read_t(q_at[j] + s * 32 * 512); };
+    auto other_stage = [&]() {
+#pragma unroll
+        for (uint32_t& a : p_at) {
+            a ^= kOpBytes;
+            asm volatile("" : "+v"(a));
+        }
+#pragma unroll
+        for (uint32_t& a : q_at) {
+            a ^= kOpBytes;
+            asm volatile("" : "+v"(a));
+        }
+    };
 
     f32x4 acc[8][4] = {};
-    if (s0 < s1) issue(s0, 0);
-    for (int kt = s0; kt < s1; ++kt) {
-        const int stage = (kt - s0) & 1;
-        __builtin_amdgcn_s_waitcnt(kWaitVm0);
-        sync();  // the slab has landed, and everyone is done with the other stage
-        if (kt + 1 < s1) issue(kt + 1, stage ^ 1);
+    bf16x8 fp[8], fq[4];
+    // One k-step: two halves, Q's fragments 0-1 then 2-3, each walking P's eight; a fragment is read again, for k-step
+    // ns, right after its last use, fifteen or more MFMAs before its next.  Each MFMA with its reads and
+    // `extra(u)` (u = 0..31) is one scheduling unit.
+    auto kstep = [&](int ns, auto&& extra) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            bf16x8 fp[8], fq[4];
+        for (int jj = 0; jj < 2; ++jj) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) fq[j] = read_q(stage, s, j);
+            for (int i = 0; i < 8; ++i) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) fp[i] = read_p(stage, s, i);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int jb = 0; jb < 2; ++jb) {
+                    const int j = 2 * jj + jb;
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fp[i], acc[i][j], 0, 0, 0);
+                    if (j == 3) fp[i] = read_p(ns, i);
+                    if (i == 7) fq[j] = read_q(ns, j);
+                    extra(16 * jj + 2 * i + jb);
+                    asm volatile("" ::: "memory");
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
         }
-    }
+    };
+    auto run = [&](auto loader_tag) {
+        constexpr bool kLoader = decltype(loader_tag)::value;
+        if (kLoader) {
+            const Slab a = slab_of(s0), b = slab_of(s0 + 1);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) issue_part(a, 0, q);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) issue_part(b, 1, q);
+            __builtin_amdgcn_s_waitcnt(kWaitVm0);
+        }
+        sync();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fp[i] = read_p(0, i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fq[j] = read_q(0, j);
+        // A slab: k-step 0, then k-step 1 with the slab barrier before its first LDS read (unit kBar): past it the next
+        // slab has landed and nobody reads this stage any more, so the slab after the next goes into it.
+        int st = 0;
+        for (int kt = s0; kt < s1; ++kt) {
+            kstep(1, [](int) {});
+            other_stage();
+            Slab b;
+            if (kLoader) b = slab_of(kt + 2);
+            kstep(0, [&](int u) {
+                if (u == kBar - 1) {
+                    if (kLoader) __builtin_amdgcn_s_waitcnt(kWaitVm0);
+                    sync();
+                }
+                if (kLoader && u >= kBar && (u - kBar) % 2 == 0 && (u - kBar) / 2 < 8) issue_part(b, st, (u - kBar) / 2);
+            });
+            st ^= 1;
+        }
+        if (kLoader) __builtin_amdgcn_s_waitcnt(kWaitVm0);  // empty loads still write LDS
+    };
+    if (wave < 4) run(std::true_type{});
+    else run(std::false_type{});
 
     // ---- lane l holds, per block, output row l % 16 and the columns 4 (l / 16) .. + 3
     const int64_t mrow = m0 + wm * 128 + (lane & 15), ncol = n0 + wn * 64 + 4 * (lane >> 4);

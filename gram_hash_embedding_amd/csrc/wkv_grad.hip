@@ -27,12 +27,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int BM = 256, BN = 256, BK = 64;
-constexpr int kThreads = 512;
-constexpr int kOpBytes = 256 * 128;  // one operand's slab: 32 KB
-constexpr int kStageBytes = 2 * kOpBytes;  // an operand's two stages
+constexpr int BK = 64;  // the reduced axis per slab
 constexpr int kXcds = 8;
-constexpr int kBar = 14;  // the slab barrier precedes unit kBar of a slab's second k-step
 constexpr int kCUs = 256;
 constexpr int kBufferWord3 = 0x00020000;
 constexpr int kWaitVm0 = 0x0F70;
@@ -76,8 +72,18 @@ __device__ inline int64_t xcd_order(int64_t pid, int64_t n) {
     return xcd * per + min(xcd, rem) + pid / kXcds;
 }
 
-template <bool kRowsP>  // P's slab holds rows of the reduced axis (dW), else rows of the output (da)
+// TS: the tile's rows and columns (256: eight waves of 128 x 64; 128: four of 64 x 64).  kRowsP: P's slab holds rows of
+// the reduced axis (dW), else rows of the output (da).
+template <int TS, bool kRowsP>
 __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* lds) {
+    constexpr int kOpBytes = TS * BK * 2;          // one operand's slab
+    constexpr int kStageBytes = 2 * kOpBytes;      // an operand's two stages
+    constexpr int PB = TS / 32;                    // blocks of 16 rows per wave (and 4 of 16 columns)
+    constexpr int kRow = TS * 2;                   // bytes of a reduced row in LDS
+    constexpr int kPieces = TS / 8;                // its 16-byte pieces
+    constexpr int kPerLoad = 1024 / kRow;          // reduced rows per load instruction
+    constexpr int kParts = 16 / kPerLoad;          // parts of a slab's loads, each one instruction per operand
+    constexpr int kBar = 2 * (PB - 1);             // the slab barrier precedes unit kBar of a slab's second k-step
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave & 1, wn = wave >> 1;
@@ -85,7 +91,7 @@ __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* ld
     const int split = static_cast<int>(unit / tiles);
     const int tile = static_cast<int>(xcd_order(unit - static_cast<int64_t>(split) * tiles, tiles));
     const int tm = tile / g.tiles_n, tn = tile - tm * g.tiles_n;
-    const int64_t m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
+    const int64_t m0 = static_cast<int64_t>(tm) * TS, n0 = static_cast<int64_t>(tn) * TS;
     const int s0 = static_cast<int>(static_cast<int64_t>(g.slabs) * split / g.splits);
     const int s1 = static_cast<int>(static_cast<int64_t>(g.slabs) * (split + 1) / g.splits);
 
@@ -96,16 +102,17 @@ __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* ld
         asm volatile("" ::: "memory");
     };
 
-    // ---- slab loads, by waves 0-3: 8 KB of each operand per wave, 1 KB per instruction.  A slab of reduced rows: two
-    // rows of 512 bytes per instruction, lane l the piece that belongs at slot l % 32 of row 2 q + l / 32 of the wave's
-    // 16; a slab of output rows: eight rows of 128 bytes, lane l at slot l % 8 of row 8 q + l / 8 of the wave's 64,
-    // 16-byte pieces swizzled by row / 2.  Rows past the reduced axis or past M lie outside the resource and read as
-    // zero (the row term sits in the range-checked offset); columns past M or N read a neighbour's elements, which only
-    // reach outputs that are not stored.
-    const uint32_t t_row = (wave & 3) * 16 + (lane >> 5);
-    const uint32_t t_piece = (lane & 31) ^ (2 * (lane >> 5)) ^ (16 * (wave & 1));
+    // ---- slab loads, by waves 0-3: a quarter of each operand per wave, 1 KB per instruction.  A slab of reduced rows:
+    // kPerLoad rows per instruction, each lane the piece that belongs at its place under the swizzle (block b of row k at
+    // b XOR (k % 4 + 4 ((k / 8) % (TS / 64))): the rows that half a wave's read touches lie in different blocks); a slab of
+    // output rows: eight rows of 128 bytes, lane l at slot l % 8 of row 8 q + l / 8, 16-byte pieces swizzled by row / 2.
+    // Rows past the reduced axis or past M lie outside the resource and read as zero (the row term sits in the
+    // range-checked offset); columns past M or N read a neighbour's elements, which only reach outputs that are not stored.
+    const uint32_t l_row = lane / kPieces;
+    const uint32_t t_row = (wave & 3) * 16 + l_row;
+    const uint32_t t_piece = (lane % kPieces) ^ (2 * l_row) ^ (TS == 256 ? 16 * (wave & 1) : 0);
     const uint32_t ldp = static_cast<uint32_t>((kRowsP ? g.M : g.R) * 2), ldq = static_cast<uint32_t>(g.N * 2);
-    const uint32_t p_row = kRowsP ? t_row * ldp : ((wave & 3) * 64 + (lane >> 3)) * ldp;
+    const uint32_t p_row = kRowsP ? t_row * ldp : ((wave & 3) * (TS / 4) + (lane >> 3)) * ldp;
     const uint32_t p_piece = (lane & 7) ^ (lane >> 4);
     const uint32_t q_row = t_row * ldq;
     struct Slab {
@@ -125,40 +132,42 @@ __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* ld
             b.p = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(g.p + at * g.M + m0), 0,
                                                     rows > 0 ? static_cast<int>(rows * g.M * 2 - m0 * 2) : 0, kBufferWord3);
         } else {
-            const int64_t outs = min<int64_t>(BM, g.M - m0);
+            const int64_t outs = min<int64_t>(TS, g.M - m0);
             b.p = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(g.p + m0 * g.R), 0,
                                                     rows > 0 ? static_cast<int>(outs * g.R * 2) : 0, kBufferWord3);
         }
         return b;
     };
-    // part q (0..7) of a slab into stage st; the offsets are formed here from four held values (opaque, so that they are
+    // part q of a slab into stage st; the offsets are formed here from four held values (opaque, so that they are
     // not hoisted out of the slab loop as 16 registers)
     auto issue_part = [&](const Slab& b, int st, int q) {
         uint32_t tp = t_piece, pr = p_row, qr = q_row;
         asm volatile("" : "+v"(tp), "+v"(pr), "+v"(qr));
-        const uint32_t piece = (tp ^ (4 * (q & 1)) ^ (8 * (q >> 2))) << 4;
-        uint8_t* to = lds + st * kOpBytes + ((wave & 3) * 16 + 2 * q) * 512;
+        const uint32_t piece = (TS == 256 ? tp ^ (4 * (q & 1)) ^ (8 * (q >> 2)) : tp ^ (8 * (q >> 1))) << 4;
+        uint8_t* to = lds + st * kOpBytes + ((wave & 3) * 16 + kPerLoad * q) * kRow;
         if constexpr (kRowsP) {
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(b.p, to, 16, pr + 2 * q * ldp + piece, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(b.p, to, 16, pr + kPerLoad * q * ldp + piece, 0, 0, 0);
         } else {
             uint32_t pp = p_piece;
             asm volatile("" : "+v"(pp));
             const uint32_t pc = pp ^ (4 * (q & 1));
             const uint32_t voff = static_cast<int>(pc) * 8 < b.left ? pr + 8 * q * ldp + (pc << 4) : kOutside;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(b.p, lds + st * kOpBytes + ((wave & 3) * 64 + 8 * q) * 128, 16, voff,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(b.p, lds + st * kOpBytes + ((wave & 3) * (TS / 4) + 8 * q) * 128, 16,
+                                                     voff,
                                                      static_cast<int>(b.r0 * 2), 0, 0);
         }
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(b.q, to + kStageBytes, 16, qr + 2 * q * ldq + piece, 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(b.q, to + kStageBytes, 16, qr + kPerLoad * q * ldq + piece, 0, 0, 0);
     };
 
     // ---- fragments of k-step s (32 of the slab's 64): lane l holds row or column l % 16, reduced 8 (l / 16) .. + 7.
     // LDS: P's two stages, then Q's; k-step and half lie in the instruction's offset, the stage in the address.
-    const uint32_t t_lane = (8 * (lane >> 4) + ((lane >> 2) & 3)) * 512 + (lane & 3) * 8 + ((lane >> 2) << 5);
-    const uint32_t r_lane = (wm * 128 + (lane & 15)) * 128 + (((lane >> 4) ^ ((lane >> 1) & 7)) << 4);
-    uint32_t p_at[kRowsP ? 8 : 2], q_at[4];
+    const uint32_t t_lane =
+        (8 * (lane >> 4) + ((lane >> 2) & 3)) * kRow + (lane & 3) * 8 + (((lane >> 2) & (TS / 16 - 1)) << 5);
+    const uint32_t r_lane = (wm * (TS / 2) + (lane & 15)) * 128 + (((lane >> 4) ^ ((lane >> 1) & 7)) << 4);
+    uint32_t p_at[kRowsP ? PB : 2], q_at[4];
     if constexpr (kRowsP) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p_at[i] = t_lane ^ ((wm * 8 + i) << 5);
+        for (int i = 0; i < PB; ++i) p_at[i] = t_lane ^ ((wm * PB + i) << 5);
     } else {
         p_at[0] = r_lane;
         p_at[1] = r_lane ^ 64;
@@ -173,15 +182,15 @@ __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* ld
     auto read_t = [&](uint32_t at) {
         typedef short s16x8 __attribute__((ext_vector_type(8)));
         const s16x4 lo = read_transposed((lds_s16x4)(lds + at));
-        const s16x4 hi = read_transposed((lds_s16x4)(lds + at + 4 * 512));
+        const s16x4 hi = read_transposed((lds_s16x4)(lds + at + 4 * kRow));
         const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         return __builtin_bit_cast(bf16x8, v);
     };
     auto read_p = [&](int s, int i) -> bf16x8 {
-        if constexpr (kRowsP) return read_t(p_at[i] + s * 32 * 512);
+        if constexpr (kRowsP) return read_t(p_at[i] + s * 32 * kRow);
         else return *reinterpret_cast<const bf16x8*>(lds + p_at[s] + i * 16 * 128);
     };
-    auto read_q = [&](int s, int j) { return read_t(q_at[j] + s * 32 * 512); };
+    auto read_q = [&](int s, int j) { return read_t(q_at[j] + s * 32 * kRow); };
     auto other_stage = [&]() {
 #pragma unroll
         for (uint32_t& a : p_at) {
@@ -195,23 +204,23 @@ __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* ld
         }
     };
 
-    f32x4 acc[8][4] = {};
-    bf16x8 fp[8], fq[4];
-    // One k-step: two halves, Q's fragments 0-1 then 2-3, each walking P's eight; a fragment is read again, for k-step
-    // ns, right after its last use, fifteen or more MFMAs before its next.  Each MFMA with its reads and
-    // `extra(u)` (u = 0..31) is one scheduling unit.
+    f32x4 acc[PB][4] = {};
+    bf16x8 fp[PB], fq[4];
+    // One k-step: two halves, Q's fragments 0-1 then 2-3, each walking P's; a fragment is read again, for k-step
+    // ns, right after its last use, at least 2 PB - 1 MFMAs before its next.  Each MFMA with its reads and
+    // `extra(u)` (u = 0 .. 4 PB - 1) is one scheduling unit.
     auto kstep = [&](int ns, auto&& extra) {
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < PB; ++i) {
 #pragma unroll
                 for (int jb = 0; jb < 2; ++jb) {
                     const int j = 2 * jj + jb;
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fp[i], acc[i][j], 0, 0, 0);
                     if (j == 3) fp[i] = read_p(ns, i);
-                    if (i == 7) fq[j] = read_q(ns, j);
-                    extra(16 * jj + 2 * i + jb);
+                    if (i == PB - 1) fq[j] = read_q(ns, j);
+                    extra(2 * PB * jj + 2 * i + jb);
                     asm volatile("" ::: "memory");
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -223,14 +232,14 @@ __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* ld
         if (kLoader) {
             const Slab a = slab_of(s0), b = slab_of(s0 + 1);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) issue_part(a, 0, q);
+            for (int q = 0; q < kParts; ++q) issue_part(a, 0, q);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) issue_part(b, 1, q);
+            for (int q = 0; q < kParts; ++q) issue_part(b, 1, q);
             __builtin_amdgcn_s_waitcnt(kWaitVm0);
         }
         sync();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) fp[i] = read_p(0, i);
+        for (int i = 0; i < PB; ++i) fp[i] = read_p(0, i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) fq[j] = read_q(0, j);
         // A slab: k-step 0, then k-step 1 with the slab barrier before its first LDS read (unit kBar): past it the next
@@ -246,19 +255,19 @@ __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* ld
                     if (kLoader) __builtin_amdgcn_s_waitcnt(kWaitVm0);
                     sync();
                 }
-                if (kLoader && u >= kBar && (u - kBar) % 2 == 0 && (u - kBar) / 2 < 8) issue_part(b, st, (u - kBar) / 2);
+                if (kLoader && u >= kBar && (u - kBar) % 2 == 0 && (u - kBar) / 2 < kParts) issue_part(b, st, (u - kBar) / 2);
             });
             st ^= 1;
         }
         if (kLoader) __builtin_amdgcn_s_waitcnt(kWaitVm0);  // empty loads still write LDS
     };
-    if (wave < 4) run(std::true_type{});
+    if (TS == 128 || wave < 4) run(std::true_type{});
     else run(std::false_type{});
 
     // ---- lane l holds, per block, output row l % 16 and the columns 4 (l / 16) .. + 3
-    const int64_t mrow = m0 + wm * 128 + (lane & 15), ncol = n0 + wn * 64 + 4 * (lane >> 4);
+    const int64_t mrow = m0 + wm * (TS / 2) + (lane & 15), ncol = n0 + wn * 64 + 4 * (lane >> 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < PB; ++i) {
         const int64_t m = mrow + 16 * i;
         if (m >= g.M) continue;
 #pragma unroll
@@ -286,13 +295,24 @@ __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* ld
     }
 }
 
-__global__ __launch_bounds__(kThreads, 1) void wkv_grad_kernel(GradArgs a) {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStageBytes];
+template <int TS>
+__device__ __forceinline__ void either(const GradArgs& a, uint8_t* lds) {
     const int64_t b = blockIdx.x;
     const bool first = b < a.first_units;
     const int64_t unit = first ? b : b - a.first_units;
-    if (first == (a.first_dw != 0)) product<true>(a.dw, unit, lds);
-    else product<false>(a.da, unit, lds);
+    if (first == (a.first_dw != 0)) product<TS, true>(a.dw, unit, lds);
+    else product<TS, false>(a.da, unit, lds);
+}
+
+__global__ __launch_bounds__(512, 1) void wkv_grad_kernel(GradArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * 256 * BK * 2];
+    either<256>(a, lds);
+}
+
+// two workgroups a CU: one's stores run under the other's loads
+__global__ __launch_bounds__(256, 2) void wkv_grad_small_kernel(GradArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * 128 * BK * 2];
+    either<128>(a, lds);
 }
 
 // The partial tiles of a split reduction, added in order: eight outputs per thread.
@@ -301,13 +321,19 @@ __global__ __launch_bounds__(256) void wkv_grad_join_kernel(const float* part, i
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= n8) return;
     float s[8] = {};
-    for (int k = 0; k < splits; ++k) {
-        Piece<F32> p;
-        float f[8];
-        p.load_nt(part, k * n8 + i);
-        p.to(f);
+    constexpr int kBatch = 8;
+    for (int k = 0; k < splits; k += kBatch) {
+        Piece<F32> p[kBatch];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] += f[e];
+        for (int b = 0; b < kBatch; ++b) p[b].load(part, min(k + b, splits - 1) * n8 + i);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (k + b >= splits) break;
+            float f[8];
+            p[b].to(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += f[e];
+        }
     }
     if (out_f32) {
         Piece<F32> o;
@@ -334,23 +360,30 @@ __global__ __launch_bounds__(256) void wkv_grad_join_kernel(const float* part, i
     }
 }
 
-int splits_of(int64_t tiles, int64_t slabs) {
-    if (tiles >= kCUs) return 1;
-    int64_t s = kCUs / tiles;
+int splits_of(int64_t tiles, int64_t slabs, int size) {
+    const int64_t room = size == 128 ? 2 * kCUs : kCUs;  // workgroups that run at once
+    if (tiles >= room) return 1;
+    int64_t s = room / tiles;
     if (s > slabs / 4) s = slabs / 4;
     return static_cast<int>(s < 1 ? 1 : s);
 }
 
-Prod prod_of(int64_t M, int64_t N, int64_t R) {
+Prod prod_of(int64_t M, int64_t N, int64_t R, int size) {
     Prod p = {};
     p.M = M;
     p.N = N;
     p.R = R;
-    p.tiles_m = static_cast<int>((M + BM - 1) / BM);
-    p.tiles_n = static_cast<int>((N + BN - 1) / BN);
+    p.tiles_m = static_cast<int>((M + size - 1) / size);
+    p.tiles_n = static_cast<int>((N + size - 1) / size);
     p.slabs = static_cast<int>((R + BK - 1) / BK);
-    p.splits = splits_of(static_cast<int64_t>(p.tiles_m) * p.tiles_n, p.slabs);
+    p.splits = splits_of(static_cast<int64_t>(p.tiles_m) * p.tiles_n, p.slabs, size);
     return p;
+}
+
+int tile_size(int64_t T, int32_t K, int32_t Nout) {
+    // 128 x 128 tiles for little work: more workgroups, and two of them a CU (251 x 1,536 x 25,600: 97 against 107 us; 512:
+    // 135 and 138; 768: 177 and 169; 2,805 x 456 x 7,864: 79 and 87)
+    return 2.0 * T * K * Nout < 5e10 ? 128 : 256;
 }
 
 int64_t part_bytes(const Prod& p) { return p.splits > 1 ? p.splits * p.M * p.N * 4 : 0; }
@@ -368,7 +401,8 @@ using namespace engram;
 extern "C" int64_t engram_wkv_backward_workspace_bytes(int64_t T, int32_t K, int32_t Nout) {
     if (!shape_ok(T, K, Nout)) return -1;
     if (T == 0) return 0;
-    return part_bytes(prod_of(T, K, Nout)) + part_bytes(prod_of(Nout, K, T));
+    const int size = tile_size(T, K, Nout);
+    return part_bytes(prod_of(T, K, Nout, size)) + part_bytes(prod_of(Nout, K, T, size));
 }
 
 extern "C" int engram_wkv_backward(const uint16_t* dkv, const uint16_t* a, const uint16_t* w, uint16_t* da, void* dw,
@@ -393,11 +427,12 @@ extern "C" int engram_wkv_backward(const uint16_t* dkv, const uint16_t* a, const
         if (!dw || accumulate) return ENGRAM_OK;
         return launch_zero(dw, static_cast<int64_t>(Nout) * K * (dw_dtype == ENGRAM_F32 ? 4 : 2), s, what);
     }
+    const int size = tile_size(T, K, Nout);
     GradArgs g = {};
     int64_t need = 0;
     float* part = static_cast<float*>(workspace);
     if (da) {
-        g.da = prod_of(T, K, Nout);
+        g.da = prod_of(T, K, Nout, size);
         g.da.p = dkv;
         g.da.q = w;
         g.da.out = da;
@@ -405,7 +440,7 @@ extern "C" int engram_wkv_backward(const uint16_t* dkv, const uint16_t* a, const
         need += part_bytes(g.da);
     }
     if (dw) {
-        g.dw = prod_of(Nout, K, T);
+        g.dw = prod_of(Nout, K, T, size);
         g.dw.p = dkv;
         g.dw.q = a;
         g.dw.out = dw;
@@ -425,7 +460,9 @@ extern "C" int engram_wkv_backward(const uint16_t* dkv, const uint16_t* a, const
     // the longer reductions first: the shorter ones fill in behind them
     g.first_dw = !da || (dw && g.dw.slabs / g.dw.splits > g.da.slabs / g.da.splits);
     g.first_units = g.first_dw ? u_dw : u_da;
-    hipLaunchKernelGGL(wkv_grad_kernel, dim3(static_cast<unsigned>(u_da + u_dw)), dim3(kThreads), 0, s, g);
+    const dim3 grid(static_cast<unsigned>(u_da + u_dw));
+    if (size == 128) hipLaunchKernelGGL(wkv_grad_small_kernel, grid, dim3(256), 0, s, g);
+    else hipLaunchKernelGGL(wkv_grad_kernel, grid, dim3(512), 0, s, g);
     for (const Prod* p : {&g.da, &g.dw}) {
         if (!p->out || p->splits <= 1) continue;
         const int64_t n8 = p->M * p->N / 8;

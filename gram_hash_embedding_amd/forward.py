@@ -11,16 +11,24 @@ projection and the gate pre-activation run as one entry point
 stored) and the output, if asked for, comes from engram_gate_residual.  This
 module only allocates outputs and workspace and calls the HIP entry points in
 that order.
+
+Training runs the same layers back: `EngramForward.backward` takes a layer's output gradient through the gate and the
+residual (engram_gate_output_backward), the projection (engram_wkv_backward) and the lookup (engram_embed_grad_rows) to
+the gradients of its stream, its weights and the table rows its ids reach; `clip_grads` clips a list of those and any
+other gradients by their common norm (engram_grad_norm, engram_clip_grads).
 """
 from __future__ import annotations
 
 import dataclasses
 from typing import List, Optional
 
-from . import (engram_gate_dot, engram_gate_output, engram_gate_residual, engram_gather_dequant,
-               engram_gather_dequant_packed, engram_gather_mx, engram_hash, engram_hash_gather_packed,
+from . import (engram_clip_grads, engram_embed_grad_rows, engram_embed_grad_workspace_bytes, engram_gate_dot,
+               engram_gate_output, engram_gate_output_backward, engram_gate_output_backward_workspace_bytes,
+               engram_gate_residual, engram_gather_dequant,
+               engram_gather_dequant_packed, engram_gather_mx, engram_grad_norm, engram_hash, engram_hash_gather_packed,
                engram_mx_quant, engram_wkv, engram_wkv_gate, engram_wkv_gate_layers,
-               engram_wkv_gate_workspace_bytes, engram_wkv_mx, engram_wkv_mx_gate)
+               engram_wkv_backward, engram_wkv_backward_workspace_bytes, engram_wkv_gate_workspace_bytes, engram_wkv_mx,
+               engram_wkv_mx_gate)
 
 
 @dataclasses.dataclass
@@ -50,6 +58,24 @@ class LayerWeights:
     packed: "Optional[torch.Tensor]" = None  # uint8 [R, 2*D]: the same table as one record per row (engram_pack_table)
     # the wkv weight in the fp8 block-scaled (OCP MX) form: (E4M3 bytes [Nout, K], E8M0 scales), for fp8=True
     wkv_mx: "Optional[tuple]" = None
+
+
+@dataclasses.dataclass
+class LayerGrads:
+    """What EngramForward.backward returns for one layer (all but dx are the object's buffers, overwritten by the next call
+    for the layer)."""
+
+    dx: "torch.Tensor"             # bf16, x's shape
+    dwkv: "torch.Tensor"           # float32 [dim*(hc+1), C*D]
+    dq: "torch.Tensor"             # float32 [hc, dim]
+    dk: "torch.Tensor"             # float32 [hc, dim]
+    row_ids: "torch.Tensor"        # int64 [T*C]: the table rows the ids reach, ascending; -1 past `row_count`
+    rows: "torch.Tensor"           # float32 [T*C, D]: their gradients (of the dequantised values); 0 past `row_count`
+    row_count: "torch.Tensor"      # int32 [1]
+
+    def tensors(self):
+        """The weights' gradients, to be clipped together (rows past row_count are zeros)."""
+        return [self.dwkv, self.dq, self.dk, self.rows]
 
 
 class EngramForward:
@@ -228,6 +254,41 @@ class EngramForward:
         self._timed(events, "gate_dot", lambda: engram_gate_dot(x3, kv, lw.q_weight, lw.k_weight, self.eps, out=dot))
         return a, kv, dot
 
+    def backward(self, e: int, hash_ids, x, a, kv, dot, dout, token_mask=None, events=None, dx=None):
+        """LayerGrads of layer e from `dout`, the gradient of the output stream of `layer(e, hash_ids, x, token_mask=...,
+        output=True)`, and what that call returned: a, kv and dot.  `dx` (dout itself is allowed) receives the stream's
+        gradient; by default it is a new tensor."""
+        import torch
+
+        lw = self.layers[e]
+        T = hash_ids.shape[0] * hash_ids.shape[1]
+        dev = hash_ids.device
+        hc, dim = x.shape[-2], x.shape[-1]
+        D, N = lw.weight.shape[1], lw.wkv.shape[0]
+        K, n = self.C * D, T * self.C
+        ws = self._buf("backward_workspace", (max(16, engram_gate_output_backward_workspace_bytes(T, hc, dim),
+                                                  engram_wkv_backward_workspace_bytes(T, K, N),
+                                                  engram_embed_grad_workspace_bytes(n, D, lw.weight.shape[0])),),
+                       torch.uint8, dev)
+        dkv = self._buf("dkv", (T, N), torch.bfloat16, dev)
+        da = self._buf("da", (T, K), torch.bfloat16, dev)
+        dq = self._buf(("dq", e), (hc, dim), torch.float32, dev)
+        dk = self._buf(("dk", e), (hc, dim), torch.float32, dev)
+        dw = self._buf(("dwkv", e), (N, K), torch.float32, dev)
+        ids = self._buf(("row_ids", e), (n,), torch.int64, dev)
+        rows = self._buf(("rows", e), (n, D), torch.float32, dev)
+        count = self._buf(("row_count", e), (1,), torch.int32, dev)
+        if dx is None:
+            dx = torch.empty_like(x)
+        self._timed(events, "gate_output_backward", lambda: engram_gate_output_backward(
+            x, kv, lw.q_weight, lw.k_weight, self.eps, dot, dout, token_mask, dx=dx, dkv=dkv, dq=dq, dk=dk, workspace=ws))
+        self._timed(events, "wkv_backward", lambda: engram_wkv_backward(dkv, a.view(T, K), lw.wkv, da=da, dw=dw,
+                                                                        workspace=ws))
+        self._timed(events, "embed_grad_rows", lambda: engram_embed_grad_rows(
+            hash_ids, da, lw.weight.shape[0], row_start=lw.row_start, layer=e, unique=ids, rows=rows, count=count,
+            workspace=ws))
+        return LayerGrads(dx, dw, dq, dk, ids, rows, count)
+
     def step(self, input_ids, start_pos: int, xs, token_mask=None, events=None, output=False, fused=False,
              packed=False, hash_gather=False, all_layers=False, fp8=False, gather_mx=False):
         """One forward over all engram layers; xs[e] is layer e's residual stream [B, L, hc, dim]
@@ -286,6 +347,14 @@ class EngramForward:
         return res
 
 
+def clip_grads(grads, max_norm: float, stream=None):
+    """Clips `grads` (a list of bf16 / float32 tensors, LayerGrads.tensors() of several layers and any others) in place by
+    their common norm, which is returned (float32 [1], on the GPU)."""
+    norm = engram_grad_norm(grads, stream=stream)
+    engram_clip_grads(grads, norm, max_norm, stream=stream)
+    return norm
+
+
 def _numel(shape) -> int:
     n = 1
     for d in shape:
@@ -293,4 +362,4 @@ def _numel(shape) -> int:
     return n
 
 
-__all__ = ["HashState", "LayerWeights", "EngramForward"]
+__all__ = ["HashState", "LayerWeights", "LayerGrads", "EngramForward", "clip_grads"]

@@ -15,10 +15,19 @@ does not hand their memory on before that stream is done with it.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
-from . import _check, _dev, lib
+from . import _check, lib
+
+torch = None  # imported by the first call, as in the rest of the package
+
+
+def _load():
+    global torch
+    import torch as t
+
+    torch = t
+
 
 BF16, F32 = 0, 1  # ENGRAM_BF16, ENGRAM_F32
 
@@ -43,78 +52,107 @@ def declare(L: ctypes.CDLL) -> None:
 
 
 class _On:
-    """The call's stream: `handle` for the C side, `empty` for what the call allocates."""
+    """Where a call runs: the device of its tensors (which has to be the current one) and its stream.  At the smallest
+    sizes this binding is most of a call's time, so it asks for the raw stream and passes plain integers."""
 
-    def __init__(self, stream):
-        import torch
+    __slots__ = ("index", "handle", "side")
 
-        self.torch = torch
-        self.current = torch.cuda.current_stream()
-        self.stream = self.current if stream is None else stream
-        self.other = stream is not None and stream.cuda_stream != self.current.cuda_stream
-        self.handle = ctypes.c_void_p(self.stream.cuda_stream)
+    def __init__(self, stream, like=None, name="tensor"):
+        if torch is None:
+            _load()
+        if like is None:
+            self.index = torch.cuda.current_device()
+        else:
+            if not isinstance(like, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if not like.is_cuda:
+                raise ValueError(f"{name} must be a GPU tensor")
+            self.index = like.get_device()
+            if self.index != torch.cuda.current_device():
+                raise ValueError(f"{name} is on GPU {self.index}, the current device is {torch.cuda.current_device()}")
+        current = torch._C._cuda_getCurrentRawStream(self.index)
+        self.handle, self.side = current, None
+        if stream is not None and stream.cuda_stream != current:
+            self.handle, self.side = stream.cuda_stream, stream
 
-    def empty(self, shape, dtype, device, keep=True):
+    def ptr(self, t, name, dtype, ndim=None):
+        """Address of a contiguous tensor of the call's device."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} is on GPU {t.get_device()}, the call runs on GPU {self.index}")
+        if ndim is not None and t.dim() != ndim:
+            raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def real(self, t, name, ndim=None):
+        """(address, element type) of a contiguous bf16 or float32 tensor."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        kind = BF16 if t.dtype is torch.bfloat16 else F32
+        if kind == F32 and t.dtype is not torch.float32:
+            raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+        return self.ptr(t, name, t.dtype, ndim), kind
+
+    def ids(self, ids):
+        """(address, bytes per id)."""
+        if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int64, torch.int32):
+            raise TypeError("ids must be an int64 or int32 tensor")
+        return self.ptr(ids, "ids", ids.dtype), ids.element_size()
+
+    def empty(self, shape, dtype, keep=True):
         """An uninitialised tensor of the call's stream; `keep`: the caller gets it (and may use it on its own)."""
-        if not self.other:
-            return self.torch.empty(shape, dtype=dtype, device=device)
-        with self.torch.cuda.stream(self.stream):
-            t = self.torch.empty(shape, dtype=dtype, device=device)
+        if self.side is None:
+            return torch.empty(shape, dtype=dtype, device=self.index)
+        with torch.cuda.stream(self.side):
+            t = torch.empty(shape, dtype=dtype, device=self.index)
         if keep:
-            t.record_stream(self.current)
+            t.record_stream(torch.cuda.current_stream())
         return t
 
-
-def _float_type(dtype, name):
-    import torch
-
-    if dtype == torch.bfloat16:
-        return BF16
-    if dtype == torch.float32:
-        return F32
-    raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
-
-
-def _any_float(t, name, ndim=None):
-    """(pointer, element type) of a contiguous bf16 or float32 GPU tensor."""
-    return _dev(t, name, t.dtype, ndim), _float_type(t.dtype, name)
-
-
-def _ids(ids):
-    import torch
-
-    if ids.dtype not in (torch.int64, torch.int32):
-        raise TypeError(f"ids must be int64 or int32, got {ids.dtype}")
-    return _dev(ids, "ids", ids.dtype), ids.element_size()
+    def workspace(self, given, need):
+        """(tensor, address, bytes) of the call's scratch; (None, None, 0) where it needs none and none is given."""
+        if given is None:
+            if need == 0:
+                return None, None, 0
+            given = self.empty(need, torch.uint8, keep=False)
+            return given, given.data_ptr(), need
+        return given, self.ptr(given, "workspace", torch.uint8), given.numel()
 
 
 def engram_embed(ids, table, scale=1.0, row_start=0, out=None, out_dtype=None, stream=None):
     """out [*ids.shape, D] = scale * table[ids - row_start] (zeros for ids outside the table's rows).
 
     ids: int64 or int32 of any shape; table: bf16 or float32 [R, D]; out in `out_dtype` (the table's by default)."""
-    on = _On(stream)
-    tp, td = _any_float(table, "table", 2)
-    ip, ib = _ids(ids)
+    on = _On(stream, table, "table")
+    tp, td = on.real(table, "table", 2)
+    ip, ib = on.ids(ids)
     R, D = table.shape
     if out is None:
-        out = on.empty((*ids.shape, D), table.dtype if out_dtype is None else out_dtype, ids.device)
+        out = on.empty((*ids.shape, D), table.dtype if out_dtype is None else out_dtype)
     elif tuple(out.shape) != (*ids.shape, D) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be [*ids.shape, D] of out_dtype")
-    op, od = _any_float(out, "out")
+    op, od = on.real(out, "out")
     _check(lib().engram_embed(ip, ib, ids.numel(), tp, td, R, int(row_start), D, float(scale), op, od, on.handle))
     return out
 
 
-def _lookup(ids, grad, layer):
+def _lookup(on, ids, grad, layer):
     """(ids pointer, id bytes, T, token stride, C, D) of ids [*] with grad [*, D], or of layer `layer` of ids
     [B, L, E, C] with grad [B*L, C, D] or [B*L, C*D]."""
-    ip, ib = _ids(ids)
+    ip, ib = on.ids(ids)
     if layer is not None:
         if ids.dim() != 4 or not 0 <= layer < ids.shape[2]:
             raise ValueError("`layer` needs ids [B, L, E, C] with that layer")
         B, L, E, C = ids.shape
         T, stride = B * L, E * C
-        ip = ctypes.c_void_p(ids.data_ptr() + ids.element_size() * layer * C)
+        ip += ib * layer * C
         n = T * C
         if grad.dim() == 2 and T > 0 and grad.shape[0] == T and grad.shape[1] % C == 0 and C > 1:
             D = grad.shape[1] // C
@@ -134,14 +172,6 @@ def engram_embed_grad_workspace_bytes(n: int, D: int, num_rows: int) -> int:
     return b
 
 
-def _workspace(on, workspace, need, device):
-    import torch
-
-    if workspace is None:
-        workspace = on.empty(max(need, 16), torch.uint8, device, keep=False)
-    return _dev(workspace, "workspace", torch.uint8), workspace.numel()
-
-
 def engram_embed_grad(ids, grad, num_rows, scale=1.0, row_start=0, layer=None, out=None, out_dtype=None, accumulate=False,
                       workspace=None, stream=None):
     """The gradient of a lookup: out [num_rows, D], row r = scale * (sum of grad's rows whose id is row_start + r).
@@ -149,19 +179,17 @@ def engram_embed_grad(ids, grad, num_rows, scale=1.0, row_start=0, layer=None, o
     ids: int64 or int32 of any shape with grad [*ids.shape, D] (bf16 or float32); or engram_hash's [B, L, E, C] with
     `layer` and grad [B*L, C, D] or [B*L, C*D].  out is float32 unless `out_dtype` says bf16; with `accumulate` the sum
     is added to the given `out`, whose other rows are not touched."""
-    import torch
-
-    on = _On(stream)
-    ip, ib, T, stride, C, n, D = _lookup(ids, grad, layer)
-    gp, gd = _any_float(grad, "grad")
+    on = _On(stream, grad, "grad")
+    ip, ib, T, stride, C, n, D = _lookup(on, ids, grad, layer)
+    gp, gd = on.real(grad, "grad")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs the out to add to")
-        out = on.empty((num_rows, D), torch.float32 if out_dtype is None else out_dtype, ids.device)
+        out = on.empty((num_rows, D), torch.float32 if out_dtype is None else out_dtype)
     elif tuple(out.shape) != (num_rows, D) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be [num_rows, D] of out_dtype")
-    op, od = _any_float(out, "out", 2)
-    wp, wn = _workspace(on, workspace, engram_embed_grad_workspace_bytes(n, D, num_rows), ids.device)
+    op, od = on.real(out, "out", 2)
+    _ws, wp, wn = on.workspace(workspace, engram_embed_grad_workspace_bytes(n, D, num_rows))
     _check(lib().engram_embed_grad(ip, ib, T, stride, C, gp, gd, int(num_rows), int(row_start), D, float(scale), op, od,
                                    int(bool(accumulate)), wp, wn, on.handle))
     return out
@@ -172,25 +200,23 @@ def engram_embed_grad_rows(ids, grad, num_rows, scale=1.0, row_start=0, layer=No
     """The same gradient as its distinct rows: (unique int64 [n] ascending, -1 past the last; rows [n, D], zeros past
     the last; count int32 [1]), n the number of ids.  Arguments as engram_embed_grad; rows float32 unless `out_dtype`
     says bf16."""
-    import torch
-
-    on = _On(stream)
-    ip, ib, T, stride, C, n, D = _lookup(ids, grad, layer)
-    gp, gd = _any_float(grad, "grad")
+    on = _On(stream, grad, "grad")
+    ip, ib, T, stride, C, n, D = _lookup(on, ids, grad, layer)
+    gp, gd = on.real(grad, "grad")
     if unique is None:
-        unique = on.empty((n,), torch.int64, ids.device)
+        unique = on.empty((n,), torch.int64)
     if rows is None:
-        rows = on.empty((n, D), torch.float32 if out_dtype is None else out_dtype, ids.device)
+        rows = on.empty((n, D), torch.float32 if out_dtype is None else out_dtype)
     elif out_dtype is not None and rows.dtype != out_dtype:
         raise ValueError("rows must be of out_dtype")
     if count is None:
-        count = on.empty((1,), torch.int32, ids.device)
+        count = on.empty((1,), torch.int32)
     if tuple(unique.shape) != (n,) or tuple(rows.shape) != (n, D) or count.numel() != 1:
         raise ValueError("unique must be [n], rows [n, D] and count [1]")
-    rp, rd = _any_float(rows, "rows", 2)
-    wp, wn = _workspace(on, workspace, engram_embed_grad_workspace_bytes(n, D, num_rows), ids.device)
+    rp, rd = on.real(rows, "rows", 2)
+    _ws, wp, wn = on.workspace(workspace, engram_embed_grad_workspace_bytes(n, D, num_rows))
     _check(lib().engram_embed_grad_rows(ip, ib, T, stride, C, gp, gd, int(num_rows), int(row_start), D, float(scale),
-                                        _dev(unique, "unique", torch.int64), rp, rd, _dev(count, "count", torch.int32),
+                                        on.ptr(unique, "unique", torch.int64), rp, rd, on.ptr(count, "count", torch.int32),
                                         wp, wn, on.handle))
     return unique, rows, count
 
@@ -207,16 +233,16 @@ def engram_gate_output_backward(x, kv, q_weight, k_weight, eps, dot, dout, token
     """(dx bf16 of x's shape, dkv bf16 [T, (hc+1)*dim], dq, dk float32 [hc, dim]) from dout, the gradient of
     engram_gate_output's out (or engram_gate_residual's), and the forward's x, kv [T, >= (hc+1)*dim] and dot float32
     [T, hc]; token_mask as the forward's.  `dx` may be dout itself."""
-    import torch
-
-    on = _On(stream)
-    x3 = x.reshape(-1, x.shape[-2], x.shape[-1])
-    T, hc, dim = x3.shape
+    on = _On(stream, x, "x")
+    if x.dim() < 3:
+        raise ValueError("x must be [T, hc, dim] (or [B, L, hc, dim])")
+    hc, dim = x.shape[-2:]
+    T = x.numel() // (hc * dim) if hc * dim else 0
     if kv.dim() != 2 or kv.shape[0] != T or kv.shape[1] < (hc + 1) * dim:
         raise ValueError("kv must be [T, >= (hc+1)*dim]")
-    if tuple(q_weight.shape) != (hc, dim) or tuple(k_weight.shape) != (hc, dim):
+    if q_weight.shape != (hc, dim) or k_weight.shape != (hc, dim):
         raise ValueError("q_weight and k_weight must be [hc, dim]")
-    if tuple(dot.shape) != (T, hc):
+    if dot.shape != (T, hc):
         raise ValueError("dot must be [T, hc]")
     if dout.shape != x.shape:
         raise ValueError("dout must have x's shape")
@@ -226,25 +252,28 @@ def engram_gate_output_backward(x, kv, q_weight, k_weight, eps, dot, dout, token
             raise ValueError("token_mask must hold one entry per token")
         if token_mask.dtype == torch.bool:
             token_mask = token_mask.view(torch.uint8)
-        mask_p = _dev(token_mask, "token_mask", torch.uint8)
+        mask_p = on.ptr(token_mask, "token_mask", torch.uint8)
+    need = engram_gate_output_backward_workspace_bytes(T, hc, dim)
+    bf, f32 = torch.bfloat16, torch.float32
     if dx is None:
-        dx = on.empty(x.shape, torch.bfloat16, x.device)
+        dx = on.empty(x.shape, bf)
+    elif dx.shape != x.shape:
+        raise ValueError("dx must have x's shape")
     if dkv is None:
-        dkv = on.empty((T, (hc + 1) * dim), torch.bfloat16, x.device)
+        dkv = on.empty((T, (hc + 1) * dim), bf)
+    elif dkv.shape != (T, (hc + 1) * dim):
+        raise ValueError("dkv must be [T, (hc+1)*dim]")
     if dq is None:
-        dq = on.empty((hc, dim), torch.float32, x.device)
+        dq = on.empty((hc, dim), f32)
     if dk is None:
-        dk = on.empty((hc, dim), torch.float32, x.device)
-    if dx.shape != x.shape or tuple(dkv.shape) != (T, (hc + 1) * dim):
-        raise ValueError("dx must have x's shape and dkv be [T, (hc+1)*dim]")
-    if tuple(dq.shape) != (hc, dim) or tuple(dk.shape) != (hc, dim):
+        dk = on.empty((hc, dim), f32)
+    if dq.shape != (hc, dim) or dk.shape != (hc, dim):
         raise ValueError("dq and dk must be [hc, dim]")
-    wp, wn = _workspace(on, workspace, engram_gate_output_backward_workspace_bytes(T, hc, dim), x.device)
-    bf = torch.bfloat16
+    _ws, wp, wn = on.workspace(workspace, need)
     _check(lib().engram_gate_output_backward(
-        _dev(x, "x", bf), _dev(kv, "kv", bf, 2), kv.shape[1], _dev(q_weight, "q_weight", bf, 2),
-        _dev(k_weight, "k_weight", bf, 2), float(eps), _dev(dot, "dot", torch.float32, 2), _dev(dout, "dout", bf), mask_p,
-        _dev(dx, "dx", bf), _dev(dkv, "dkv", bf, 2), _dev(dq, "dq", torch.float32, 2), _dev(dk, "dk", torch.float32, 2),
+        on.ptr(x, "x", bf), on.ptr(kv, "kv", bf, 2), kv.shape[1], on.ptr(q_weight, "q_weight", bf, 2),
+        on.ptr(k_weight, "k_weight", bf, 2), float(eps), on.ptr(dot, "dot", f32, 2), on.ptr(dout, "dout", bf), mask_p,
+        on.ptr(dx, "dx", bf), on.ptr(dkv, "dkv", bf, 2), on.ptr(dq, "dq", f32, 2), on.ptr(dk, "dk", f32, 2),
         wp, wn, T, hc, dim, on.handle))
     return dx, dkv, dq, dk
 
@@ -262,93 +291,86 @@ def engram_wkv_backward(dkv, a, w, da=None, dw=None, dw_dtype=None, accumulate=F
 
     dw is float32 unless `dw_dtype` says bf16; with `accumulate` the product is added to the given `dw`.  With
     need_da / need_dw False that product is not computed (None) and the operand only it reads (w / a) may be None."""
-    import torch
-
-    on = _On(stream)
+    on = _On(stream, dkv, "dkv")
     if not (need_da or need_dw):
         raise ValueError("neither da nor dw is asked for")
     if (need_da and w is None) or (need_dw and a is None):
         raise ValueError("da needs w, dw needs a")
     bf = torch.bfloat16
-    dp = _dev(dkv, "dkv", bf, 2)
+    dp = on.ptr(dkv, "dkv", bf, 2)
     T, N = dkv.shape
-    ap = wp_ = dap = dwp = None
-    K = None
+    ap = wp = dap = dwp = K = None
     if w is not None:
-        wp_ = _dev(w, "w", bf, 2)
-        K = w.shape[1]
+        wp = on.ptr(w, "w", bf, 2)
         if w.shape[0] != N:
             raise ValueError(f"w must be [Nout={N}, K], got {tuple(w.shape)}")
+        K = w.shape[1]
     if a is not None:
-        ap = _dev(a, "a", bf)
+        ap = on.ptr(a, "a", bf)
         Ka = a.shape[1] * a.shape[2] if a.dim() == 3 else a.shape[-1]
         if a.dim() not in (2, 3) or a.shape[0] != T or (K is not None and Ka != K):
             raise ValueError(f"a must be [T={T}, K={K}], got {tuple(a.shape)}")
         K = Ka
-    if need_da:
-        if da is None:
-            da = on.empty((T, K), bf, dkv.device)
-        if da.numel() != T * K:
-            raise ValueError("da must hold T * K elements")
-        dap = _dev(da, "da", bf)
-    else:
+    need = engram_wkv_backward_workspace_bytes(T, K, N)
+    if not need_da:
         da = None
-    dwt = F32
-    if need_dw:
+    else:
+        if da is None:
+            da = on.empty((T, K), bf)
+        elif da.numel() != T * K:
+            raise ValueError("da must hold T * K elements")
+        dap = on.ptr(da, "da", bf)
+    kind = F32
+    if not need_dw:
+        dw = None
+    else:
         if dw is None:
             if accumulate:
                 raise ValueError("accumulate needs the dw to add to")
-            dw = on.empty((N, K), torch.float32 if dw_dtype is None else dw_dtype, dkv.device)
-        if tuple(dw.shape) != (N, K) or (dw_dtype is not None and dw.dtype != dw_dtype):
+            dw = on.empty((N, K), torch.float32 if dw_dtype is None else dw_dtype)
+        elif dw.shape != (N, K) or (dw_dtype is not None and dw.dtype != dw_dtype):
             raise ValueError("dw must be [Nout, K] of dw_dtype")
-        dwp, dwt = _any_float(dw, "dw", 2)
-    else:
-        dw = None
-    wsp, wsn = _workspace(on, workspace, engram_wkv_backward_workspace_bytes(T, K, N), dkv.device)
-    _check(lib().engram_wkv_backward(dp, ap, wp_, dap, dwp, dwt, int(bool(accumulate)), wsp, wsn, T, K, N, on.handle))
+        dwp, kind = on.real(dw, "dw", 2)
+    _ws, sp, sn = on.workspace(workspace, need)
+    _check(lib().engram_wkv_backward(dp, ap, wp, dap, dwp, kind, int(bool(accumulate)), sp, sn, T, K, N, on.handle))
     return da, dw
 
 
-def _tensor_list(grads):
-    """(count, host arrays of pointers, element counts and element types) of contiguous bf16 / float32 tensors."""
+def _tensor_list(on, grads, name):
+    """(count, host arrays of addresses, element counts and element types) of contiguous bf16 / float32 tensors."""
     n = len(grads)
-    got = [_any_float(g, f"grads[{i}]") for i, g in enumerate(grads)]
-    return (n, (ctypes.c_void_p * n)(*[p.value for p, _ in got]), (ctypes.c_int64 * n)(*[g.numel() for g in grads]),
+    got = [on.real(g, f"{name}[{i}]") for i, g in enumerate(grads)]
+    return (n, (ctypes.c_void_p * n)(*[p for p, _ in got]), (ctypes.c_int64 * n)(*[g.numel() for g in grads]),
             (ctypes.c_int32 * n)(*[d for _, d in got]))
 
 
 def engram_grad_norm(grads, out=None, workspace=None, stream=None):
     """float32 [1]: the 2-norm of all elements of `grads` (a list of contiguous bf16 / float32 tensors) together."""
-    import torch
-
-    on = _On(stream)
-    n, ptrs, sizes, types = _tensor_list(grads)
+    on = _On(stream, grads[0] if len(grads) else None, "grads[0]")
+    n, ptrs, sizes, types = _tensor_list(on, grads, "grads")
     if out is None:
-        out = on.empty((1,), torch.float32, grads[0].device if n else "cuda")
-    if out.numel() != 1:
+        out = on.empty((1,), torch.float32)
+    elif out.numel() != 1:
         raise ValueError("out must hold one element")
-    need = lib().engram_grad_norm_workspace_bytes(n, sizes, types)
-    wp, wn = _workspace(on, workspace, need, out.device)
-    _check(lib().engram_grad_norm(n, ptrs, sizes, types, _dev(out, "out", torch.float32), wp, wn, on.handle))
+    _ws, wp, wn = on.workspace(workspace, lib().engram_grad_norm_workspace_bytes(n, sizes, types))
+    _check(lib().engram_grad_norm(n, ptrs, sizes, types, on.ptr(out, "out", torch.float32), wp, wn, on.handle))
     return out
 
 
 def engram_clip_grads(grads, norm, max_norm, outs=None, stream=None):
     """Every gradient times min(1, max_norm / (norm + 1e-6)): into `outs` (tensors of the gradients' types and sizes), or
     in place.  `norm`: float32 [1] on the GPU (engram_grad_norm's).  Returns the clipped tensors."""
-    import torch
-
-    on = _On(stream)
-    n, ptrs, sizes, types = _tensor_list(grads)
+    on = _On(stream, norm, "norm")
+    n, ptrs, sizes, types = _tensor_list(on, grads, "grads")
     if outs is None:
         outs, optrs = grads, ptrs
     else:
         if len(outs) != n or any(o.dtype != g.dtype or o.numel() != g.numel() for o, g in zip(outs, grads)):
             raise ValueError("outs must match grads in number, types and sizes")
-        optrs = (ctypes.c_void_p * n)(*[_dev(o, f"outs[{i}]", o.dtype).value for i, o in enumerate(outs)])
+        optrs = (ctypes.c_void_p * n)(*[on.ptr(o, "outs", o.dtype) for o in outs])
     if norm.numel() != 1:
         raise ValueError("norm must hold one element")
-    _check(lib().engram_clip_grads(n, ptrs, optrs, sizes, types, _dev(norm, "norm", torch.float32), float(max_norm),
+    _check(lib().engram_clip_grads(n, ptrs, optrs, sizes, types, on.ptr(norm, "norm", torch.float32), float(max_norm),
                                    on.handle))
     return outs
 

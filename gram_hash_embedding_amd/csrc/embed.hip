@@ -51,8 +51,11 @@ struct EmbedArgs {
     uint8_t* out;
 };
 
-__device__ inline int64_t load_id(const void* ids, int id_bytes, int64_t i) {
-    return id_bytes == 8 ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
+// the table row of an id, or -1 outside [row_start, row_start + R) (whatever 64-bit number it is)
+__device__ inline int64_t row_of(const void* ids, int id_bytes, int64_t i, int64_t row_start, int64_t R) {
+    const int64_t id = id_bytes == 8 ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
+    const uint64_t r = static_cast<uint64_t>(id) - static_cast<uint64_t>(row_start);
+    return id >= row_start && r < static_cast<uint64_t>(R) ? static_cast<int64_t>(r) : -1;
 }
 
 // One piece of kRows rows per thread, the pieces in memory order.  LPR 0: a workgroup (of up to 1,024 threads) takes a row,
@@ -71,8 +74,8 @@ __global__ __launch_bounds__(LPR == 0 ? 1024 : kThreads) void embed_kernel(Embed
 #pragma unroll
     for (int q = 0; q < kRows; ++q) {
         const int64_t i = i0 + q * kGroups;
-        const int64_t r = i < a.n ? load_id(a.ids, a.id_bytes, i) - a.row_start : -1;
-        ok[q] = r >= 0 && r < a.R;
+        const int64_t r = i < a.n ? row_of(a.ids, a.id_bytes, i, a.row_start, a.R) : -1;
+        ok[q] = r >= 0;
         if (ok[q]) v[q].load(a.table + r * a.D * TT::kBytes, piece);
     }
 #pragma unroll
@@ -179,8 +182,8 @@ __device__ inline uint32_t load_key(const SortArgs& a, uint32_t i) {
         const uint32_t t = i / static_cast<uint32_t>(a.C);
         at = static_cast<int64_t>(t) * a.stride + (i - t * static_cast<uint32_t>(a.C));
     }
-    const int64_t r = load_id(a.ids, a.id_bytes, at) - a.row_start;
-    return r >= 0 && r < static_cast<int64_t>(a.R) ? static_cast<uint32_t>(r) : a.R;
+    const int64_t r = row_of(a.ids, a.id_bytes, at, a.row_start, a.R);
+    return r >= 0 ? static_cast<uint32_t>(r) : a.R;
 }
 
 // A pass's digit counts per tile; the first pass's workgroups behind the tiles write the dense form's zeros (skipping the
@@ -416,6 +419,7 @@ struct FoldArgs {
     uint32_t* leave_to;  // rows form: [chunks] the distinct row that leaves the chunk
     float* leave;       // [chunks][D] sum of a segment that begins in the chunk and goes on after it
     float* enter;       // [chunks][D] sum of the chunk's share of a segment that began before it
+    uint32_t join_blocks;  // workgroups that join; those behind them write the rows form's tail
 };
 
 // Distinct rows per chunk (before it in its tile) and per tile.
@@ -551,123 +555,126 @@ __global__ __launch_bounds__(kThreads) void fold_kernel(FoldArgs a) {
 }
 
 // Segments that cross chunks: the chunk where one begins adds its own partial sum and those of the chunks it enters.
-// A workgroup looks at kJoinChunks chunks of one column block, a wave at a quarter of them; the 64 / LPR groups of lanes
-// of the wave take a segment's chunks in turn and their sums are added by shuffles.  A segment of kLong chunks or more
-// (a hot row) is taken by the whole workgroup, kBatch chunks per group at a time.  Every order is fixed.  In the rows
-// form also the rows past the last distinct one: zeros, and -1 for their ids.
-constexpr int kJoinChunks = 16;
+// Each group of LPR lanes takes such segments of its wave's chunks in turn; a segment of kLong chunks or more (a hot row)
+// is taken by the whole workgroup, kBatch chunks per group at a time.  Every order is fixed.  In the rows form the
+// workgroups behind them write the rows past the last distinct one: zeros, and -1 for their ids.
 constexpr int kLong = 16;
 
 template <int LPR>
-__device__ inline void add_groups(float (&acc)[8]) {
-#pragma unroll
-    for (int off = LPR; off < 64; off <<= 1)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) acc[q] += __shfl_xor(acc[q], off, 64);
+constexpr int join_chunks() {  // chunks per wave: two per group of lanes (four or eight leave too few waves)
+    return 64 / LPR * 2;
 }
 
 template <class OT, int LPR>
 __global__ __launch_bounds__(kThreads) void join_kernel(FoldArgs a) {
-    constexpr int kWaves = kThreads / 64, kGroups = 64 / LPR, kBatch = 4;
-    __shared__ float sums[kWaves][LPR][9];
-    const int cb = blockIdx.x % a.cols;
-    const uint32_t c0 = blockIdx.x / a.cols * kJoinChunks;
-    const uint32_t c1 = min(c0 + kJoinChunks, a.chunks);
+    constexpr int kWaves = kThreads / 64, kGroups = 64 / LPR, kBatch = 4, kPerWave = join_chunks<LPR>();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int group = lane / LPR, piece = cb * LPR + lane % LPR;
-    const bool live = piece < a.D / 8;
-    // which chunks a segment that began in them leaves, and which of those are long: the same in every wave
-    bool crosses = false, goes_far = false;
-    uint32_t my_key = a.R;
-    if (lane < kJoinChunks && c0 + lane < c1) {
-        const uint32_t s = (c0 + lane) * kChunk, e = min(s + kChunk, a.n);
-        if (e < a.n) {
-            const uint32_t far = c0 + lane + kLong;
-            my_key = a.sorted[e].key;
-            const uint32_t last = a.sorted[e - 1].key, prev = s ? a.sorted[s - 1].key : a.R;
-            const uint32_t far_key = far < a.chunks ? a.sorted[far * kChunk].key : a.R;
-            crosses = my_key < a.R && last == my_key && prev != my_key;
-            goes_far = crosses && far_key == my_key;
-        }
-    }
-    const uint64_t all_crossing = __ballot(crosses), far = __ballot(goes_far);
-    if (a.unique) {
+    const int group = lane / LPR;
+    if (blockIdx.x >= a.join_blocks) {
         const uint32_t all = heads_before(a, a.tiles);
-        if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = static_cast<int32_t>(all);
-        const uint32_t e = min(c1 * kChunk, a.n);
-        if (live && e > all) {
-            Piece<OT> z;
-            const float zero[8] = {};
-            z.from(zero);
-            for (uint32_t k = max(c0 * kChunk, all) + threadIdx.x / LPR; k < e; k += kThreads / LPR) {
-                z.store(a.out + static_cast<int64_t>(k) * a.D * OT::kBytes, piece);
-                if (piece == 0) a.unique[k] = -1;
+        if (blockIdx.x == a.join_blocks && threadIdx.x == 0) *a.count = static_cast<int32_t>(all);
+        // 16 bytes a thread of the rows behind the last distinct one, and their ids
+        const uint32_t per = static_cast<uint32_t>(a.D * OT::kBytes / 16);
+        const int64_t from = static_cast<int64_t>(all) * per, to = static_cast<int64_t>(a.n) * per;
+        const int64_t step = static_cast<int64_t>(gridDim.x - a.join_blocks) * kThreads;
+        const int64_t me = static_cast<int64_t>(blockIdx.x - a.join_blocks) * kThreads + threadIdx.x;
+        for (int64_t i = from + me; i < to; i += step) reinterpret_cast<u32x4*>(a.out)[i] = u32x4{0, 0, 0, 0};
+        for (int64_t k = all + me; k < a.n; k += step) a.unique[k] = -1;
+        return;
+    }
+    __shared__ float sums[kWaves][LPR][9];
+    __shared__ uint32_t keys[kWaves][kPerWave];
+    __shared__ uint64_t far_of[kWaves];
+    const int cb = blockIdx.x % a.cols;
+    const int piece = cb * LPR + lane % LPR;
+    const bool live = piece < a.D / 8;
+    const uint32_t base = blockIdx.x / a.cols * (kWaves * kPerWave);
+    const uint32_t c0 = base + wave * kPerWave;
+    // which of the wave's chunks a segment that began in them leaves, and which of those segments are long
+    bool crosses = false, goes_far = false;
+    if (lane < kPerWave) {
+        uint32_t key = a.R;
+        if (c0 + lane < a.chunks) {
+            const uint32_t s = (c0 + lane) * kChunk, e = min(s + kChunk, a.n), far = c0 + lane + kLong;
+            if (e < a.n) {
+                key = a.sorted[e].key;
+                const uint32_t last = a.sorted[e - 1].key, prev = s ? a.sorted[s - 1].key : a.R;
+                const uint32_t far_key = far < a.chunks ? a.sorted[far * kChunk].key : a.R;
+                crosses = key < a.R && last == key && prev != key;
+                goes_far = crosses && far_key == key;
             }
         }
+        keys[wave][lane] = key;
     }
-    auto add = [&](float (&acc)[8], uint32_t chunk) {
+    const uint64_t near = __ballot(crosses && !goes_far), far = __ballot(goes_far);
+    if (lane == 0) far_of[wave] = far;
+    __syncthreads();
+    auto add = [&](float (&acc)[8], const float* from, uint32_t chunk) {
         float f[8];
         Piece<F32> p;
-        p.load(a.enter + static_cast<int64_t>(chunk) * a.D, piece);
+        p.load(from + static_cast<int64_t>(chunk) * a.D, piece);
         p.to(f);
 #pragma unroll
         for (int q = 0; q < 8; ++q) acc[q] += f[q];
     };
-    auto first = [&](float (&acc)[8], uint32_t chunk) {
-        Piece<F32> p;
-        p.load(a.leave + static_cast<int64_t>(chunk) * a.D, piece);
-        p.to(acc);
-    };
-    constexpr int kQuarter = kJoinChunks / kWaves;
-    for (uint64_t todo = all_crossing & ~far & (((1ull << kQuarter) - 1) << (wave * kQuarter)); todo; todo &= todo - 1) {
-        const int bit = __builtin_ctzll(todo);
-        const uint32_t chunk = c0 + bit, key = __shfl(my_key, bit, 64);
-        float acc[8] = {};
-        if (group == 0 && live) first(acc, chunk);
-        for (uint32_t c = chunk + 1 + group; c < a.chunks && a.sorted[c * kChunk].key == key; c += kGroups)
-            if (live) add(acc, c);
-        add_groups<LPR>(acc);
-        if (group == 0 && live) put_row<OT>(a, key, a.unique ? a.leave_to[chunk] : 0, piece, acc);
-    }
-    for (uint64_t todo = far; todo; todo &= todo - 1) {
-        const int bit = __builtin_ctzll(todo);
-        const uint32_t chunk = c0 + bit, key = __shfl(my_key, bit, 64);
-        float acc[8] = {};
-        if (wave == 0 && group == 0 && live) first(acc, chunk);
-        constexpr int kStep = kWaves * kGroups * kBatch;
-        for (uint32_t c = chunk + 1 + (wave * kGroups + group) * kBatch; c < a.chunks; c += kStep) {
-            uint32_t k[kBatch];
-            Piece<F32> p[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                k[j] = c + j < a.chunks ? a.sorted[(c + j) * kChunk].key : a.R;
-                // (a chunk that is not entered holds anything: loaded, not used)
-                if (live && c + j < a.chunks) p[j].load(a.enter + static_cast<int64_t>(c + j) * a.D, piece);
-            }
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                if (k[j] != key || !live) continue;
-                float f[8];
-                p[j].to(f);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) acc[q] += f[q];
-            }
-            if (k[kBatch - 1] != key) break;
-        }
-        add_groups<LPR>(acc);
-        if (group == 0)
-#pragma unroll
-            for (int q = 0; q < 8; ++q) sums[wave][lane][q] = acc[q];
-        __syncthreads();
-        if (wave == 0 && group == 0 && live) {
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w)
-#pragma unroll
-                for (int q = 0; q < 8; ++q) acc[q] += sums[w][lane][q];
+    {
+        uint64_t todo = near;
+        for (int skip = group; todo && skip; --skip) todo &= todo - 1;
+        while (todo && live) {
+            const int bit = __builtin_ctzll(todo);
+            const uint32_t chunk = c0 + bit, key = keys[wave][bit];
+            float acc[8] = {};
+            add(acc, a.leave, chunk);
+            uint32_t c = chunk + 1;
+            do add(acc, a.enter, c++);
+            while (c < a.chunks && a.sorted[c * kChunk].key == key);
             put_row<OT>(a, key, a.unique ? a.leave_to[chunk] : 0, piece, acc);
+            for (int skip = kGroups; todo && skip; --skip) todo &= todo - 1;
         }
-        __syncthreads();
     }
+    for (int w = 0; w < kWaves; ++w)
+        for (uint64_t todo = far_of[w]; todo; todo &= todo - 1) {
+            const int bit = __builtin_ctzll(todo);
+            const uint32_t chunk = base + w * kPerWave + bit, key = keys[w][bit];
+            float acc[8] = {};
+            if (wave == 0 && group == 0 && live) add(acc, a.leave, chunk);
+            constexpr int kStep = kWaves * kGroups * kBatch;
+            for (uint32_t c = chunk + 1 + (wave * kGroups + group) * kBatch; c < a.chunks; c += kStep) {
+                uint32_t k[kBatch];
+                Piece<F32> p[kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    k[j] = c + j < a.chunks ? a.sorted[(c + j) * kChunk].key : a.R;
+                    // (a chunk that is not entered holds anything: loaded, not used)
+                    if (live && c + j < a.chunks) p[j].load(a.enter + static_cast<int64_t>(c + j) * a.D, piece);
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    if (k[j] != key || !live) continue;
+                    float f[8];
+                    p[j].to(f);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) acc[q] += f[q];
+                }
+                if (k[kBatch - 1] != key) break;
+            }
+#pragma unroll
+            for (int off = LPR; off < 64; off <<= 1)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) acc[q] += __shfl_xor(acc[q], off, 64);
+            if (group == 0)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) sums[wave][lane][q] = acc[q];
+            __syncthreads();
+            if (wave == 0 && group == 0 && live) {
+#pragma unroll
+                for (int v = 1; v < kWaves; ++v)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) acc[q] += sums[v][lane][q];
+                put_row<OT>(a, key, a.unique ? a.leave_to[chunk] : 0, piece, acc);
+            }
+            __syncthreads();
+        }
 }
 
 // Up to kSmall ids: every workgroup sorts them in LDS (a bitonic network over (row, position)) and folds its share of
@@ -863,10 +870,13 @@ int launch_fold_as(FoldArgs& a, const SortArgs* small, hipStream_t stream, const
         return check_launch(what);
     }
     const int64_t blocks = (static_cast<int64_t>(a.chunks) * a.cols + kThreads / LPR - 1) / (kThreads / LPR);
-    if (blocks > 0x7FFFFFFF) return fail(ENGRAM_EINVAL, "%s: too many ids for the row width", what);
     hipLaunchKernelGGL((fold_kernel<GT, OT, LPR>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a);
-    const int64_t joins = static_cast<int64_t>((a.chunks + kJoinChunks - 1) / kJoinChunks) * a.cols;
-    hipLaunchKernelGGL((join_kernel<OT, LPR>), dim3(static_cast<unsigned>(joins)), dim3(kThreads), 0, stream, a);
+    constexpr int kPerBlock = kThreads / 64 * join_chunks<LPR>();
+    const int64_t joins = static_cast<int64_t>((a.chunks + kPerBlock - 1) / kPerBlock) * a.cols;
+    const int64_t tail = a.unique ? (static_cast<int64_t>(a.n) * a.D * OT::kBytes / 16 + 16 * kThreads - 1) / (16 * kThreads) : 0;
+    a.join_blocks = static_cast<uint32_t>(joins);
+    hipLaunchKernelGGL((join_kernel<OT, LPR>), dim3(static_cast<unsigned>(joins + (tail < 4096 ? tail : 4096))), dim3(kThreads), 0,
+                       stream, a);
     return check_launch(what);
 }
 
@@ -896,6 +906,12 @@ int check_ids(const char* what, int32_t id_bytes, int64_t T, int64_t stride, int
     if (stride < C) return fail(ENGRAM_EINVAL, "%s: id_token_stride < C", what);
     if (T > kMaxIds / C) return fail(ENGRAM_EINVAL, "%s: more than 2^30 ids", what);
     if (R < 1 || R > 0x7FFFFFFF) return fail(ENGRAM_EINVAL, "%s: R=%lld outside [1, 2^31)", what, (long long)R);
+    return ENGRAM_OK;
+}
+
+// the launches' grids: n D / 2^15 workgroups at most
+int check_work(const char* what, int64_t n, int32_t D) {
+    if (n > (1ll << 45) / D) return fail(ENGRAM_EINVAL, "%s: too many ids for the row width", what);
     return ENGRAM_OK;
 }
 
@@ -1017,6 +1033,7 @@ extern "C" int engram_embed_grad(const void* ids, int32_t id_bytes, int64_t T, i
     const char* what = "engram_embed_grad";
     int rc = check_ids(what, id_bytes, T, id_token_stride, C, R);
     if (rc == ENGRAM_OK) rc = check_width(what, D);
+    if (rc == ENGRAM_OK) rc = check_work(what, T * C, D);
     if (rc != ENGRAM_OK) return rc;
     if (!known_dtype(up_dtype) || !known_dtype(grad_dtype)) return fail(ENGRAM_EINVAL, "%s: unknown dtype", what);
     const int64_t n = T * C;
@@ -1044,6 +1061,7 @@ extern "C" int engram_embed_grad_rows(const void* ids, int32_t id_bytes, int64_t
     const char* what = "engram_embed_grad_rows";
     int rc = check_ids(what, id_bytes, T, id_token_stride, C, R);
     if (rc == ENGRAM_OK) rc = check_width(what, D);
+    if (rc == ENGRAM_OK) rc = check_work(what, T * C, D);
     if (rc != ENGRAM_OK) return rc;
     if (!known_dtype(up_dtype) || !known_dtype(rows_dtype)) return fail(ENGRAM_EINVAL, "%s: unknown dtype", what);
     const int64_t n = T * C;

@@ -195,6 +195,41 @@ def test_embed_grad_accumulate(gpu_device, n, odt):
     assert got[7].isnan().all()
 
 
+def test_ids_at_the_ends_of_64_bits(gpu_device):
+    """Ids and first rows whose difference does not fit 64 bits are outside the table like any other."""
+    g = _eng()
+    lo, hi = -(1 << 63), (1 << 63) - 1
+    for row_start, inside in ((hi - 3, (hi - 3, hi)), (lo, (lo, lo + 3)), (5, (5, 8)), (-5, (-5, -2))):
+        ids = torch.tensor([lo, lo + 1, lo + 3, -6, -5, -2, -1, 0, 4, 5, 8, 9, hi - 4, hi - 3, hi], device=gpu_device)
+        ok = ((ids >= inside[0]) & (ids <= inside[1])).cpu()
+        out = g.engram_embed(ids, torch.ones((4, 8), device=gpu_device), row_start=row_start).cpu()
+        assert torch.equal(out[:, 0] == 1, ok) and torch.equal(out[:, 0] == 0, ~ok)
+        got = g.engram_embed_grad(ids, torch.ones((ids.numel(), 8), device=gpu_device), 4, row_start=row_start)
+        assert float(got[:, 0].sum()) == int(ok.sum())
+        unique, _, count = g.engram_embed_grad_rows(ids, torch.ones((ids.numel(), 8), device=gpu_device), 4,
+                                                    row_start=row_start)
+        assert int(count) == int(ok.sum()) and torch.equal(unique[:int(count)].cpu(), torch.unique(ids.cpu()[ok]))
+
+
+def test_offsets_past_32_bits(gpu_device):
+    """A table and its gradient of 2.5 G elements: rows on both sides of 2^31 elements and 2^32 bytes."""
+    g, R, D = _eng(), 610000, 4096
+    table = torch.zeros((R, D), dtype=BF, device=gpu_device)
+    pick = torch.tensor([0, 1, 262143, 262144, 524287, 524288, 524289, R - 1], device=gpu_device)
+    rows = torch.randn((pick.numel(), D), device=gpu_device).to(BF)
+    table[pick] = rows
+    for reps in (1, 300):  # one launch, and the sorted path
+        ids = pick.repeat(reps)
+        assert torch.equal(g.engram_embed(ids, table), rows.repeat(reps, 1))
+        up = torch.zeros((ids.numel(), D), dtype=BF, device=gpu_device)
+        up[:pick.numel()] = rows
+        grad = g.engram_embed_grad(ids, up, R, out=torch.full((R, D), NAN, dtype=BF, device=gpu_device))
+        assert torch.equal(grad[pick], rows)
+        grad[pick] = 0
+        assert not grad.any()
+        del grad
+
+
 def test_embed_grad_no_ids_and_non_finite(gpu_device):
     g = _eng()
     none = torch.empty((0,), dtype=torch.int64, device=gpu_device)
@@ -314,6 +349,23 @@ def test_gate_backward_edges_of_the_dot(gpu_device, hc):
         assert torch.equal(got[0][i].cpu(), dout[i]), i
 
 
+def test_gate_backward_past_32_bits(gpu_device):
+    """108,000 tokens: the stream holds 2.2 G elements, kv 2.8 G; sampled tokens, and the rest must be finite."""
+    g, T, hc, dim = _eng(), 108000, 4, 5120
+    gen = torch.Generator(device=gpu_device).manual_seed(3)
+    r = lambda *s: torch.empty(s, dtype=BF, device=gpu_device).normal_(generator=gen)  # noqa: E731
+    x, kv, dout = r(T, hc, dim), r(T, (hc + 1) * dim), r(T, hc, dim)
+    q, k = 1 + 0.1 * r(hc, dim), 1 + 0.1 * r(hc, dim)
+    dot = torch.empty((T, hc), device=gpu_device).normal_(generator=gen)
+    dx, dkv, dq, dk = g.engram_gate_output_backward(x, kv, q, k, 1e-20, dot, dout)
+    at = torch.tensor([0, 1, 53687, 52428, 83886, 104857, 104858, T - 2, T - 1])
+    c = lambda t: t[at.to(gpu_device)].cpu()  # noqa: E731
+    want = ref.gate_backward(c(x), c(kv), q.cpu(), k.cpu(), 1e-20, c(dot), c(dout))
+    for name, t in (("dx", c(dx)), ("dkv", c(dkv))):
+        _within(t, want[name], 2 * (dim + 64) * ref.U32 * want[name + "_mag"] + ref.U16 * want[name].abs(), name)
+    assert torch.isfinite(dq).all() and torch.isfinite(dk).all()
+
+
 def test_gate_backward_refusals(gpu_device):
     g = _eng()
     x, kv, q, k, dot, dout = [t.to(gpu_device) for t in _gate_inputs(6, 4, 64, 1)]
@@ -399,6 +451,21 @@ def test_wkv_backward_no_tokens_and_non_finite(gpu_device):
     da, dw = g.engram_wkv_backward(dkv, a, w)
     assert da[66].isnan().all() and da[:66, 3].isinf().all() and torch.isfinite(da[:66, 4:]).all()
     assert dw[10].isnan().all() and torch.isfinite(dw[:10]).all() and torch.isfinite(dw[11:]).all()
+
+
+def test_wkv_backward_past_32_bits(gpu_device):
+    """dkv of 2.4 G elements: one-hot tokens pick rows of w and rows of a, exactly, on both sides of 2^31 elements."""
+    g, T, K, N = _eng(), 95000, 64, 25600
+    gen = torch.Generator().manual_seed(4)
+    w, a = _randn(gen, (N, K), BF).to(gpu_device), _randn(gen, (T, K), BF).to(gpu_device)
+    dkv = torch.zeros((T, N), dtype=BF, device=gpu_device)
+    tok = torch.tensor([0, 5, 41943, 83885, 83886, 83887, 94999], device=gpu_device)
+    col = torch.tensor([0, 25599, 12800, 255, 256, 77, 20000], device=gpu_device)
+    dkv[tok, col] = 1
+    da, dw = g.engram_wkv_backward(dkv, a, w)
+    assert torch.equal(da[tok], w[col]) and torch.equal(dw[col], a[tok].float())
+    da[tok], dw[col] = 0, 0
+    assert not da.any() and not dw.any()
 
 
 def test_wkv_backward_refusals(gpu_device):

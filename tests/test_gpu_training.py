@@ -131,6 +131,15 @@ def test_embed_grad(gpu_device, kind, n, R, D, gdt, odt):
     _check_grad(_eng(), ids, _randn(gen, (n, D), gdt), R, D, gpu_device, odt, scale=3.0, what=f"{kind} {n}")
 
 
+@pytest.mark.parametrize("kind", ["one", "runs", "zipf"])
+@pytest.mark.parametrize("n", [1024, 2047, 2049, 8191, 8192, 8193])
+def test_embed_grad_at_the_sorts_edges(gpu_device, n, kind):
+    """Where one launch, one sorting workgroup and the sort over tiles hand over."""
+    gen = torch.Generator().manual_seed(n)
+    for R in (3, 300, 70000):
+        _check_grad(_eng(), _ids_of(kind, n, R, gen), _randn(gen, (n, 16), BF), R, 16, gpu_device, F32, what=f"{kind} {R}")
+
+
 @pytest.mark.parametrize("n,R,D,kind", [(270000, 3988006, 8, "zipf"), (300001, 129280, 8, "runs"), (262144, 513, 8, "one")])
 def test_embed_grad_many_tiles(gpu_device, n, R, D, kind):
     gen = torch.Generator().manual_seed(n)

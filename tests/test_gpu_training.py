@@ -416,11 +416,14 @@ def test_wkv_backward(gpu_device, T, K, N, dwt):
     _within(dw, p.t() @ q, tol, "dw")
     again = g.engram_wkv_backward(dd, ad, wd, dw_dtype=dwt)
     assert torch.equal(again[0], da) and torch.equal(again[1], dw)
-    # each product alone gives the same bits; accumulation adds to what is there
+    # each product alone (its sum may be cut into other parts); accumulation adds to what is there
+    tol_da = 2 * N * ref.U32 * (p.abs() @ r.abs()) + ref.U16 * (p @ r).abs()
     only_da, none = g.engram_wkv_backward(dd, None, wd, need_dw=False)
-    assert none is None and torch.equal(only_da, da)
+    assert none is None
+    _within(only_da, p @ r, tol_da, "da alone")
     none, only_dw = g.engram_wkv_backward(dd, ad, None, need_da=False, dw_dtype=dwt)
-    assert none is None and torch.equal(only_dw, dw)
+    assert none is None
+    _within(only_dw, p.t() @ q, tol, "dw alone")
     base = _randn(gen, (N, K), dwt)
     _, acc = g.engram_wkv_backward(dd, ad, wd, dw=base.to(gpu_device), accumulate=True)
     want = p.t() @ q + base.double()

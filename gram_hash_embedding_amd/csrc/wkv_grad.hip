@@ -397,9 +397,10 @@ void split_both(Prod& a, Prod& b, int size) {
 }
 
 int tile_size(int64_t T, int32_t K, int32_t Nout) {
-    // 128 x 128 tiles for little work: more workgroups, and two of them a CU (251 x 1,536 x 25,600: 97 against 107 us; 512:
-    // 135 and 138; 768: 177 and 169; 2,805 x 456 x 7,864: 79 and 87)
-    return 2.0 * T * K * Nout < 5e10 ? 128 : 256;
+    // 128 x 128 tiles for little work: more workgroups, and two of them a CU.  us with 128 and 256: 251 x 1,536 x 25,600 85
+    // and 98, 400 119 and 108, 512 121 and 118; 2,000 x 1,536 x 5,120 81 and 98, 4,000 136 and 137; 8,192 x 456 x 2,000 47
+    // and 52, x 7,864 136 and 122.
+    return 2.0 * T * K * Nout < 3.2e10 ? 128 : 256;
 }
 
 int64_t part_bytes(const Prod& p) { return p.splits > 1 ? p.splits * p.M * p.N * 4 : 0; }

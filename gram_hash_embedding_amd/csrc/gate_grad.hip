@@ -100,14 +100,39 @@ __device__ inline float wave_sum_last(float v) {
     return v;
 }
 
-template <int HC, int kMaxThreads>
+// kLds: q * k in LDS (where a workgroup fills the CU); else read for every token from L2 (where other workgroups on the
+// CU hide that).
+template <int HC, int kMaxThreads, bool kLds>
 __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) {
     constexpr int kSums = 3 * HC, kReads = (kSums + 3) / 4;
     __shared__ float sums[2][4 * kReads][kMaxWaves];  // [sum][wave]; waves the workgroup lacks hold zeros
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int piece = threadIdx.x;
     const bool live = piece < p.dim / 8;
+    __shared__ float weight[kLds ? HC : 1][kLds ? 2 : 1][kLds ? kMaxThreads * 4 : 1];  // [copy][half of a piece][4 each]
     for (int i = threadIdx.x; i < 2 * 4 * kReads * kMaxWaves; i += blockDim.x) (&sums[0][0][0])[i] = 0.f;
+    auto weights = [&](int c, int at, float (&w)[8]) {
+        Piece<Bf16> qr, kw;
+        float kf[8];
+        qr.load(p.q, at);
+        kw.load(p.k, at);
+        qr.to(w);
+        kw.to(kf);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] *= kf[e];  // exact: bf16 * bf16 fits fp32
+    };
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    if constexpr (kLds) {
+        if (live) {
+#pragma unroll
+            for (int c = 0; c < HC; ++c) {
+                float w[8];
+                weights(c, c * (p.dim / 8) + piece, w);
+                reinterpret_cast<f32x4*>(weight[c][0])[piece] = f32x4{w[0], w[1], w[2], w[3]};
+                reinterpret_cast<f32x4*>(weight[c][1])[piece] = f32x4{w[4], w[5], w[6], w[7]};
+            }
+        }
+    }
     __syncthreads();
     float acc[HC][8] = {};
     Piece<Bf16> hr[HC], kr[HC], ur[HC], vr;
@@ -185,20 +210,27 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) 
             Coef k = coef_of(p, total(3 * c), total(3 * c + 1), total(3 * c + 2), p.dot[t * HC + c]);
             k = Coef{uniform(k.g), uniform(k.a), uniform(k.bh), uniform(k.bk)};
             if (live) {
-                Piece<Bf16> qr, kw;
-                int at = c * (p.dim / 8) + piece;
-                asm volatile("" : "+v"(at));  // read anew for every token (from L2), not held in registers over them
-                qr.load(p.q, at);
-                kw.load(p.k, at);
-                float h[8], key[8], u[8], qf[8], kf[8], ox[8], ok[8];
+                float w[8];
+                if constexpr (kLds) {
+                    const f32x4 lo = reinterpret_cast<const f32x4*>(weight[c][0])[piece];
+                    const f32x4 hi = reinterpret_cast<const f32x4*>(weight[c][1])[piece];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = lo[e];
+                        w[4 + e] = hi[e];
+                    }
+                } else {
+                    int at = c * (p.dim / 8) + piece;
+                    asm volatile("" : "+v"(at));  // read anew for every token, not held in registers over them
+                    weights(c, at, w);
+                }
+                float h[8], key[8], u[8], ox[8], ok[8];
                 hr[c].to(h);
                 kr[c].to(key);
                 ur[c].to(u);
-                qr.to(qf);
-                kw.to(kf);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float aw = k.a * (qf[e] * kf[e]);
+                    const float aw = k.a * w[e];
                     ox[e] = u[e] + (aw * key[e] - k.bh * h[e]);
                     ok[e] = aw * h[e] - k.bk * key[e];
                     dv[e] += k.g * u[e];
@@ -416,10 +448,11 @@ extern "C" int engram_gate_output_backward(const uint16_t* x, const uint16_t* kv
     const int threads = threads_of(dim);
     if (T > 0) {
         const dim3 grid(static_cast<unsigned>(groups)), block(threads);
-        if (hc == 4 && threads <= 640) hipLaunchKernelGGL((gate_grad_kernel<4, 640>), grid, block, 0, s, p);
-        else if (hc == 4) hipLaunchKernelGGL((gate_grad_kernel<4, 1024>), grid, block, 0, s, p);
-        else if (hc == 2) hipLaunchKernelGGL((gate_grad_kernel<2, 1024>), grid, block, 0, s, p);
-        else if (hc == 1) hipLaunchKernelGGL((gate_grad_kernel<1, 1024>), grid, block, 0, s, p);
+        if (hc == 4 && threads > 640) hipLaunchKernelGGL((gate_grad_kernel<4, 1024, true>), grid, block, 0, s, p);
+        else if (hc == 4 && threads > 384) hipLaunchKernelGGL((gate_grad_kernel<4, 640, true>), grid, block, 0, s, p);
+        else if (hc == 4) hipLaunchKernelGGL((gate_grad_kernel<4, 384, false>), grid, block, 0, s, p);
+        else if (hc == 2) hipLaunchKernelGGL((gate_grad_kernel<2, 1024, false>), grid, block, 0, s, p);
+        else if (hc == 1) hipLaunchKernelGGL((gate_grad_kernel<1, 1024, false>), grid, block, 0, s, p);
         else hipLaunchKernelGGL(gate_grad_any_kernel, grid, block, 0, s, p);
     }
     const int cols = hc * dim;

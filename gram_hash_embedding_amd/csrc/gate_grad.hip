@@ -14,8 +14,13 @@
 // HBM-bound: per token (3 hc + 1) rows of dim are read and 2 hc + 1 written, every one once.  A workgroup holds a
 // whole token, one 16-byte piece of every row per thread: the rows stay in registers between the sums that need all
 // of a row and the outputs that need the sums, and the sum over tokens of dq and dk stays in registers over all of
-// the workgroup's tokens.  One barrier per token (the sums of the waves, in two LDS buffers taken in turn).  A second
-// launch adds the workgroups' sums in their order, so the same call gives the same bits.
+// the workgroup's tokens.  The next token's rows are asked for as this one's are used up, so loads are in flight over
+// the barrier (one per token: the sums of the waves, in two LDS buffers taken in turn).  A second launch adds the
+// workgroups' sums in their order, so the same call gives the same bits.
+//
+// 8,192 tokens, both launches: 4 copies of 5,120 335 us (5.5 TB/s of the bytes above), of 2,048 146 (5.0), of 1,024 84
+// (4.4), of 256 41 (2.2, bound by the tokens' chains of barrier and sums), of 8,192 633 (4.7); 2 of 5,120 193 (5.2), 1 of
+// 5,120 125 (4.7); 3 of 2,048 184 (3.1, the kernel for any count of copies, which takes a barrier a copy).
 #include <type_traits>
 
 #include "rows.h"
@@ -100,41 +105,59 @@ __device__ inline float wave_sum_last(float v) {
     return v;
 }
 
-// kLds: q * k in LDS (where a workgroup fills the CU); else read for every token from L2 (where other workgroups on the
-// CU hide that).
-template <int HC, int kMaxThreads, bool kLds>
+// The LDS holds q * k (read for every token from L2 it cost 428 us where this takes 342, 8,192 x 4 x 5,120); of a workgroup
+// of more than 640 threads and four copies, whose registers do not hold rows and sums together, the sums instead, and q
+// and k come from L2 a copy ahead.
+template <int HC, int kMaxThreads>
 __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) {
     constexpr int kSums = 3 * HC, kReads = (kSums + 3) / 4;
     __shared__ float sums[2][4 * kReads][kMaxWaves];  // [sum][wave]; waves the workgroup lacks hold zeros
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int piece = threadIdx.x;
     const bool live = piece < p.dim / 8;
-    __shared__ float weight[kLds ? HC : 1][kLds ? 2 : 1][kLds ? kMaxThreads * 4 : 1];  // [copy][half of a piece][4 each]
+    constexpr bool kSumsInLds = HC == 4 && kMaxThreads > 640;
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    __shared__ f32x4 held[HC][2][kMaxThreads];  // [copy][half of a piece][thread]: q * k, or the sums
     for (int i = threadIdx.x; i < 2 * 4 * kReads * kMaxWaves; i += blockDim.x) (&sums[0][0][0])[i] = 0.f;
-    auto weights = [&](int c, int at, float (&w)[8]) {
-        Piece<Bf16> qr, kw;
-        float kf[8];
+    auto put = [&](int c, const float (&w)[8]) {
+        held[c][0][piece] = f32x4{w[0], w[1], w[2], w[3]};
+        held[c][1][piece] = f32x4{w[4], w[5], w[6], w[7]};
+    };
+    auto get = [&](int c, float (&w)[8]) {
+        const f32x4 lo = held[c][0][piece], hi = held[c][1][piece];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[e] = lo[e];
+            w[4 + e] = hi[e];
+        }
+    };
+    Piece<Bf16> qr, kr_w;
+    auto load_weights = [&](int c) {
+        int at = c * (p.dim / 8) + piece;
+        asm volatile("" : "+v"(at));  // read here, not once for all tokens into registers held over them
         qr.load(p.q, at);
-        kw.load(p.k, at);
+        kr_w.load(p.k, at);
+    };
+    auto weights = [&](float (&w)[8]) {
+        float kf[8];
         qr.to(w);
-        kw.to(kf);
+        kr_w.to(kf);
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] *= kf[e];  // exact: bf16 * bf16 fits fp32
     };
-    typedef float f32x4 __attribute__((ext_vector_type(4)));
-    if constexpr (kLds) {
-        if (live) {
+    if (live) {
 #pragma unroll
-            for (int c = 0; c < HC; ++c) {
-                float w[8];
-                weights(c, c * (p.dim / 8) + piece, w);
-                reinterpret_cast<f32x4*>(weight[c][0])[piece] = f32x4{w[0], w[1], w[2], w[3]};
-                reinterpret_cast<f32x4*>(weight[c][1])[piece] = f32x4{w[4], w[5], w[6], w[7]};
+        for (int c = 0; c < HC; ++c) {
+            float w[8] = {};
+            if constexpr (!kSumsInLds) {
+                load_weights(c);
+                weights(w);
             }
+            put(c, w);
         }
     }
     __syncthreads();
-    float acc[HC][8] = {};
+    float acc[kSumsInLds ? 1 : HC][8] = {};
     Piece<Bf16> hr[HC], kr[HC], ur[HC], vr;
     auto load_copy = [&](int64_t t, int c) {
         hr[c].load_nt(p.x + (t * HC + c) * p.dim, piece);
@@ -184,6 +207,9 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) 
                 }
             }
         }
+        if constexpr (kSumsInLds) {
+            if (live) load_weights(0);
+        }
         __syncthreads();
         // the rows as they were loaded: widened again below rather than held as floats over the barrier
 #pragma unroll
@@ -210,19 +236,13 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) 
             Coef k = coef_of(p, total(3 * c), total(3 * c + 1), total(3 * c + 2), p.dot[t * HC + c]);
             k = Coef{uniform(k.g), uniform(k.a), uniform(k.bh), uniform(k.bk)};
             if (live) {
-                float w[8];
-                if constexpr (kLds) {
-                    const f32x4 lo = reinterpret_cast<const f32x4*>(weight[c][0])[piece];
-                    const f32x4 hi = reinterpret_cast<const f32x4*>(weight[c][1])[piece];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        w[e] = lo[e];
-                        w[4 + e] = hi[e];
-                    }
+                float w[8], sum[8];
+                if constexpr (kSumsInLds) {
+                    weights(w);
+                    if (c + 1 < HC) load_weights(c + 1);
+                    get(c, sum);
                 } else {
-                    int at = c * (p.dim / 8) + piece;
-                    asm volatile("" : "+v"(at));  // read anew for every token, not held in registers over them
-                    weights(c, at, w);
+                    get(c, w);
                 }
                 float h[8], key[8], u[8], ox[8], ok[8];
                 hr[c].to(h);
@@ -234,8 +254,11 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) 
                     ox[e] = u[e] + (aw * key[e] - k.bh * h[e]);
                     ok[e] = aw * h[e] - k.bk * key[e];
                     dv[e] += k.g * u[e];
-                    acc[c][e] += k.a * (h[e] * key[e]);
+                    const float add = k.a * (h[e] * key[e]);
+                    if constexpr (kSumsInLds) sum[e] += add;
+                    else acc[c][e] += add;
                 }
+                if constexpr (kSumsInLds) put(c, sum);
                 Piece<Bf16> o;
                 o.from(ox);
                 o.store_nt(p.dx + (t * HC + c) * p.dim, piece);
@@ -257,7 +280,13 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) 
 #pragma unroll
     for (int c = 0; c < HC; ++c) {
         Piece<F32> o;
-        o.from(acc[c]);
+        if constexpr (kSumsInLds) {
+            float sum[8];
+            get(c, sum);
+            o.from(sum);
+        } else {
+            o.from(acc[c]);
+        }
         o.store(p.part + (static_cast<int64_t>(blockIdx.x) * HC + c) * p.dim, piece);
     }
 }
@@ -349,13 +378,16 @@ __global__ __launch_bounds__(1024) void gate_grad_any_kernel(GateGradArgs p) {
     }
 }
 
-// dq = k * sum, dk = q * sum over the workgroups' sums: 64 columns per workgroup, 16 runs of rows.
+// dq = k * sum, dk = q * sum over the workgroups' sums: kCols columns per workgroup, 1024 / kCols runs of rows.  Bound by
+// the latency of its reads, eight in flight a thread.
+template <int kCols>
 __global__ __launch_bounds__(1024) void gate_grad_sum_kernel(const float* part, int rows, int cols, const uint16_t* q,
                                                              const uint16_t* k, float* dq, float* dk) {
-    __shared__ float run_sum[16][64];
-    const int col = blockIdx.x * 64 + (threadIdx.x & 63);
-    const int run = threadIdx.x >> 6;
-    const int per = (rows + 15) / 16;
+    constexpr int kRuns = 1024 / kCols;
+    __shared__ float run_sum[kRuns][kCols];
+    const int col = blockIdx.x * kCols + threadIdx.x % kCols;
+    const int run = threadIdx.x / kCols;
+    const int per = (rows + kRuns - 1) / kRuns;
     const int r0 = min(run * per, rows), r1 = min(r0 + per, rows);
     float s = 0.f;
     if (col < cols) {
@@ -367,14 +399,25 @@ __global__ __launch_bounds__(1024) void gate_grad_sum_kernel(const float* part, 
             for (int j = 0; j < 8; ++j) s += v[j];
         }
     }
-    run_sum[run][threadIdx.x & 63] = s;
+    run_sum[run][threadIdx.x % kCols] = s;
     __syncthreads();
     if (run != 0 || col >= cols) return;
     s = 0.f;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s += run_sum[r][threadIdx.x];
+    for (int r = 0; r < kRuns; ++r) s += run_sum[r][threadIdx.x];
     dq[col] = s * __uint_as_float(static_cast<uint32_t>(k[col]) << 16);
     dk[col] = s * __uint_as_float(static_cast<uint32_t>(q[col]) << 16);
+}
+
+template <int HC>
+void launch_gate_grad(const GateGradArgs& p, int64_t groups, int threads, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(groups)), block(threads);
+    if (threads <= 64) hipLaunchKernelGGL((gate_grad_kernel<HC, 64>), grid, block, 0, s, p);
+    else if (threads <= 128) hipLaunchKernelGGL((gate_grad_kernel<HC, 128>), grid, block, 0, s, p);
+    else if (threads <= 256) hipLaunchKernelGGL((gate_grad_kernel<HC, 256>), grid, block, 0, s, p);
+    else if (threads <= 384) hipLaunchKernelGGL((gate_grad_kernel<HC, 384>), grid, block, 0, s, p);
+    else if (threads <= 640) hipLaunchKernelGGL((gate_grad_kernel<HC, 640>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((gate_grad_kernel<HC, 1024>), grid, block, 0, s, p);
 }
 
 int threads_of(int dim) { return (dim / 8 + 63) / 64 * 64; }
@@ -447,16 +490,19 @@ extern "C" int engram_gate_output_backward(const uint16_t* x, const uint16_t* kv
     p.rsqrt_dim = static_cast<float>(1.0 / __builtin_sqrt(static_cast<double>(dim)));
     const int threads = threads_of(dim);
     if (T > 0) {
-        const dim3 grid(static_cast<unsigned>(groups)), block(threads);
-        if (hc == 4 && threads > 640) hipLaunchKernelGGL((gate_grad_kernel<4, 1024, true>), grid, block, 0, s, p);
-        else if (hc == 4 && threads > 384) hipLaunchKernelGGL((gate_grad_kernel<4, 640, true>), grid, block, 0, s, p);
-        else if (hc == 4) hipLaunchKernelGGL((gate_grad_kernel<4, 384, false>), grid, block, 0, s, p);
-        else if (hc == 2) hipLaunchKernelGGL((gate_grad_kernel<2, 1024, false>), grid, block, 0, s, p);
-        else if (hc == 1) hipLaunchKernelGGL((gate_grad_kernel<1, 1024, false>), grid, block, 0, s, p);
-        else hipLaunchKernelGGL(gate_grad_any_kernel, grid, block, 0, s, p);
+        if (hc == 4) launch_gate_grad<4>(p, groups, threads, s);
+        else if (hc == 2) launch_gate_grad<2>(p, groups, threads, s);
+        else if (hc == 1) launch_gate_grad<1>(p, groups, threads, s);
+        else hipLaunchKernelGGL(gate_grad_any_kernel, dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s, p);
     }
     const int cols = hc * dim;
-    hipLaunchKernelGGL(gate_grad_sum_kernel, dim3((cols + 63) / 64), dim3(1024), 0, s, p.part, static_cast<int>(groups), cols,
-                       q_weight, k_weight, dq, dk);
+    // few columns: fewer of them per workgroup, so that there are workgroups enough
+    const int rows = static_cast<int>(groups);
+    if (cols >= 64 * kCUs)
+        hipLaunchKernelGGL(gate_grad_sum_kernel<64>, dim3((cols + 63) / 64), dim3(1024), 0, s, p.part, rows, cols, q_weight,
+                           k_weight, dq, dk);
+    else
+        hipLaunchKernelGGL(gate_grad_sum_kernel<16>, dim3((cols + 15) / 16), dim3(1024), 0, s, p.part, rows, cols, q_weight,
+                           k_weight, dq, dk);
     return check_launch(what);
 }

@@ -10,8 +10,8 @@
 //
 // Sort: least significant digit first, 8 bytes (row, position) per element, digits of at most kMaxDigitBits bits over
 // the bits that rows actually have, so the fewest passes (17 bits of a token vocabulary: two, 29 bits of a 384 M row
-// table: three).  A pass counts the digits per tile, then every workgroup ranks a tile of kSortTile elements (per wave by ballots over
-// the digit's bits, so stable), adds the tiles before it from the table of per-tile digit counts, and scatters.
+// table: three).  A pass counts the digits per tile, then every workgroup ranks a tile of elements (per wave by ballots over the
+// digit's bits, so stable), adds the tiles before it from the table of per-tile digit counts, and scatters.
 //
 // Fold: the sorted positions are cut into chunks of kChunk; a group of lanes adds a segment's positions within a chunk
 // in registers and writes the table row if the segment ends there.  A segment that crosses chunks leaves fp32 partial
@@ -25,14 +25,17 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kSortItems = 8;
-constexpr int kSortTile = kSortThreads * kSortItems;
+// ids per thread, and so per tile: few for up to this many ids, which else make too few workgroups (24,000 ids of 29 bits
+// 61 -> 53 us, 72,000 69 -> 62, 196,608 of 22 bits 70 -> 66, 480,000 of 29 bits 122 -> 117; 1,572,864 220 -> 229)
+constexpr int kFewItems = 4, kManyItems = 8;
+constexpr int64_t kFewIds = 1 << 19;
 constexpr int kMaxDigitBits = 11;
 constexpr int kMaxDigits = 1 << kMaxDigitBits;
 // up to this many tiles every scattering workgroup adds the digit counts of the tiles before it by itself; past it a
 // launch of its own turns the counts into prefixes
 constexpr int kDirectTiles = 64;
 constexpr int kChunk = 16;   // sorted positions per chunk of the fold
+constexpr int kHeadsTile = kThreads * kChunk;  // sorted positions per workgroup that counts distinct rows
 constexpr int64_t kMaxIds = 1ll << 30;
 constexpr int64_t kMaxGridX = 1ll << 23;  // workgroups along x: x * threads stays below 2^32
 constexpr int kSmall = 1024;              // up to this many ids one launch sorts and folds
@@ -168,7 +171,7 @@ struct SortArgs {
     int64_t row_start;
     uint32_t R;
     uint32_t n;
-    const Pair* in;    // later passes
+    const Pair* in;    // later passes; null: the first
     Pair* out;
     uint32_t* hist;    // [tiles][digits] this pass's digit counts per tile (or their prefixes over the tiles)
     uint32_t* totals;  // [digits], with prefixes
@@ -190,7 +193,7 @@ __device__ inline uint32_t load_key(const SortArgs& a, uint32_t i) {
 // A pass's digit counts per tile; the first pass's workgroups behind the tiles write the dense form's zeros (skipping the
 // rows that will be written costs more than it saves: a byte per row looked up before each store took 520 us for the
 // 385 us of stores).
-template <bool kFirst>
+template <bool kFirst, int kItems>
 __global__ __launch_bounds__(kSortThreads) void hist_kernel(SortArgs a, Zeros z) {
     __shared__ uint32_t h[kMaxDigits];
     if (kFirst && static_cast<int>(blockIdx.x) >= a.tiles) {
@@ -200,9 +203,9 @@ __global__ __launch_bounds__(kSortThreads) void hist_kernel(SortArgs a, Zeros z)
     const int digits = 1 << a.bits;
     for (int d = threadIdx.x; d < digits; d += kSortThreads) h[d] = 0;
     __syncthreads();
-    const uint32_t base = blockIdx.x * kSortTile + threadIdx.x;
+    const uint32_t base = blockIdx.x * (kSortThreads * kItems) + threadIdx.x;
 #pragma unroll
-    for (int u = 0; u < kSortItems; ++u) {
+    for (int u = 0; u < kItems; ++u) {
         const uint32_t i = base + u * kSortThreads;
         if (i < a.n) atomicAdd(&h[((kFirst ? load_key(a, i) : a.in[i].key) >> a.shift) & (digits - 1)], 1u);
     }
@@ -260,9 +263,9 @@ __device__ inline void load_counts(const uint32_t* p, uint32_t (&v)[kPer]) {
 }
 
 // kPer: digits per thread (digits = kPer * kSortThreads, or fewer than kSortThreads with kPer 1)
-template <bool kFirst, int kPer>
+template <bool kFirst, int kItems, int kPer>
 __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
-    constexpr int kDigits = kPer * kSortThreads;
+    constexpr int kDigits = kPer * kSortThreads, kSortTile = kSortThreads * kItems;
     __shared__ uint16_t cnt[kSortWaves][kDigits];
     __shared__ uint32_t move[kDigits];  // a digit's elements: their place in the output less that in the tile
     __shared__ Pair tile[kSortTile];    // the tile in order of the digit
@@ -272,12 +275,12 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
     const uint32_t mask_bits = static_cast<uint32_t>(digits - 1);
     for (int d = threadIdx.x; d < kSortWaves * kDigits / 2; d += kSortThreads) reinterpret_cast<uint32_t*>(cnt)[d] = 0;
 
-    // the wave's kSortItems * 64 consecutive elements
-    Pair e[kSortItems];
-    uint32_t rank[kSortItems];
-    const uint32_t first = blockIdx.x * kSortTile + wave * (64 * kSortItems) + lane;
+    // the wave's kItems * 64 consecutive elements
+    Pair e[kItems];
+    uint32_t rank[kItems];
+    const uint32_t first = blockIdx.x * kSortTile + wave * (64 * kItems) + lane;
 #pragma unroll
-    for (int u = 0; u < kSortItems; ++u) {
+    for (int u = 0; u < kItems; ++u) {
         const uint32_t i = first + u * 64;
         e[u] = Pair{0, i};
         if (i < a.n) {
@@ -313,7 +316,7 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
     volatile uint16_t* mine = cnt[wave];  // this wave's counters: its LDS accesses stay in program order
     const uint64_t below = (1ull << lane) - 1;
 #pragma unroll
-    for (int u = 0; u < kSortItems; ++u) {
+    for (int u = 0; u < kItems; ++u) {
         const bool live = first + u * 64 < a.n;
         const uint32_t d = (e[u].key >> a.shift) & mask_bits;
         uint64_t same = __ballot(live);
@@ -373,14 +376,14 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
     __syncthreads();
     // through LDS in the digit's order, so that the stores of neighbouring lanes fall into the same lines
 #pragma unroll
-    for (int u = 0; u < kSortItems; ++u) {
+    for (int u = 0; u < kItems; ++u) {
         if (first + u * 64 >= a.n) continue;
         tile[cnt[wave][(e[u].key >> a.shift) & mask_bits] + rank[u]] = e[u];
     }
     __syncthreads();
     const uint32_t here = min(a.n - blockIdx.x * kSortTile, static_cast<uint32_t>(kSortTile));
 #pragma unroll
-    for (int u = 0; u < kSortItems; ++u) {
+    for (int u = 0; u < kItems; ++u) {
         const uint32_t i = threadIdx.x + u * kSortThreads;
         if (i >= here) continue;
         const Pair x = tile[i];
@@ -388,13 +391,28 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
     }
 }
 
-template <bool kFirst>
+template <bool kFirst, int kItems>
 void launch_scatter(const SortArgs& a, hipStream_t stream) {
     const dim3 grid(a.tiles), block(kSortThreads);
     const int digits = 1 << a.bits;
-    if (digits > 2 * kSortThreads) hipLaunchKernelGGL((scatter_kernel<kFirst, 4>), grid, block, 0, stream, a);
-    else if (digits > kSortThreads) hipLaunchKernelGGL((scatter_kernel<kFirst, 2>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((scatter_kernel<kFirst, 1>), grid, block, 0, stream, a);
+    if (digits > 2 * kSortThreads) hipLaunchKernelGGL((scatter_kernel<kFirst, kItems, 4>), grid, block, 0, stream, a);
+    else if (digits > kSortThreads) hipLaunchKernelGGL((scatter_kernel<kFirst, kItems, 2>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((scatter_kernel<kFirst, kItems, 1>), grid, block, 0, stream, a);
+}
+
+// one pass over the digit: its counts per tile, their prefixes where the tiles are many, and the scatter
+template <int kItems>
+void launch_pass(SortArgs& a, uint32_t* totals, const Zeros& z, hipStream_t stream) {
+    const dim3 block(kSortThreads);
+    const dim3 grid(static_cast<unsigned>(a.tiles + (z.n16 + kSortThreads - 1) / kSortThreads));
+    if (a.in) hipLaunchKernelGGL((hist_kernel<false, kItems>), grid, block, 0, stream, a, z);
+    else hipLaunchKernelGGL((hist_kernel<true, kItems>), grid, block, 0, stream, a, z);
+    if (a.tiles > kDirectTiles) {
+        a.totals = totals;
+        hipLaunchKernelGGL(prefix_kernel, dim3(((1 << a.bits) + 63) / 64), dim3(1024), 0, stream, a);
+    }
+    if (a.in) launch_scatter<false, kItems>(a, stream);
+    else launch_scatter<true, kItems>(a, stream);
 }
 
 // ---------------------------------------------------------------------------------------------------------------------
@@ -413,7 +431,7 @@ struct FoldArgs {
     int64_t* unique;    // [n], or null: the dense form
     int32_t* count;     // [1]
     int64_t row_start;
-    uint32_t* heads;       // [tiles] distinct rows that begin in each tile of kSortTile sorted positions
+    uint32_t* heads;       // [tiles] distinct rows that begin in each kHeadsTile sorted positions
     uint32_t* chunk_base;  // [chunks] of those, the ones before the chunk
     int tiles;
     uint32_t chunks;
@@ -425,10 +443,8 @@ struct FoldArgs {
 
 // Distinct rows per chunk (before it in its tile) and per tile.
 __global__ __launch_bounds__(kThreads) void heads_kernel(FoldArgs a) {
-    constexpr int kPerTile = kSortTile / kChunk;
-    static_assert(kPerTile == kThreads, "one chunk per thread");
     __shared__ uint32_t wsum[kThreads / 64];
-    const uint32_t chunk = blockIdx.x * kPerTile + threadIdx.x;
+    const uint32_t chunk = blockIdx.x * kThreads + threadIdx.x;
     const uint32_t s = chunk * kChunk;
     uint32_t c = 0;
     if (s < a.n) {
@@ -555,7 +571,7 @@ __global__ __launch_bounds__(kOneThreads, 8) void one_sort_kernel(SortArgs a, Fo
     if (!f.unique) return;
     // distinct rows that begin before each chunk in its tile, and in each tile
     static_assert(kChunk == 2 * kOneItems, "a chunk per two threads");
-    constexpr int kPerTile = kSortTile / kOneItems;  // threads
+    constexpr int kPerTile = kHeadsTile / kOneItems;  // threads
     const uint32_t s = tid * kOneItems;
     uint32_t heads = 0, prev = s && s < a.n ? tile[s - 1].key : 0xFFFFFFFFu;
 #pragma unroll
@@ -567,7 +583,7 @@ __global__ __launch_bounds__(kOneThreads, 8) void one_sort_kernel(SortArgs a, Fo
     const uint32_t before = scan(heads);
     uint32_t* tile_base = reinterpret_cast<uint32_t*>(cnt);
     if (tid % kPerTile == 0) tile_base[tid / kPerTile] = before;
-    if (tid == kOneThreads - 1) tile_base[kOneSort / kSortTile] = before + heads;
+    if (tid == kOneThreads - 1) tile_base[kOneSort / kHeadsTile] = before + heads;
     __syncthreads();
     const int t = tid / kPerTile;
     if (tid % 2 == 0 && static_cast<uint32_t>(tid / 2) < f.chunks) f.chunk_base[tid / 2] = before - tile_base[t];
@@ -608,7 +624,7 @@ __device__ inline void put_row(const FoldArgs& a, uint32_t key, uint32_t u, int 
 // 64 bf16).
 template <class GT, class OT, int LPR, bool kPast>
 __global__ __launch_bounds__(kThreads) void fold_kernel(FoldArgs a) {
-    constexpr int kGroups = kThreads / LPR, kPerTile = kSortTile / kChunk;
+    constexpr int kGroups = kThreads / LPR, kPerTile = kHeadsTile / kChunk;
     constexpr int kBatch = GT::kBytes == 2 ? kChunk : kChunk / 2;  // rows in flight
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / LPR;
     const uint32_t chunk = static_cast<uint32_t>(unit / a.cols);
@@ -910,7 +926,7 @@ int bits_of(uint32_t v) { return v ? 32 - __builtin_clz(v) : 1; }
 
 struct Plan {
     int bits, passes;      // digit bits and passes
-    int tiles;
+    int items, tiles, head_tiles;
     uint32_t chunks;
     int64_t pairs, hist, totals, heads, chunk_base, leave_to, leave, enter, bytes;  // offsets
 };
@@ -922,7 +938,9 @@ Plan plan_of(int64_t n, int32_t D, int64_t R) {
     const int key_bits = bits_of(static_cast<uint32_t>(R));  // the key R stands for ids outside
     p.passes = (key_bits + kMaxDigitBits - 1) / kMaxDigitBits;
     p.bits = (key_bits + p.passes - 1) / p.passes;
-    p.tiles = static_cast<int>((n + kSortTile - 1) / kSortTile);
+    p.items = n <= kFewIds ? kFewItems : kManyItems;
+    p.tiles = static_cast<int>((n + p.items * kSortThreads - 1) / (p.items * kSortThreads));
+    p.head_tiles = static_cast<int>((n + kHeadsTile - 1) / kHeadsTile);
     p.chunks = static_cast<uint32_t>((n + kChunk - 1) / kChunk);
     int64_t at = 0;
     p.pairs = at;
@@ -932,7 +950,7 @@ Plan plan_of(int64_t n, int32_t D, int64_t R) {
     p.totals = at;
     at += up16(4ll << p.bits);
     p.heads = at;
-    at += up16(4ll * p.tiles);
+    at += up16(4ll * p.head_tiles);
     p.chunk_base = at;
     at += up16(4ll * p.chunks);
     p.leave_to = at;
@@ -963,20 +981,14 @@ const Pair* sort_ids(const Plan& p, const void* ids, int id_bytes, int64_t n, in
     // (what a grid does not hold, 1 TB and more, in a launch of its own)
     const int64_t n16 = zeros / 16, most = (kMaxGridX / 2 - p.tiles) * kSortThreads;
     const Zeros z = {static_cast<u32x4*>(zero), n16 < most ? n16 : most};
-    const dim3 grid(static_cast<unsigned>(p.tiles + (z.n16 + kSortThreads - 1) / kSortThreads));
     if (n16 > most) launch_zero(z.p + most, (n16 - most) * 16, stream, "engram_embed_grad");
+    uint32_t* totals = reinterpret_cast<uint32_t*>(ws + p.totals);
     for (int q = 0; q < p.passes; ++q) {
         a.shift = q * p.bits;
-        a.in = buf[(q + 1) & 1];
+        a.in = q ? buf[(q + 1) & 1] : nullptr;
         a.out = buf[q & 1];
-        if (q == 0) hipLaunchKernelGGL(hist_kernel<true>, grid, dim3(kSortThreads), 0, stream, a, z);
-        else hipLaunchKernelGGL(hist_kernel<false>, dim3(p.tiles), dim3(kSortThreads), 0, stream, a, Zeros{});
-        if (p.tiles > kDirectTiles) {
-            a.totals = reinterpret_cast<uint32_t*>(ws + p.totals);
-            hipLaunchKernelGGL(prefix_kernel, dim3(((1 << p.bits) + 63) / 64), dim3(1024), 0, stream, a);
-        }
-        if (q == 0) launch_scatter<true>(a, stream);
-        else launch_scatter<false>(a, stream);
+        if (p.items == kFewItems) launch_pass<kFewItems>(a, totals, q ? Zeros{} : z, stream);
+        else launch_pass<kManyItems>(a, totals, q ? Zeros{} : z, stream);
     }
     return buf[(p.passes - 1) & 1];
 }
@@ -1164,7 +1176,7 @@ int embed_grad(FoldArgs& f, const void* ids, int32_t id_bytes, int64_t n, int64_
         return fail(ENGRAM_ERANGE, "%s: workspace of %lld bytes, needs %lld", what, (long long)workspace_bytes,
                     (long long)p.bytes);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    f.tiles = p.tiles;
+    f.tiles = p.head_tiles;
     f.chunks = p.chunks;
     f.heads = reinterpret_cast<uint32_t*>(ws + p.heads);
     f.chunk_base = reinterpret_cast<uint32_t*>(ws + p.chunk_base);
@@ -1175,7 +1187,7 @@ int embed_grad(FoldArgs& f, const void* ids, int32_t id_bytes, int64_t n, int64_
         f.sorted = one_sort(p, ids, id_bytes, n, C, stride, R, row_start, ws, f, fill ? bytes : 0, s);
     } else {
         f.sorted = sort_ids(p, ids, id_bytes, n, C, stride, R, row_start, ws, f.out, fill ? bytes : 0, s);
-        if (f.unique) hipLaunchKernelGGL(heads_kernel, dim3(p.tiles), dim3(kThreads), 0, s, f);
+        if (f.unique) hipLaunchKernelGGL(heads_kernel, dim3(p.head_tiles), dim3(kThreads), 0, s, f);
     }
     return launch_fold_types(f, nullptr, past, up_dtype, out_dtype, s, what);
 }

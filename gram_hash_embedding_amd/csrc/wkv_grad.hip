@@ -5,15 +5,20 @@
 //
 // Both are products on v_mfma_f32_16x16x32_bf16 with fp32 accumulation.  Neither has both operands contiguous along
 // the reduced axis, which is what the instruction's lanes take: W of da and both operands of dW have it as their rows.
-// Such an operand's slab (64 rows of the reduced axis, 256 columns) goes into LDS as it lies in memory and is turned
-// on the way to the registers by ds_read_b64_tr_b16 (within 16 lanes, lane i supplies the address of four elements,
-// row i / 4, columns 4 (i % 4) .. + 3, and receives column i of the four rows: lane layout measured on gfx950), so
-// nothing is transposed in memory.  Its rows of 512 bytes are swizzled by 32-byte blocks (block b of row k at b XOR
-// (k % 4 + 4 ((k / 8) % 4))): the sixteen rows that one read touches then lie in sixteen different blocks.
+// Such an operand's slab (64 rows of the reduced axis) goes into LDS as it lies in memory and is turned on the way to the
+// registers by ds_read_b64_tr_b16 (within 16 lanes, lane i supplies the address of four elements, row i / 4, columns
+// 4 (i % 4) .. + 3, and receives column i of the four rows: lane layout measured on gfx950), so nothing is transposed in
+// memory.  Its rows are swizzled by 32-byte blocks, so that the rows that one read touches lie in different blocks.
 //
-// A workgroup (eight waves) makes a 256 x 256 tile of the output, 128 x 64 per wave, from slabs of 64 of the reduced
-// axis in two stages of LDS filled by direct-to-LDS loads.  Where the tiles are fewer than the CUs the reduced axis is
-// split over workgroups, whose fp32 partial tiles a second launch adds in order.  da and dW of a call are one launch.
+// A workgroup makes a 256 x 256 tile of the output (eight waves, 128 x 64 each) or, where the work is little, 128 x 128
+// (four waves, 64 x 64 each, two workgroups a CU), from slabs of 64 of the reduced axis in two stages of LDS filled by
+// direct-to-LDS loads.  Where the tiles are fewer than the CUs the reduced axis is split over workgroups, whose fp32
+// partial tiles a second launch adds in order.  da and dW of a call are one launch, the shorter reductions behind the
+// longer ones.
+//
+// Bound by the matrix cores where T is long: 8,192 x 1,536 x 25,600, both products, 1,053 us, 1.22 PFLOP/s (a large square
+// library product reaches 1.45-1.55 here; da alone 606 us, dW 584).  Below some 1,000 tokens by memory: W read and dW
+// written, 250 MB at 251 tokens in 105 us (da 47, dW 46: da waits on its slabs, one of which is in flight per workgroup).
 #include <type_traits>
 
 #include "rows.h"
@@ -22,7 +27,6 @@ namespace engram {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -44,7 +48,7 @@ struct Prod {
     float* part;        // [splits][M, N] when splits > 1
     int out_f32, accumulate;
     int tiles_m, tiles_n, splits, slabs;
-    int64_t units() const { return static_cast<int64_t>(tiles_m) * tiles_n * splits; }
+    __host__ __device__ int64_t units() const { return static_cast<int64_t>(tiles_m) * tiles_n * splits; }
 };
 struct GradArgs {
     Prod da, dw;
@@ -88,8 +92,11 @@ __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* ld
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave & 1, wn = wave >> 1;
     const int tiles = g.tiles_m * g.tiles_n;
-    const int split = static_cast<int>(unit / tiles);
-    const int tile = static_cast<int>(xcd_order(unit - static_cast<int64_t>(split) * tiles, tiles));
+    // an XCD takes whole parts of a split reduction, whose tiles read the same rows of P and Q (2,048 x 1,536 x 25,600 313
+    // -> 298 us against each part's tiles over all XCDs)
+    const int64_t at_unit = xcd_order(unit, g.units());
+    const int split = static_cast<int>(at_unit / tiles);
+    const int tile = static_cast<int>(at_unit - static_cast<int64_t>(split) * tiles);
     const int tm = tile / g.tiles_n, tn = tile - tm * g.tiles_n;
     const int64_t m0 = static_cast<int64_t>(tm) * TS, n0 = static_cast<int64_t>(tn) * TS;
     const int s0 = static_cast<int>(static_cast<int64_t>(g.slabs) * split / g.splits);
@@ -264,24 +271,39 @@ __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* ld
     if (TS == 128 || wave < 4) run(std::true_type{});
     else run(std::false_type{});
 
-    // ---- lane l holds, per block, output row l % 16 and the columns 4 (l / 16) .. + 3
-    const int64_t mrow = m0 + wm * (TS / 2) + (lane & 15), ncol = n0 + wn * 64 + 4 * (lane >> 4);
+    // ---- lane l holds, per block of 16 rows, row l % 16 and the columns 16 j + 4 (l / 16) .. + 3.  Through 4 KB of LDS per
+    // wave (16-byte pieces swizzled by the row), so that 16 lanes store a row's 64 columns; stores of finished tiles past
+    // the caches.  dW alone, 251 x 1,536 x 25,600: 66 us from the registers, 59 through LDS, 46 past the caches.
+    sync();
+    uint8_t* mine = lds + wave * 4096;
+    const int64_t n = n0 + wn * 64 + 4 * (lane & 15);
 #pragma unroll
     for (int i = 0; i < PB; ++i) {
-        const int64_t m = mrow + 16 * i;
-        if (m >= g.M) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = ncol + 16 * j;
-            if (n >= g.N) continue;
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<f32x4*>(mine + (lane & 15) * 256 + (((4 * j + (lane >> 4)) ^ (lane & 15)) << 4)) = acc[i][j];
+        __builtin_amdgcn_wave_barrier();
+        asm volatile("" ::: "memory");
+        f32x4 rows[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int row = 4 * k + (lane >> 4);
+            rows[k] = *reinterpret_cast<const f32x4*>(mine + row * 256 + (((lane & 15) ^ row) << 4));
+        }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t m = m0 + wm * (TS / 2) + 16 * i + 4 * k + (lane >> 4);
+            if (m >= g.M || n >= g.N) continue;
             const int64_t at = m * g.N + n;
-            f32x4 v = acc[i][j];
+            f32x4 v = rows[k];
             if (g.splits > 1) {
                 *reinterpret_cast<f32x4*>(g.part + split * g.M * g.N + at) = v;
             } else if (g.out_f32) {
                 f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + at);
                 if (g.accumulate) v += *o;
-                *o = v;
+                __builtin_nontemporal_store(v, o);
             } else {
                 u32x2* o = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(g.out) + at);
                 if (g.accumulate) {
@@ -289,7 +311,7 @@ __device__ __forceinline__ void product(const Prod& g, int64_t unit, uint8_t* ld
                     v += f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u),
                                __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u)};
                 }
-                *o = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                __builtin_nontemporal_store(u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}, o);
             }
         }
     }

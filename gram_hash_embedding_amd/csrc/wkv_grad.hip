@@ -18,7 +18,7 @@
 //
 // Bound by the matrix cores where T is long: 8,192 x 1,536 x 25,600, both products, 1,053 us, 1.22 PFLOP/s (a large square
 // library product reaches 1.45-1.55 here; da alone 606 us, dW 584).  Below some 1,000 tokens by memory: W read and dW
-// written, 250 MB at 251 tokens in 105 us (da 47, dW 46: da waits on its slabs, one of which is in flight per workgroup).
+// written, 250 MB at 251 tokens in 85 us (da alone 47, dW 45: da waits on its slabs, one of which is in flight per workgroup).
 #include <type_traits>
 
 #include "rows.h"
@@ -408,9 +408,9 @@ void split_alone(Prod& p, int size) {
 }
 
 // Both in a launch: parts no longer than a workgroup's share of all the work, the other product's units fill in beside
-// them.  A unit costs kUnitSlabs slabs more than it has (its first loads and its stores).  Measured against parts that
-// fill the room: 251 x 1,536 x 25,600 97 -> 82 us, 1,024 tokens 199 -> 188, 2,048 340 -> 322.
-constexpr int64_t kUnitSlabs = 5;
+// them.  A unit costs about kUnitSlabs slabs more than it has (its first loads and its stores).  us with 0, 2, 5 and 10:
+// 251 x 1,536 x 25,600 82, 85, 92, over 100; 512 115, 110, 118, 131; 2,000 x 1,536 x 5,120 in 256 x 256 tiles 109, 92.
+constexpr int64_t kUnitSlabs = 2;
 void split_both(Prod& a, Prod& b, int size) {
     const int64_t ta = static_cast<int64_t>(a.tiles_m) * a.tiles_n, tb = static_cast<int64_t>(b.tiles_m) * b.tiles_n;
     const int64_t share = (ta * (a.slabs + kUnitSlabs) + tb * (b.slabs + kUnitSlabs)) / room_of(size) + 1;
@@ -418,11 +418,12 @@ void split_both(Prod& a, Prod& b, int size) {
     b.splits = at_most((b.slabs + share - 1) / share, b);
 }
 
-int tile_size(int64_t T, int32_t K, int32_t Nout) {
-    // 128 x 128 tiles for little work: more workgroups, and two of them a CU.  us with 128 and 256: 251 x 1,536 x 25,600 85
-    // and 98, 400 119 and 108, 512 121 and 118; 2,000 x 1,536 x 5,120 81 and 98, 4,000 136 and 137; 8,192 x 456 x 2,000 47
-    // and 52, x 7,864 136 and 122.
-    return 2.0 * T * K * Nout < 3.2e10 ? 128 : 256;
+int tile_size(int64_t T, int32_t K, int32_t Nout, bool both) {
+    // 128 x 128 tiles for little work: more workgroups, and two of them a CU.  us with 128 and 256, both products: 64 x 1,536
+    // x 25,600 64 and 66, 251 96 and 85, 512 140 and 110; 251 x 1,536 x 5,120 27 and 27, 1,000 51 and 42, 2,000 83 and 92,
+    // 4,000 147 and 151; 8,000 x 456 x 2,000 47 and 51.  dW alone: 251 x 1,536 x 25,600 45 and 51, 400 54 and 59, 700 70 and
+    // 74 (da 77 and 71); 2,000 x 1,536 x 5,120 38 and 53 (da 51 and 46).
+    return 2.0 * T * K * Nout < (both ? 1.5e10 : 3.2e10) ? 128 : 256;
 }
 
 int64_t part_bytes(const Prod& p) { return p.splits > 1 ? p.splits * p.M * p.N * 4 : 0; }
@@ -441,13 +442,14 @@ extern "C" int64_t engram_wkv_backward_workspace_bytes(int64_t T, int32_t K, int
     if (!shape_ok(T, K, Nout)) return -1;
     if (T == 0) return 0;
     // what the call asking for both, or for either, needs at most
-    const int size = tile_size(T, K, Nout);
+    int size = tile_size(T, K, Nout, true);
     Prod da = prod_of(T, K, Nout, size), dw = prod_of(Nout, K, T, size);
     split_both(da, dw, size);
     int64_t need = part_bytes(da) + part_bytes(dw);
-    for (Prod* p : {&da, &dw}) {
-        split_alone(*p, size);
-        need = part_bytes(*p) > need ? part_bytes(*p) : need;
+    size = tile_size(T, K, Nout, false);
+    for (Prod p : {prod_of(T, K, Nout, size), prod_of(Nout, K, T, size)}) {
+        split_alone(p, size);
+        need = part_bytes(p) > need ? part_bytes(p) : need;
     }
     return need;
 }
@@ -474,7 +476,7 @@ extern "C" int engram_wkv_backward(const uint16_t* dkv, const uint16_t* a, const
         if (!dw || accumulate) return ENGRAM_OK;
         return launch_zero(dw, static_cast<int64_t>(Nout) * K * (dw_dtype == ENGRAM_F32 ? 4 : 2), s, what);
     }
-    const int size = tile_size(T, K, Nout);
+    const int size = tile_size(T, K, Nout, da && dw);
     GradArgs g = {};
     if (da) {
         g.da = prod_of(T, K, Nout, size);

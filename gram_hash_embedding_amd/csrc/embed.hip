@@ -10,13 +10,19 @@
 //
 // Sort: least significant digit first, 8 bytes (row, position) per element, digits of at most kMaxDigitBits bits over
 // the bits that rows actually have, so the fewest passes (17 bits of a token vocabulary: two, 29 bits of a 384 M row
-// table: three).  A pass counts the digits per tile, then every workgroup ranks a tile of elements (per wave by ballots over the
-// digit's bits, so stable), adds the tiles before it from the table of per-tile digit counts, and scatters.
+// table: three).  A pass counts the digits per tile, then every workgroup ranks a tile of elements (per wave by ballots
+// over the digit's bits, so stable), adds the tiles before it from the table of per-tile digit counts, and scatters.
+// Up to 8,192 ids one workgroup does all of it, up to 1,024 every workgroup does and folds too.
 //
 // Fold: the sorted positions are cut into chunks of kChunk; a group of lanes adds a segment's positions within a chunk
 // in registers and writes the table row if the segment ends there.  A segment that crosses chunks leaves fp32 partial
 // sums (one leaving a chunk, one entering) which a last launch adds in a fixed order, so that one hot row costs no more
 // than many cold ones.
+//
+// Measured: the lookup of 65,536 rows of 5,120 bf16 140 us (808 MB, 5.8 TB/s); the dense gradient of 8,192 such rows over
+// 129,280 table rows in fp32 465 us (2.73 GB, 5.9 TB/s: 418 the zeros with the sort beneath them, 38 the fold, 8 the
+// join); the distinct rows of 1,572,864 hashed ids of 64 220 us (629 MB: 71 the sort, 8 the counts, 121 the fold, 15 the
+// join and the tail), of 196,608 ids 65 us, bound by its nine launches at 4 to 9 us each.
 #include "rows.h"
 
 namespace engram {
@@ -213,7 +219,8 @@ __global__ __launch_bounds__(kSortThreads) void hist_kernel(SortArgs a, Zeros z)
     for (int d = threadIdx.x; d < digits; d += kSortThreads) a.hist[blockIdx.x * digits + d] = h[d];
 }
 
-// hist[tile][digit] into the counts of the tiles before, and the totals: 64 digits per workgroup, 16 runs of tiles.
+// hist[tile][digit] into the counts of the tiles before, and the totals: 64 digits per workgroup, 16 runs of tiles, eight
+// loads in flight a thread (96 tiles 4.4 us, 384 8.9, of which a launch alone is 4).
 __global__ __launch_bounds__(1024) void prefix_kernel(SortArgs a) {
     __shared__ uint32_t part[16][64];
     const int digits = 1 << a.bits;
@@ -262,6 +269,7 @@ __device__ inline void load_counts(const uint32_t* p, uint32_t (&v)[kPer]) {
     }
 }
 
+// Bound by latency, not by its 16 bytes an element: 196,608 elements 9 us, 1,572,864 12 to 16.
 // kPer: digits per thread (digits = kPer * kSortThreads, or fewer than kSortThreads with kPer 1)
 template <bool kFirst, int kItems, int kPer>
 __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
@@ -441,7 +449,7 @@ struct FoldArgs {
     uint32_t join_blocks;  // workgroups that join; those behind them write the rows form's tail
 };
 
-// Distinct rows per chunk (before it in its tile) and per tile.
+// Distinct rows per chunk (before it in its tile) and per tile: a chunk a thread.  196,608 positions 4.6 us, 1,572,864 8.2.
 __global__ __launch_bounds__(kThreads) void heads_kernel(FoldArgs a) {
     __shared__ uint32_t wsum[kThreads / 64];
     const uint32_t chunk = blockIdx.x * kThreads + threadIdx.x;
@@ -816,7 +824,8 @@ __global__ __launch_bounds__(kThreads) void join_kernel(FoldArgs a) {
 
 // Up to kSmall ids: every workgroup sorts them in LDS (a bitonic network over (row, position)) and folds its share of
 // (distinct row, column block) units, one group of LPR lanes each; the units past the last distinct row are the rows
-// form's tail.  One launch instead of six or more: at these sizes the launches are the time.
+// form's tail.  One launch instead of six or more: at these sizes the launches are the time (64 ids of 256 columns
+// over 1,000 rows 13 us, where the launches over tiles took 27).
 struct SmallArgs {
     SortArgs ids;
     FoldArgs fold;

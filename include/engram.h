@@ -580,7 +580,8 @@ int engram_embed(const void* ids, int32_t id_bytes, int64_t n, const void* table
  * up         [T*C, D] of up_dtype, the gradient of the looked-up rows; 16-byte aligned
  * grad       [R, D] of grad_dtype, out (in/out with accumulate); 16-byte aligned
  * workspace  engram_embed_grad_workspace_bytes(T*C, D, R) bytes, 16-byte aligned,
- *            caller-owned scratch (no initialisation needed)
+ *            caller-owned scratch (no initialisation needed); may be NULL where that
+ *            is 0 (few ids)
  * Limits: T >= 0, 1 <= C <= 1024, T*C <= 2^30; 1 <= R < 2^31; D a multiple of 8 in
  * [8, 65536].  Too small a workspace -> ENGRAM_ERANGE.
  */

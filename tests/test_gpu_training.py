@@ -403,7 +403,8 @@ def _guarded(t, device):
 @pytest.mark.parametrize("dwt", [F32, BF])
 @pytest.mark.parametrize("T,K,N", [
     (1, 8, 8), (3, 72, 200), (64, 192, 1280), (63, 64, 264), (65, 264, 72), (257, 264, 520), (300, 1536, 512), (251, 128, 2056),
-    (1000, 40, 1304), (2049, 256, 256), (5000, 64, 64)])
+    (1000, 40, 1304), (2049, 256, 256), (5000, 64, 64),
+    (700, 1032, 12552), (1003, 1544, 10616)])  # the larger tiles: both products in a launch, and alone too
 def test_wkv_backward(gpu_device, T, K, N, dwt):
     g = _eng()
     gen = torch.Generator().manual_seed(T + K + N)

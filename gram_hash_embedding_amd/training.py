@@ -338,10 +338,14 @@ def engram_wkv_backward(dkv, a, w, da=None, dw=None, dw_dtype=None, accumulate=F
 
 def _tensor_list(on, grads, name):
     """(count, host arrays of addresses, element counts and element types) of contiguous bf16 / float32 tensors."""
-    n = len(grads)
-    got = [on.real(g, f"{name}[{i}]") for i, g in enumerate(grads)]
-    return (n, (ctypes.c_void_p * n)(*[p for p, _ in got]), (ctypes.c_int64 * n)(*[g.numel() for g in grads]),
-            (ctypes.c_int32 * n)(*[d for _, d in got]))
+    n, index, bf16, fp32 = len(grads), on.index, torch.bfloat16, torch.float32
+    ptrs, sizes, types = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
+    for i, g in enumerate(grads):
+        if not isinstance(g, torch.Tensor) or g.get_device() != index or not g.is_contiguous() or (
+                g.dtype is not bf16 and g.dtype is not fp32):
+            on.real(g, f"{name}[{i}]")  # says what is wrong
+        ptrs[i], sizes[i], types[i] = g.data_ptr(), g.numel(), BF16 if g.dtype is bf16 else F32
+    return n, ptrs, sizes, types
 
 
 def engram_grad_norm(grads, out=None, workspace=None, stream=None):
@@ -365,9 +369,9 @@ def engram_clip_grads(grads, norm, max_norm, outs=None, stream=None):
     if outs is None:
         outs, optrs = grads, ptrs
     else:
-        if len(outs) != n or any(o.dtype != g.dtype or o.numel() != g.numel() for o, g in zip(outs, grads)):
+        m, optrs, osizes, otypes = _tensor_list(on, outs, "outs")
+        if m != n or bytes(osizes) != bytes(sizes) or bytes(otypes) != bytes(types):
             raise ValueError("outs must match grads in number, types and sizes")
-        optrs = (ctypes.c_void_p * n)(*[on.ptr(o, "outs", o.dtype) for o in outs])
     if norm.numel() != 1:
         raise ValueError("norm must hold one element")
     _check(lib().engram_clip_grads(n, ptrs, optrs, sizes, types, on.ptr(norm, "norm", torch.float32), float(max_norm),

@@ -77,6 +77,9 @@ class _On:
 
     def ptr(self, t, name, dtype, ndim=None):
         """Address of a contiguous tensor of the call's device."""
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == self.index and t.is_contiguous() and
+                (ndim is None or t.dim() == ndim)):
+            return t.data_ptr()
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if not t.is_cuda:
@@ -87,9 +90,7 @@ class _On:
             raise ValueError(f"{name} is on GPU {t.get_device()}, the call runs on GPU {self.index}")
         if ndim is not None and t.dim() != ndim:
             raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
+        raise ValueError(f"{name} must be contiguous")
 
     def real(self, t, name, ndim=None):
         """(address, element type) of a contiguous bf16 or float32 tensor."""

@@ -12,7 +12,7 @@
 // the bits that rows actually have, so the fewest passes (17 bits of a token vocabulary: two, 29 bits of a 384 M row
 // table: three).  A pass counts the digits per tile, then every workgroup ranks a tile of elements (per wave by ballots
 // over the digit's bits, so stable), adds the tiles before it from the table of per-tile digit counts, and scatters.
-// Up to 8,192 ids one workgroup does all of it, up to 1,024 every workgroup does and folds too.
+// Up to 8,192 ids one workgroup does all of it, up to kSmall every workgroup does and folds too.
 //
 // Fold: the sorted positions are cut into chunks of kChunk; a group of lanes adds a segment's positions within a chunk
 // in registers and writes the table row if the segment ends there.  A segment that crosses chunks leaves fp32 partial
@@ -44,7 +44,11 @@ constexpr int kChunk = 16;   // sorted positions per chunk of the fold
 constexpr int kHeadsTile = kThreads * kChunk;  // sorted positions per workgroup that counts distinct rows
 constexpr int64_t kMaxIds = 1ll << 30;
 constexpr int64_t kMaxGridX = 1ll << 23;  // workgroups along x: x * threads stays below 2^32
-constexpr int kSmall = 1024;              // up to this many ids one launch sorts and folds
+// up to this many ids one launch sorts and folds.  Against three launches (one limit for both forms, whose rows have the
+// same bits): the rows form of 500 ids 15.6 us and 23, 640 ids 26 and 23; the dense one over 1,000 rows of 256, 256 ids 13.6
+// and 16.5, 400 17.2 and 17, 640 28 and 17; over 13,225 rows of 2,048 (zeros beneath the sort there) 400 33 and 26, 640 48
+// and 27.
+constexpr int kSmall = 512;
 
 // ---------------------------------------------------------------------------------------------------------------------
 // lookup
@@ -855,7 +859,7 @@ __global__ __launch_bounds__(kThreads) void small_kernel(SmallArgs a) {
             }
         }
     __syncthreads();
-    // where each distinct row begins: four positions per thread
+    // where each distinct row begins: kPer positions per thread
     constexpr int kPer = kSmall / kThreads;
     auto key_at = [&](int i) { return i < n ? static_cast<uint32_t>(s[i] >> 32) : 0xFFFFFFFFu; };
     bool head[kPer];

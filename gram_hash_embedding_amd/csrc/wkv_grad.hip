@@ -396,26 +396,69 @@ Prod prod_of(int64_t M, int64_t N, int64_t R, int size) {
     return p;
 }
 
+int64_t tiles_of(const Prod& p) { return static_cast<int64_t>(p.tiles_m) * p.tiles_n; }
+
 int at_most(int64_t splits, const Prod& p) {  // four slabs a part, or one part
     const int64_t most = p.slabs / 4 > 1 ? p.slabs / 4 : 1;
     return static_cast<int>(splits < 1 ? 1 : splits < most ? splits : most);
 }
 
-// One product alone: as many parts as there is room for.
-void split_alone(Prod& p, int size) {
-    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-    p.splits = at_most(room_of(size) / tiles, p);
+// When n1 units of l1 slabs, then n2 of l2 <= l1, each taken by the workgroup slot that is free first, are done.
+int64_t done_at(int64_t n1, int64_t l1, int64_t n2, int64_t l2, int64_t room) {
+    const int64_t late = n1 % room, early = room - late;  // slots that the first kind leaves at hi and at lo
+    const int64_t lo = n1 / room * l1, hi = lo + l1;
+    if (n2 == 0) return late ? hi : lo;
+    const int64_t mean = (n1 * l1 + n2 * l2 + room - 1) / room;
+    int64_t m = late ? hi : lo + l2;
+    if (m < mean) m = mean;
+    while (true) {
+        const int64_t a = (m - lo) / l2, b = late ? (m - hi) / l2 : 0;
+        if (early * a + late * b >= n2) return m;
+        const int64_t next_a = lo + (a + 1) * l2, next_b = hi + (b + 1) * l2;
+        m = late && next_b < next_a ? next_b : next_a;
+    }
 }
 
-// Both in a launch: parts no longer than a workgroup's share of all the work, the other product's units fill in beside
-// them.  A unit costs about kUnitSlabs slabs more than it has (its first loads and its stores).  us with 0, 2, 5 and 10:
-// 251 x 1,536 x 25,600 82, 85, 92, over 100; 512 115, 110, 118, 131; 2,000 x 1,536 x 5,120 in 256 x 256 tiles 109, 92.
+// us that a launch takes with the products' present parts: a slab at 1.5 PFLOP/s over all slots, kUnitSlabs more for each
+// unit (its first loads and its stores), and the second launch over the partial sums.
 constexpr int64_t kUnitSlabs = 2;
-void split_both(Prod& a, Prod& b, int size) {
-    const int64_t ta = static_cast<int64_t>(a.tiles_m) * a.tiles_n, tb = static_cast<int64_t>(b.tiles_m) * b.tiles_n;
-    const int64_t share = (ta * (a.slabs + kUnitSlabs) + tb * (b.slabs + kUnitSlabs)) / room_of(size) + 1;
-    a.splits = at_most((a.slabs + share - 1) / share, a);
-    b.splits = at_most((b.slabs + share - 1) / share, b);
+double cost_of(const Prod& a, const Prod& b, int size) {
+    const int64_t room = room_of(size);
+    auto length = [](const Prod& p) { return (p.slabs + p.splits - 1) / p.splits + kUnitSlabs; };
+    const int64_t na = a.out ? a.units() : 0, nb = b.out ? b.units() : 0, la = length(a), lb = length(b);
+    double us = 2.0 * size * size * BK * static_cast<double>(room) / 1.5e9 *
+                static_cast<double>(la >= lb ? done_at(na, la, nb, lb, room) : done_at(nb, lb, na, la, room));
+    for (const Prod* p : {&a, &b})
+        if (p->out && p->splits > 1) us += 4.0 + 8.0 * p->splits * p->M * p->N / 5e6;
+    return us;
+}
+
+// How the reduced axes are split (of the products whose `out` is set): the cheapest of parts of one length for both, the
+// lengths being the whole of either product's reduction, its half, its third ..., in wider steps from its eighth on.
+// Against parts of just a slot's share of the work, which leave a few units to a round of their own: 2,000 x 1,536 x 5,120
+// 92 -> 70 us, 4,000 156 -> 118, 2,000 x 344 x 9,624 69 -> 44, 2,377 x 584 x 5,416 80 -> 60; 8,192 x 1,536 x 25,600 as it was.
+void split(Prod& a, Prod& b, int size) {
+    constexpr int kMost = 64;
+    Prod best_a = a, best_b = b;
+    double best = -1;
+    const int64_t least = (tiles_of(a) * a.slabs * (a.out != nullptr) + tiles_of(b) * b.slabs * (b.out != nullptr)) / room_of(size);
+    for (const Prod* p : {&a, &b}) {
+        if (!p->out) continue;
+        for (int k = 1; k <= kMost && 4 * k <= p->slabs + 3; k += k < 8 ? 1 : k / 4) {
+            const int64_t length = (p->slabs + k - 1) / k;
+            a.splits = at_most((a.slabs + length - 1) / length, a);
+            b.splits = at_most((b.slabs + length - 1) / length, b);
+            const double us = cost_of(a, b, size);
+            if (best < 0 || us < best) {
+                best = us;
+                best_a.splits = a.splits;
+                best_b.splits = b.splits;
+            }
+            if (2 * length < least) break;  // shorter parts only add to the sums
+        }
+    }
+    a.splits = best_a.splits;
+    b.splits = best_b.splits;
 }
 
 int tile_size(int64_t T, int32_t K, int32_t Nout, bool both) {
@@ -442,14 +485,16 @@ extern "C" int64_t engram_wkv_backward_workspace_bytes(int64_t T, int32_t K, int
     if (!shape_ok(T, K, Nout)) return -1;
     if (T == 0) return 0;
     // what the call asking for both, or for either, needs at most
-    int size = tile_size(T, K, Nout, true);
-    Prod da = prod_of(T, K, Nout, size), dw = prod_of(Nout, K, T, size);
-    split_both(da, dw, size);
-    int64_t need = part_bytes(da) + part_bytes(dw);
-    size = tile_size(T, K, Nout, false);
-    for (Prod p : {prod_of(T, K, Nout, size), prod_of(Nout, K, T, size)}) {
-        split_alone(p, size);
-        need = part_bytes(p) > need ? part_bytes(p) : need;
+    int64_t need = 0;
+    for (int ask = 1; ask <= 3; ++ask) {
+        const int size = tile_size(T, K, Nout, ask == 3);
+        Prod da = prod_of(T, K, Nout, size), dw = prod_of(Nout, K, T, size);
+        int asked;  // (no output is written here)
+        if (ask & 1) da.out = &asked;
+        if (ask & 2) dw.out = &asked;
+        split(da, dw, size);
+        const int64_t bytes = (da.out ? part_bytes(da) : 0) + (dw.out ? part_bytes(dw) : 0);
+        need = bytes > need ? bytes : need;
     }
     return need;
 }
@@ -478,22 +523,19 @@ extern "C" int engram_wkv_backward(const uint16_t* dkv, const uint16_t* a, const
     }
     const int size = tile_size(T, K, Nout, da && dw);
     GradArgs g = {};
-    if (da) {
-        g.da = prod_of(T, K, Nout, size);
-        g.da.p = dkv;
-        g.da.q = w;
-        g.da.out = da;
-    }
-    if (dw) {
-        g.dw = prod_of(Nout, K, T, size);
-        g.dw.p = dkv;
-        g.dw.q = a;
-        g.dw.out = dw;
-        g.dw.out_f32 = dw_dtype == ENGRAM_F32;
-        g.dw.accumulate = accumulate != 0;
-    }
-    if (da && dw) split_both(g.da, g.dw, size);
-    else split_alone(da ? g.da : g.dw, size);
+    g.da = prod_of(T, K, Nout, size);
+    g.da.p = dkv;
+    g.da.q = w;
+    g.da.out = da;
+    g.dw = prod_of(Nout, K, T, size);
+    g.dw.p = dkv;
+    g.dw.q = a;
+    g.dw.out = dw;
+    g.dw.out_f32 = dw_dtype == ENGRAM_F32;
+    g.dw.accumulate = accumulate != 0;
+    split(g.da, g.dw, size);
+    if (!da) g.da = Prod{};
+    if (!dw) g.dw = Prod{};
     const int64_t need = part_bytes(g.da) + part_bytes(g.dw);
     g.da.part = static_cast<float*>(workspace);
     g.dw.part = g.da.part + part_bytes(g.da) / 4;

@@ -419,14 +419,15 @@ int64_t done_at(int64_t n1, int64_t l1, int64_t n2, int64_t l2, int64_t room) {
     }
 }
 
-// us that a launch takes with the products' present parts: a slab at 1.5 PFLOP/s over all slots, kUnitSlabs more for each
-// unit (its first loads and its stores), and the second launch over the partial sums.
+// us that a launch takes with the products' present parts: a slab at 1.5 PFLOP/s over all slots (1.3 times that time in
+// the small tiles: long products of them measured 1.31 times the large ones'), kUnitSlabs more for each unit (its first
+// loads and its stores), and the second launch over the partial sums.
 constexpr int64_t kUnitSlabs = 2;
 double cost_of(const Prod& a, const Prod& b, int size) {
     const int64_t room = room_of(size);
     auto length = [](const Prod& p) { return (p.slabs + p.splits - 1) / p.splits + kUnitSlabs; };
     const int64_t na = a.out ? a.units() : 0, nb = b.out ? b.units() : 0, la = length(a), lb = length(b);
-    double us = 2.0 * size * size * BK * static_cast<double>(room) / 1.5e9 *
+    double us = 2.0 * size * size * BK * static_cast<double>(room) / (size == 128 ? 1.5e9 / 1.3 : 1.5e9) *
                 static_cast<double>(la >= lb ? done_at(na, la, nb, lb, room) : done_at(nb, lb, na, la, room));
     for (const Prod* p : {&a, &b})
         if (p->out && p->splits > 1) us += 4.0 + 8.0 * p->splits * p->M * p->N / 5e6;
@@ -437,7 +438,7 @@ double cost_of(const Prod& a, const Prod& b, int size) {
 // lengths being the whole of either product's reduction, its half, its third ..., in wider steps from its eighth on.
 // Against parts of just a slot's share of the work, which leave a few units to a round of their own: 2,000 x 1,536 x 5,120
 // 92 -> 70 us, 4,000 156 -> 118, 2,000 x 344 x 9,624 69 -> 44, 2,377 x 584 x 5,416 80 -> 60; 8,192 x 1,536 x 25,600 as it was.
-void split(Prod& a, Prod& b, int size) {
+double split(Prod& a, Prod& b, int size) {
     constexpr int kMost = 64;
     Prod best_a = a, best_b = b;
     double best = -1;
@@ -459,14 +460,28 @@ void split(Prod& a, Prod& b, int size) {
     }
     a.splits = best_a.splits;
     b.splits = best_b.splits;
+    return best;
 }
 
 int tile_size(int64_t T, int32_t K, int32_t Nout, bool both) {
-    // 128 x 128 tiles for little work: more workgroups, and two of them a CU.  us with 128 and 256, both products: 64 x 1,536
-    // x 25,600 64 and 66, 251 96 and 85, 512 140 and 110; 251 x 1,536 x 5,120 27 and 27, 1,000 51 and 42, 2,000 83 and 92,
-    // 4,000 147 and 151; 8,000 x 456 x 2,000 47 and 51.  dW alone: 251 x 1,536 x 25,600 45 and 51, 400 54 and 59, 700 70 and
-    // 74 (da 77 and 71); 2,000 x 1,536 x 5,120 38 and 53 (da 51 and 46).
-    return 2.0 * T * K * Nout < (both ? 1.5e10 : 3.2e10) ? 128 : 256;
+    // 128 x 128 tiles for little work, two workgroups a CU, and for sizes that the large tiles leave much of idle.  Both
+    // products: what costs less.  us with 128 and 256: 64 x 1,536 x 25,600 63 and 69, 251 91 and 86, 512 137 and 109; 251 x
+    // 1,536 x 5,120 27 and 27, 1,000 48 and 42, 4,000 143 and 120; 8,000 x 456 x 2,000 46 and 52; 5,984 x 344 x 9,624 130 and
+    // 159; 5,687 x 584 x 5,416 114 and 132; 3,681 x 1,024 x 18,072 373 and 306.
+    if (both) {
+        double us[2];
+        int asked;  // (no output is written here)
+        for (int i = 0; i < 2; ++i) {
+            const int size = i ? 256 : 128;
+            Prod da = prod_of(T, K, Nout, size), dw = prod_of(Nout, K, T, size);
+            da.out = dw.out = &asked;
+            us[i] = split(da, dw, size);
+        }
+        return us[0] < us[1] ? 128 : 256;
+    }
+    // One: by its work.  dW: 251 x 1,536 x 25,600 45 and 49, 400 54 and 60; 2,000 x 1,536 x 5,120 39 and 44, 3,681 x 1,024 x
+    // 18,072 209 and 193; da 48 and 48, 58 and 56, 52 and 47, 210 and 161.
+    return 2.0 * T * K * Nout < 3.2e10 ? 128 : 256;
 }
 
 int64_t part_bytes(const Prod& p) { return p.splits > 1 ? p.splits * p.M * p.N * 4 : 0; }

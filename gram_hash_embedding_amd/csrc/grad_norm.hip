@@ -20,6 +20,7 @@ constexpr int kThreads = 256;
 constexpr int kTensors = 96;         // per launch: 96 * 28 bytes of kernel arguments
 constexpr int kNormPieces = 16;       // 16-byte pieces per thread and run
 constexpr int kClipPieces = 1;
+constexpr int64_t kMaxBlocks = 1ll << 23;  // workgroups per launch: times the threads stays below 2^32
 
 struct NormList {
     const void* in[kTensors];
@@ -205,31 +206,40 @@ int check_list(const char* what, int32_t tensors, const void* const* in, const i
     return ENGRAM_OK;
 }
 
-// The tensors in lists of kTensors, each with its workgroups; `launch(list, blocks, runs before)`.
+// The tensors in lists of kTensors and of at most kMaxBlocks workgroups, a tensor that needs more of them cut between two
+// runs; `launch(list, blocks, runs before)` until one fails.
 template <class F>
-void for_lists(int32_t tensors, const void* const* in, void* const* out, const int64_t* n, const int32_t* dtype,
-               int pieces, F&& launch) {
+int for_lists(int32_t tensors, const void* const* in, void* const* out, const int64_t* n, const int32_t* dtype,
+              int pieces, F&& launch) {
     NormList l = {};
     int64_t blocks = 0, before = 0;
     auto flush = [&]() {
-        if (l.tensors) launch(l, static_cast<unsigned>(blocks), before);
+        const int rc = l.tensors ? launch(l, static_cast<unsigned>(blocks), before) : ENGRAM_OK;
         before += blocks;
         l = NormList{};
         blocks = 0;
+        return rc;
     };
     for (int i = 0; i < tensors; ++i) {
-        if (n[i] == 0) continue;
-        const int64_t r = runs_of(n[i], dtype[i], pieces);
-        if (l.tensors == kTensors || blocks + r > 0x7FFFFFFF) flush();
-        const int at = l.tensors++;
-        l.in[at] = in[i];
-        l.out[at] = out ? out[i] : nullptr;
-        l.n[at] = n[i];
-        l.first[at] = static_cast<uint32_t>(blocks);
-        if (dtype[i] == ENGRAM_F32) l.f32[at >> 5] |= 1u << (at & 31);
-        blocks += r;
+        const int64_t size = dtype[i] == ENGRAM_F32 ? 4 : 2, run = static_cast<int64_t>(pieces) * kThreads * 16 / size;
+        for (int64_t done = 0; done < n[i];) {
+            if (l.tensors == kTensors || blocks == kMaxBlocks) {
+                const int rc = flush();
+                if (rc != ENGRAM_OK) return rc;
+            }
+            const int64_t left = runs_of(n[i] - done, dtype[i], pieces), room = kMaxBlocks - blocks;
+            const int64_t r = left < room ? left : room;
+            const int at = l.tensors++;
+            l.in[at] = static_cast<const uint8_t*>(in[i]) + done * size;
+            l.out[at] = out ? static_cast<uint8_t*>(out[i]) + done * size : nullptr;
+            l.n[at] = r * run < n[i] - done ? r * run : n[i] - done;
+            l.first[at] = static_cast<uint32_t>(blocks);
+            if (dtype[i] == ENGRAM_F32) l.f32[at >> 5] |= 1u << (at & 31);
+            blocks += r;
+            done += l.n[at];
+        }
     }
-    flush();
+    return flush();
 }
 
 }  // namespace
@@ -250,7 +260,7 @@ extern "C" int64_t engram_grad_norm_workspace_bytes(int32_t tensors, const int64
 extern "C" int engram_grad_norm(int32_t tensors, const void* const* grads, const int64_t* n, const int32_t* dtype,
                                 float* norm, void* workspace, int64_t workspace_bytes, void* stream) {
     const char* what = "engram_grad_norm";
-    const int rc = check_list(what, tensors, grads, n, dtype);
+    int rc = check_list(what, tensors, grads, n, dtype);
     if (rc != ENGRAM_OK) return rc;
     if (!norm || !aligned(norm, 4)) return fail(ENGRAM_EINVAL, "%s: norm is null or misaligned", what);
     const int64_t need = engram_grad_norm_workspace_bytes(tensors, n, dtype);
@@ -261,9 +271,11 @@ extern "C" int engram_grad_norm(int32_t tensors, const void* const* grads, const
                     (long long)need);
     hipStream_t s = as_stream(stream);
     double* part = static_cast<double*>(workspace);
-    for_lists(tensors, grads, nullptr, n, dtype, kNormPieces, [&](const NormList& l, unsigned blocks, int64_t before) {
+    rc = for_lists(tensors, grads, nullptr, n, dtype, kNormPieces, [&](const NormList& l, unsigned blocks, int64_t before) {
         hipLaunchKernelGGL(norm_kernel, dim3(blocks), dim3(kThreads), 0, s, l, part + before);
+        return check_launch(what);
     });
+    if (rc != ENGRAM_OK) return rc;
     hipLaunchKernelGGL(norm_sum_kernel, dim3(1), dim3(1024), 0, s, part, need / 8, norm);
     return check_launch(what);
 }
@@ -284,8 +296,8 @@ extern "C" int engram_clip_grads(int32_t tensors, const void* const* grads, void
             return fail(ENGRAM_EINVAL, "%s: output %d: misaligned pointer", what, i);
     }
     hipStream_t s = as_stream(stream);
-    for_lists(tensors, grads, out, n, dtype, kClipPieces, [&](const NormList& l, unsigned blocks, int64_t) {
+    return for_lists(tensors, grads, out, n, dtype, kClipPieces, [&](const NormList& l, unsigned blocks, int64_t) {
         hipLaunchKernelGGL(clip_kernel, dim3(blocks), dim3(kThreads), 0, s, l, norm, max_norm);
+        return check_launch(what);
     });
-    return check_launch(what);
 }

@@ -575,6 +575,26 @@ def test_norm_extremes(gpu_device):
             assert out.isnan().all()
 
 
+def test_norm_and_clip_past_a_launch(gpu_device):
+    """64 GiB in one tensor, more than a launch's grid holds: every element, on both sides of each cut, and the tensors
+    around it."""
+    g, n = _eng(), (1 << 35) + 2053
+    first, last = torch.full((1025,), 0.5, device=gpu_device), torch.full((77,), -0.25, dtype=BF, device=gpu_device)
+    big = torch.full((n,), 2.0 ** -10, dtype=BF, device=gpu_device)
+    at = torch.tensor([0, (1 << 34) - 1, 1 << 34, (1 << 35) - 1, 1 << 35, n - 1], device=gpu_device)
+    big[at] = 3.0
+    want = math.sqrt(1025 * 0.25 + 77 * 0.0625 + (n - 6) * 2.0 ** -20 + 6 * 9)
+    norm = g.engram_grad_norm([first, big, last])
+    assert abs(float(norm) - want) <= 2 * ref.U32 * want
+    g.engram_clip_grads([first, big, last], torch.full((1,), 4.0, device=gpu_device), 2.0)
+    # the factor is 2 / (4 + 1e-6): a half less 1.25e-7, and both values round to their halves in bf16
+    assert (big[at] == 1.5).all()
+    big[at] = 2.0 ** -11
+    for i in range(0, n, 1 << 32):
+        assert bool((big[i:i + (1 << 32)] == 2.0 ** -11).all()), i
+    assert (last == -0.125).all() and (first - 0.25).abs().max() <= 2.0 ** -23
+
+
 def test_norm_and_clip_refusals(gpu_device):
     g = _eng()
     t = torch.ones(8, device=gpu_device)

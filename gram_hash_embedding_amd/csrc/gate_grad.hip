@@ -66,8 +66,12 @@ __device__ inline Coef coef_of(const GateGradArgs& p, float hh, float kk, float 
     const float rh = rsqrtf(hh * p.inv_dim + p.eps), rk = rsqrtf(kk * p.inv_dim + p.eps);
     const float z = sqrtf(fmaxf(fabsf(d), 1e-6f));
     Coef c;
-    c.g = 1.0f / (1.0f + expf(-copysignf(z, d)));
-    const float dd = fabsf(d) < 1e-6f ? 0.f : dg * c.g * (1.0f - c.g) / (2.0f * z);
+    const float e = expf(-copysignf(z, d));
+    c.g = 1.0f / (1.0f + e);
+    // 1 - g = e g: where g is near 1 (e small) the difference has lost the digits that the product keeps (3e-4 of the slope
+    // at d = 72, all of it from 300), where e is large it has them and the product may overflow
+    const float shut = d > 0.f ? e * c.g : 1.0f - c.g;
+    const float dd = fabsf(d) < 1e-6f ? 0.f : dg * c.g * shut / (2.0f * z);
     c.a = c.bh = c.bk = 0.f;
     if (dd != 0.f) {  // (a zero gradient stays zero next to the large norms of zero rows; NaN goes on)
         c.a = dd * (rh * rk * p.rsqrt_dim);

@@ -358,6 +358,22 @@ def test_gate_backward_edges_of_the_dot(gpu_device, hc):
         assert torch.equal(got[0][i].cpu(), dout[i]), i
 
 
+@pytest.mark.parametrize("hc", [1, 2, 4, 3])
+@pytest.mark.parametrize("d", [20.0, 72.0, 300.0, 400.0, -72.0, -400.0, -1000.0])
+def test_gate_backward_far_from_the_corner(gpu_device, hc, d):
+    """Every pre-activation large: the sigmoid's slope is small and keeps its digits (dq and dk are float32).  A rounding of
+    sqrt(|d|) moves the slope by up to sqrt(1000) U32, well inside the sums' (dim + 64) U32.  (Past 400 the float64
+    reference's own 1 - g has fewer digits than that.)"""
+    g, dim = _eng(), 64
+    x, kv, q, k, dot, dout = _gate_inputs(12, hc, dim, 11)
+    dot = torch.full_like(dot, d)
+    got = g.engram_gate_output_backward(*[t.to(gpu_device) for t in (x, kv, q, k)], 1e-20, dot.to(gpu_device),
+                                        dout.to(gpu_device))
+    want = ref.gate_backward(x, kv, q, k, 1e-20, dot, dout)
+    assert want["dq"].abs().max() > 1e-20
+    _check_gate(got, want, 12, dim, f"{d}")
+
+
 def test_gate_backward_past_32_bits(gpu_device):
     """108,000 tokens: the stream holds 2.2 G elements, kv 2.8 G; sampled tokens, and the rest must be finite."""
     g, T, hc, dim = _eng(), 108000, 4, 5120

@@ -155,7 +155,7 @@ def _lookup(on, ids, grad, layer):
         T, stride = B * L, E * C
         ip += ib * layer * C
         n = T * C
-        if grad.dim() == 2 and T > 0 and grad.shape[0] == T and grad.shape[1] % C == 0 and C > 1:
+        if grad.dim() == 2 and grad.shape[0] == T and grad.shape[1] % C == 0:
             D = grad.shape[1] // C
         else:
             D = grad.shape[-1]

@@ -260,6 +260,18 @@ def test_embed_grad_no_ids_and_non_finite(gpu_device):
     assert torch.equal(got, want)
 
 
+def test_embed_grad_of_one_layer_of_no_tokens(gpu_device):
+    g, E, C, D, R = _eng(), 3, 6, 32, 50
+    for B, L in ((0, 9), (2, 0)):
+        ids = torch.zeros((B, L, E, C), dtype=torch.int64, device=gpu_device)
+        for shape in ((0, C, D), (B, L, C, D), (0, C * D)):
+            up = torch.zeros(shape, dtype=BF, device=gpu_device)
+            out = g.engram_embed_grad(ids, up, R, layer=1)
+            assert out.shape == (R, D) and not out.any(), shape
+            unique, rows, count = g.engram_embed_grad_rows(ids, up, R, layer=1)
+            assert unique.shape == (0,) and rows.shape == (0, D) and int(count) == 0, shape
+
+
 def test_embed_grad_refusals(gpu_device):
     g = _eng()
     ids = torch.zeros(6, dtype=torch.int64, device=gpu_device)

@@ -154,3 +154,35 @@ def test_norm_and_clip_validation():
     assert L.engram_clip_grads(2, p, p, n, d, FAKE, float("nan"), None) == 1 and "max_norm" in _err()
     assert L.engram_clip_grads(2, p, _list(ptr=0)[0], n, d, FAKE, 1.0, None) == 1 and "output 0" in _err()
     assert L.engram_clip_grads(0, None, None, None, None, None, 1.0, None) == 0
+
+
+class _Addresses:
+    """Stands in for a call's device: takes any ids."""
+
+    def ids(self, ids):
+        return ids.data_ptr(), ids.element_size()
+
+
+@pytest.mark.parametrize("tokens", [(0, 7), (3, 0), (2, 7)])
+@pytest.mark.parametrize("C,D", [(6, 32), (24, 64), (1, 8)])
+def test_rows_of_a_layers_gradient(tokens, C, D):
+    """[B*L, C, D], [B, L, C, D] and [B*L, C*D] are all rows of D, for an empty batch too."""
+    from gram_hash_embedding_amd import training
+
+    training._load()
+    (B, L), E = tokens, 3
+    T = B * L
+    ids = torch.zeros((B, L, E, C), dtype=torch.int64)
+    for shape in ((T, C, D), (B, L, C, D), (T, C * D)):
+        ip, ib, t, stride, c, n, d = training._lookup(_Addresses(), ids, torch.zeros(shape), 1)
+        assert (t, stride, c, n, d) == (T, E * C, C, T * C, D), shape
+        assert ip == ids.data_ptr() + 8 * C and ib == 8
+
+
+def test_rows_of_a_layers_gradient_that_do_not_divide():
+    from gram_hash_embedding_amd import training
+
+    training._load()
+    ids = torch.zeros((2, 7, 1, 6), dtype=torch.int64)
+    with pytest.raises(ValueError, match="row of D elements"):
+        training._lookup(_Addresses(), ids, torch.zeros((14, 6 * 32 + 8)), 0)

@@ -976,9 +976,9 @@ Plan plan_of(int64_t n, int32_t D, int64_t R) {
     return p;
 }
 
-// sorted (row, position) pairs of the ids, in the workspace; `zeros` bytes at `zero` are written on the way
-const Pair* sort_ids(const Plan& p, const void* ids, int id_bytes, int64_t n, int C, int64_t stride, int64_t R,
-                     int64_t row_start, uint8_t* ws, void* zero, int64_t zeros, hipStream_t stream) {
+// sorted (row, position) pairs of the ids, in the workspace; `zeros` bytes at f's output are written on the way
+int sort_ids(const Plan& p, const void* ids, int id_bytes, int64_t n, int C, int64_t stride, int64_t R, int64_t row_start,
+             uint8_t* ws, FoldArgs& f, int64_t zeros, hipStream_t stream, const char* what) {
     Pair* buf[2] = {reinterpret_cast<Pair*>(ws + p.pairs), reinterpret_cast<Pair*>(ws + p.pairs) + n};
     SortArgs a = {};
     a.ids = ids;
@@ -991,10 +991,13 @@ const Pair* sort_ids(const Plan& p, const void* ids, int id_bytes, int64_t n, in
     a.bits = p.bits;
     a.tiles = p.tiles;
     a.hist = reinterpret_cast<uint32_t*>(ws + p.hist);
-    // (what a grid does not hold, 1 TB and more, in a launch of its own)
+    // (what a grid does not hold, some 32 GiB and more, in a launch of its own)
     const int64_t n16 = zeros / 16, most = (kMaxGridX / 2 - p.tiles) * kSortThreads;
-    const Zeros z = {static_cast<u32x4*>(zero), n16 < most ? n16 : most};
-    if (n16 > most) launch_zero(z.p + most, (n16 - most) * 16, stream, "engram_embed_grad");
+    const Zeros z = {reinterpret_cast<u32x4*>(f.out), n16 < most ? n16 : most};
+    if (n16 > most) {
+        const int rc = launch_zero(z.p + most, (n16 - most) * 16, stream, what);
+        if (rc != ENGRAM_OK) return rc;
+    }
     uint32_t* totals = reinterpret_cast<uint32_t*>(ws + p.totals);
     for (int q = 0; q < p.passes; ++q) {
         a.shift = q * p.bits;
@@ -1003,12 +1006,13 @@ const Pair* sort_ids(const Plan& p, const void* ids, int id_bytes, int64_t n, in
         if (p.items == kFewItems) launch_pass<kFewItems>(a, totals, q ? Zeros{} : z, stream);
         else launch_pass<kManyItems>(a, totals, q ? Zeros{} : z, stream);
     }
-    return buf[(p.passes - 1) & 1];
+    f.sorted = buf[(p.passes - 1) & 1];
+    return ENGRAM_OK;
 }
 
 // the same by one workgroup, the rows form's counts in f's arrays
-const Pair* one_sort(const Plan& p, const void* ids, int id_bytes, int64_t n, int C, int64_t stride, int64_t R,
-                     int64_t row_start, uint8_t* ws, const FoldArgs& f, int64_t zeros, hipStream_t stream) {
+int one_sort(const Plan& p, const void* ids, int id_bytes, int64_t n, int C, int64_t stride, int64_t R, int64_t row_start,
+             uint8_t* ws, FoldArgs& f, int64_t zeros, hipStream_t stream, const char* what) {
     SortArgs a = {};
     a.ids = ids;
     a.id_bytes = id_bytes;
@@ -1023,10 +1027,14 @@ const Pair* one_sort(const Plan& p, const void* ids, int id_bytes, int64_t n, in
     a.out = reinterpret_cast<Pair*>(ws + p.pairs);
     const int64_t n16 = zeros / 16, most = (kMaxGridX / 4 - 1) * kOneThreads;
     const Zeros z = {reinterpret_cast<u32x4*>(f.out), n16 < most ? n16 : most};
-    if (n16 > most) launch_zero(z.p + most, (n16 - most) * 16, stream, "engram_embed_grad");
+    if (n16 > most) {
+        const int rc = launch_zero(z.p + most, (n16 - most) * 16, stream, what);
+        if (rc != ENGRAM_OK) return rc;
+    }
     hipLaunchKernelGGL(one_sort_kernel, dim3(static_cast<unsigned>(1 + (z.n16 + kOneThreads - 1) / kOneThreads)),
                        dim3(kOneThreads), 0, stream, a, f, z);
-    return a.out;
+    f.sorted = a.out;
+    return ENGRAM_OK;
 }
 
 // `past`: the call moves more than the Infinity Cache holds.  Then upstream rows and finished ones pass it by, which leaves
@@ -1196,12 +1204,10 @@ int embed_grad(FoldArgs& f, const void* ids, int32_t id_bytes, int64_t n, int64_
     f.leave_to = reinterpret_cast<uint32_t*>(ws + p.leave_to);
     f.leave = reinterpret_cast<float*>(ws + p.leave);
     f.enter = reinterpret_cast<float*>(ws + p.enter);
-    if (n <= kOneSort) {
-        f.sorted = one_sort(p, ids, id_bytes, n, C, stride, R, row_start, ws, f, fill ? bytes : 0, s);
-    } else {
-        f.sorted = sort_ids(p, ids, id_bytes, n, C, stride, R, row_start, ws, f.out, fill ? bytes : 0, s);
-        if (f.unique) hipLaunchKernelGGL(heads_kernel, dim3(p.head_tiles), dim3(kThreads), 0, s, f);
-    }
+    const int rc = (n <= kOneSort ? one_sort : sort_ids)(p, ids, id_bytes, n, C, stride, R, row_start, ws, f,
+                                                         fill ? bytes : 0, s, what);
+    if (rc != ENGRAM_OK) return rc;
+    if (n > kOneSort && f.unique) hipLaunchKernelGGL(heads_kernel, dim3(p.head_tiles), dim3(kThreads), 0, s, f);
     return launch_fold_types(f, nullptr, past, up_dtype, out_dtype, s, what);
 }
 

@@ -59,3 +59,68 @@ def test_norm_of_any_size(library, sizes, kinds):
     status, launches = library.call("engram_grad_norm", [*head, *tail, ("p", AT), ("p", AT), ("i64", 1 << 50), ("p", None)])
     assert status == 0
     assert sum(x for x, *_ in launches[:-1]) == sum(-(-n * (4 if k else 2) // 65536) for n, k in zip(sizes, kinds))
+
+
+def _dense(library, n, R, D, fail_at=None, C=1, kind=1):
+    return library.call("engram_embed_grad", [
+        ("p", AT), ("i32", 8), ("i64", n // C), ("i64", C), ("i32", C), ("p", AT), ("i32", 0), ("i64", R), ("i64", 0), ("i32", D),
+        ("f32", 1.0), ("p", AT), ("i32", kind), ("i32", 0), ("p", AT), ("i64", 1 << 60), ("p", None)], fail_at)
+
+
+def _rows(library, n, R, D, fail_at=None):
+    return library.call("engram_embed_grad_rows", [
+        ("p", AT), ("i32", 8), ("i64", n), ("i64", 1), ("i32", 1), ("p", AT), ("i32", 0), ("i64", R), ("i64", 0), ("i32", D),
+        ("f32", 1.0), ("p", AT), ("p", AT), ("i32", 1), ("p", AT), ("p", AT), ("i64", 1 << 60), ("p", None)], fail_at)
+
+
+def _embed(library, n, D, fail_at=None):
+    return library.call("engram_embed", [("p", AT), ("i32", 8), ("i64", n), ("p", AT), ("i32", 0), ("i64", 1000), ("i64", 0),
+                                         ("i32", D), ("f32", 1.0), ("p", AT), ("i32", 0), ("p", None)], fail_at)
+
+
+def _gate(library, T, hc, dim, fail_at=None):
+    return library.call("engram_gate_output_backward", [
+        ("p", AT), ("p", AT), ("i64", (hc + 1) * dim), ("p", AT), ("p", AT), ("f32", 1e-20), ("p", AT), ("p", AT), ("p", None),
+        *[("p", AT)] * 5, ("i64", 1 << 60), ("i64", T), ("i32", hc), ("i32", dim), ("p", None)], fail_at)
+
+
+def _wkv(library, T, K, N, fail_at=None, da=AT, dw=AT):
+    return library.call("engram_wkv_backward", [
+        ("p", AT), ("p", AT), ("p", AT), ("p", da), ("p", dw), ("i32", 1), ("i32", 0), ("p", AT), ("i64", 1 << 60), ("i64", T),
+        ("i32", K), ("i32", N), ("p", None)], fail_at)
+
+
+def _norm(library, sizes, fail_at=None):
+    head, tail = _lists(sizes, [1] * len(sizes))
+    return library.call("engram_grad_norm", [*head, *tail, ("p", AT), ("p", AT), ("i64", 1 << 60), ("p", None)], fail_at)
+
+
+BIG = 384006168  # the released table's rows: 98 GB of float32 zeros, more than a launch of the sort writes beside it
+CALLS = {
+    "lookup": lambda lib, f: _embed(lib, 1000, 64, f),
+    "dense, no ids": lambda lib, f: _dense(lib, 0, 100, 64, f),
+    "dense, few ids": lambda lib, f: _dense(lib, 100, 100, 64, f),
+    "dense, one workgroup's sort": lambda lib, f: _dense(lib, 3000, 100, 64, f),
+    "dense, one workgroup's sort, big": lambda lib, f: _dense(lib, 3000, BIG, 64, f),
+    "dense, sort over tiles": lambda lib, f: _dense(lib, 300000, 100, 64, f),
+    "dense, sort over tiles, big": lambda lib, f: _dense(lib, 30000, BIG, 64, f),
+    "rows, no ids": lambda lib, f: _rows(lib, 0, 100, 64, f),
+    "rows, few ids": lambda lib, f: _rows(lib, 100, 100, 64, f),
+    "rows, one workgroup's sort": lambda lib, f: _rows(lib, 3000, 100, 64, f),
+    "rows, sort over tiles": lambda lib, f: _rows(lib, 600000, BIG, 64, f),
+    "gate": lambda lib, f: _gate(lib, 100, 4, 256, f),
+    "gate, any copies": lambda lib, f: _gate(lib, 100, 3, 256, f),
+    "gate, no tokens": lambda lib, f: _gate(lib, 0, 4, 256, f),
+    "projection": lambda lib, f: _wkv(lib, 251, 1536, 25600, f),
+    "projection, no tokens": lambda lib, f: _wkv(lib, 0, 64, 64, f),
+    "norm": lambda lib, f: _norm(lib, [1000] * 200, f),
+    "clip": lambda lib, f: _clip(lib, [1000] * 200, [1] * 200, f),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_every_failed_launch_is_reported(library, name):
+    status, launches = CALLS[name](library, None)
+    assert status == 0 and launches
+    for i in range(len(launches)):
+        assert CALLS[name](library, i)[0] == EHIP, f"launch {i} of {len(launches)}: {launches[i]}"

@@ -435,7 +435,7 @@ struct FoldArgs {
     uint32_t n, R;
     const uint8_t* up;  // [n, D] upstream rows
     int D;
-    int cols;           // column blocks of 64 pieces
+    int cols;           // column blocks of a group's lanes, a piece each
     float scale;
     uint8_t* out;       // dense: [R, D]; rows: [n, D]
     int accumulate;
@@ -1064,14 +1064,18 @@ int launch_fold_as(FoldArgs& a, const SortArgs* small, bool past, hipStream_t st
     return check_launch(what);
 }
 
+// lanes that share a row in the fold, the join and the one launch of few ids
+int lanes_of(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
+
 template <class GT, class OT>
 int launch_fold(FoldArgs& a, const SortArgs* small, bool past, hipStream_t stream, const char* what) {
-    const int pieces = a.D / 8;
-    if (pieces <= 4) return launch_fold_as<GT, OT, 4>(a, small, past, stream, what);
-    if (pieces <= 8) return launch_fold_as<GT, OT, 8>(a, small, past, stream, what);
-    if (pieces <= 16) return launch_fold_as<GT, OT, 16>(a, small, past, stream, what);
-    if (pieces <= 32) return launch_fold_as<GT, OT, 32>(a, small, past, stream, what);
-    return launch_fold_as<GT, OT, 64>(a, small, past, stream, what);
+    switch (lanes_of(a.D)) {
+        case 4: return launch_fold_as<GT, OT, 4>(a, small, past, stream, what);
+        case 8: return launch_fold_as<GT, OT, 8>(a, small, past, stream, what);
+        case 16: return launch_fold_as<GT, OT, 16>(a, small, past, stream, what);
+        case 32: return launch_fold_as<GT, OT, 32>(a, small, past, stream, what);
+        default: return launch_fold_as<GT, OT, 64>(a, small, past, stream, what);
+    }
 }
 
 int launch_fold_types(FoldArgs& a, const SortArgs* small, bool past, int32_t gd, int32_t od, hipStream_t stream,
@@ -1094,9 +1098,11 @@ int check_ids(const char* what, int32_t id_bytes, int64_t T, int64_t stride, int
     return ENGRAM_OK;
 }
 
-// the launches' grids: n D / 2^15 workgroups at most
+// The fold's threads, the most of any launch here: its lanes for every chunk and column block.  2^32 of them, which no grid
+// holds, are 2^30 positions times blocks of 512 columns: half a TB of upstream rows at the least.
 int check_work(const char* what, int64_t n, int32_t D) {
-    if (n > (1ll << 45) / D) return fail(ENGRAM_EINVAL, "%s: too many ids for the row width", what);
+    const int64_t lanes = lanes_of(D), cols = (D / 8 + lanes - 1) / lanes, chunks = (n + kChunk - 1) / kChunk;
+    if (chunks * cols * lanes + kThreads > 1ll << 32) return fail(ENGRAM_EINVAL, "%s: too many ids for the row width", what);
     return ENGRAM_OK;
 }
 

@@ -582,8 +582,8 @@ int engram_embed(const void* ids, int32_t id_bytes, int64_t n, const void* table
  * workspace  engram_embed_grad_workspace_bytes(T*C, D, R) bytes, 16-byte aligned,
  *            caller-owned scratch (no initialisation needed); may be NULL where that
  *            is 0 (few ids)
- * Limits: T >= 0, 1 <= C <= 1024, T*C <= 2^30; 1 <= R < 2^31; D a multiple of 8 in
- * [8, 65536].  Too small a workspace -> ENGRAM_ERANGE.
+ * Limits: T >= 0, 1 <= C <= 1024, T*C <= 2^30, T*C*ceil(D/512) < 2^30 where D > 256;
+ * 1 <= R < 2^31; D a multiple of 8 in [8, 65536].  Too small a workspace -> ENGRAM_ERANGE.
  */
 int engram_embed_grad(const void* ids, int32_t id_bytes, int64_t T, int64_t id_token_stride, int32_t C, const void* up,
                       int32_t up_dtype, int64_t R, int64_t row_start, int32_t D, float scale, void* grad,

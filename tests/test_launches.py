@@ -124,3 +124,16 @@ def test_every_failed_launch_is_reported(library, name):
     assert status == 0 and launches
     for i in range(len(launches)):
         assert CALLS[name](library, i)[0] == EHIP, f"launch {i} of {len(launches)}: {launches[i]}"
+
+
+@pytest.mark.parametrize("n", [600, 9000, 1 << 20, (1 << 28) + 1, 1 << 30])
+@pytest.mark.parametrize("D", [8, 32, 64, 128, 256, 264, 512, 520, 4096, 5120, 65536])
+def test_embedding_gradients_of_any_size(library, n, D):
+    """All ids that 288 GB can hold rows of are taken; what a grid does not hold is refused before anything is launched."""
+    for call in (lambda: _dense(library, n, 1000, D), lambda: _rows(library, n, 1000, D)):
+        status, launches = call()
+        assert status in (0, 1)
+        assert status == 0 or (not launches and n * D * 2 > 288 << 30), (n, D)
+    for m in (n, 16 * n):
+        status, launches = _embed(library, m, D)
+        assert status == 0 or (status == 1 and not launches and m * D * 2 > 288 << 30), (m, D)

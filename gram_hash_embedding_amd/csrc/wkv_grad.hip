@@ -561,13 +561,15 @@ extern "C" int engram_wkv_backward(const uint16_t* dkv, const uint16_t* a, const
                         (long long)need);
     }
     const int64_t u_da = da ? g.da.units() : 0, u_dw = dw ? g.dw.units() : 0;
-    if (u_da + u_dw > 0x7FFFFFFF) return fail(ENGRAM_EINVAL, "%s: too many tiles", what);
+    const int threads = size == 128 ? 256 : 512;
+    // (2^23 tiles and more: outputs of 1 TB, or of narrow rows of which the tiles hold little)
+    if ((u_da + u_dw) * threads >= 1ll << 32) return fail(ENGRAM_EINVAL, "%s: too many tiles", what);
     // the longer reductions first: the shorter ones fill in behind them
     g.first_dw = !da || (dw && g.dw.slabs / g.dw.splits > g.da.slabs / g.da.splits);
     g.first_units = g.first_dw ? u_dw : u_da;
     const dim3 grid(static_cast<unsigned>(u_da + u_dw));
-    if (size == 128) hipLaunchKernelGGL(wkv_grad_small_kernel, grid, dim3(256), 0, s, g);
-    else hipLaunchKernelGGL(wkv_grad_kernel, grid, dim3(512), 0, s, g);
+    if (size == 128) hipLaunchKernelGGL(wkv_grad_small_kernel, grid, dim3(threads), 0, s, g);
+    else hipLaunchKernelGGL(wkv_grad_kernel, grid, dim3(threads), 0, s, g);
     for (const Prod* p : {&g.da, &g.dw}) {
         if (!p->out || p->splits <= 1) continue;
         const int64_t n8 = p->M * p->N / 8;

@@ -661,7 +661,7 @@ int64_t engram_gate_output_backward_workspace_bytes(int64_t T, int32_t hc, int32
  * workspace  engram_wkv_backward_workspace_bytes(T, K, Nout) bytes, 16-byte aligned, caller-owned
  *       scratch (no initialisation needed; NULL where it needs none)
  * Limits: 0 <= T <= 2^30; K a multiple of 8 in [8, 2^20]; Nout a multiple of 8 in
- * [8, 2^21].  Too small a workspace -> ENGRAM_ERANGE.
+ * [8, 2^21]; outputs of fewer than 2^23 tiles of 256 x 256 (or 2^24 of 128 x 128).  Too small a workspace -> ENGRAM_ERANGE.
  */
 int engram_wkv_backward(const uint16_t* dkv, const uint16_t* a, const uint16_t* w, uint16_t* da, void* dw,
                         int32_t dw_dtype, int32_t accumulate, void* workspace, int64_t workspace_bytes, int64_t T,

@@ -137,3 +137,18 @@ def test_embedding_gradients_of_any_size(library, n, D):
     for m in (n, 16 * n):
         status, launches = _embed(library, m, D)
         assert status == 0 or (status == 1 and not launches and m * D * 2 > 288 << 30), (m, D)
+
+
+@pytest.mark.parametrize("T,K,N", [
+    (1, 8, 8), (251, 1536, 25600), (1 << 30, 8, 8), (1 << 30, 64, 64), (1 << 30, 264, 264), (1 << 27, 1536, 256),
+    (1 << 30, 1 << 20, 8), (1 << 30, 8, 1 << 21), (1, 1 << 20, 1 << 21), (1 << 30, 1 << 20, 1 << 21)])
+@pytest.mark.parametrize("da,dw", [(AT, AT), (AT, None), (None, AT)])
+def test_projection_gradients_of_any_size(library, T, K, N, da, dw):
+    status, launches = _wkv(library, T, K, N, da=da, dw=dw)
+    held = 2 * (T * N + (T * K if da else 0) + (T * K if dw else 0) + (N * K if da else 0)) + (4 * N * K if dw else 0)
+    assert status == 0 or (status == 1 and not launches and held > 288 << 30)
+
+
+@pytest.mark.parametrize("T,hc,dim", [(1 << 20, 4, 8192), (1 << 31, 1, 8), (1 << 30, 3, 8), (1 << 24, 64, 8), (7, 64, 8192)])
+def test_gate_gradients_of_any_size(library, T, hc, dim):
+    assert _gate(library, T, hc, dim)[0] == 0

@@ -18,7 +18,7 @@
 //
 // Bound by the matrix cores where T is long: 8,192 x 1,536 x 25,600, both products, 1,053 us, 1.22 PFLOP/s (a large square
 // library product reaches 1.45-1.55 here; da alone 606 us, dW 584).  Below some 1,000 tokens by memory: W read and dW
-// written, 250 MB at 251 tokens in 85 us (da alone 47, dW 45: da waits on its slabs, one of which is in flight per workgroup).
+// written, 250 MB at 251 tokens in 85 us (da alone 45, dW 45: da waits on its slabs, one of which is in flight per workgroup).
 #include <type_traits>
 
 #include "rows.h"
@@ -434,17 +434,15 @@ double cost_of(const Prod& a, const Prod& b, int size) {
     return us;
 }
 
-// How the reduced axes are split (of the products whose `out` is set): the cheapest of parts of one length for both, the
-// lengths being the whole of either product's reduction, its half, its third ..., in wider steps from its eighth on.
+// How the reduced axes are split in a call of both products: the cheapest of parts of one length for both, the lengths being the whole of either product's reduction, its half, its third ..., in wider steps from its eighth on.
 // Against parts of just a slot's share of the work, which leave a few units to a round of their own: 2,000 x 1,536 x 5,120
 // 92 -> 70 us, 4,000 156 -> 118, 2,000 x 344 x 9,624 69 -> 44, 2,377 x 584 x 5,416 80 -> 60; 8,192 x 1,536 x 25,600 as it was.
 double split(Prod& a, Prod& b, int size) {
     constexpr int kMost = 64;
     Prod best_a = a, best_b = b;
     double best = -1;
-    const int64_t least = (tiles_of(a) * a.slabs * (a.out != nullptr) + tiles_of(b) * b.slabs * (b.out != nullptr)) / room_of(size);
+    const int64_t least = (tiles_of(a) * a.slabs + tiles_of(b) * b.slabs) / room_of(size);
     for (const Prod* p : {&a, &b}) {
-        if (!p->out) continue;
         for (int k = 1; k <= kMost && 4 * k <= p->slabs + 3; k += k < 8 ? 1 : k / 4) {
             const int64_t length = (p->slabs + k - 1) / k;
             a.splits = at_most((a.slabs + length - 1) / length, a);
@@ -463,25 +461,49 @@ double split(Prod& a, Prod& b, int size) {
     return best;
 }
 
-int tile_size(int64_t T, int32_t K, int32_t Nout, bool both) {
-    // 128 x 128 tiles for little work, two workgroups a CU, and for sizes that the large tiles leave much of idle.  Both
-    // products: what costs less.  us with 128 and 256: 64 x 1,536 x 25,600 63 and 69, 251 91 and 86, 512 137 and 109; 251 x
-    // 1,536 x 5,120 27 and 27, 1,000 48 and 42, 4,000 143 and 120; 8,000 x 456 x 2,000 46 and 52; 5,984 x 344 x 9,624 130 and
-    // 159; 5,687 x 584 x 5,416 114 and 132; 3,681 x 1,024 x 18,072 373 and 306.
-    if (both) {
-        double us[2];
-        int asked;  // (no output is written here)
-        for (int i = 0; i < 2; ++i) {
-            const int size = i ? 256 : 128;
-            Prod da = prod_of(T, K, Nout, size), dw = prod_of(Nout, K, T, size);
-            da.out = dw.out = &asked;
-            us[i] = split(da, dw, size);
-        }
-        return us[0] < us[1] ? 128 : 256;
+// The products as a call runs them, `da` and `dw` saying which are asked for.
+//
+// Both: 128 x 128 tiles for little work, two workgroups a CU, and for sizes that the large tiles leave much of idle: what
+// costs less.  us with 128 and 256: 64 x 1,536 x 25,600 63 and 69, 251 91 and 86, 512 137 and 109; 251 x 1,536 x 5,120 27 and
+// 27, 1,000 48 and 42, 4,000 143 and 120; 8,000 x 456 x 2,000 46 and 52; 5,984 x 344 x 9,624 130 and 159; 5,687 x 584 x 5,416
+// 114 and 132; 3,681 x 1,024 x 18,072 373 and 306.
+//
+// One alone: its sum is split as a call of both splits it, so that its bits do not depend on whether the other is asked
+// for.  A split of its own is faster where the two products balance each other (da of 2,048 x 1,536 x 25,600 152 us and 219
+// as here, 1,024 89 and 102, 5,984 x 344 x 9,624 82 and 116; dW of the last 76 and 105) and as fast elsewhere.  The tiles are
+// its own, for the bits do not depend on them: small ones for little work (dW of 251 x 1,536 x 25,600 45 us with 128, 50 with
+// 256; 400 55 and 60), else by the cost, the large ones where it is near (3,681 x 1,024 x 18,072 206 and 188).
+struct Choice {
+    Prod da, dw;
+    int size;
+};
+Choice choose(int64_t T, int32_t K, int32_t Nout, bool da, bool dw) {
+    int asked;  // (no output is written here)
+    Choice c[2];
+    double us[2];
+    for (int i = 0; i < 2; ++i) {
+        const int size = i ? 256 : 128;
+        c[i] = Choice{prod_of(T, K, Nout, size), prod_of(Nout, K, T, size), size};
+        c[i].da.out = c[i].dw.out = &asked;
+        us[i] = split(c[i].da, c[i].dw, size);
     }
-    // One: by its work.  dW: 251 x 1,536 x 25,600 45 and 49, 400 54 and 60; 2,000 x 1,536 x 5,120 39 and 44, 3,681 x 1,024 x
-    // 18,072 209 and 193; da 48 and 48, 58 and 56, 52 and 47, 210 and 161.
-    return 2.0 * T * K * Nout < 3.2e10 ? 128 : 256;
+    int best = us[0] < us[1] ? 0 : 1;
+    if (!da || !dw) {
+        const int splits_da = c[best].da.splits, splits_dw = c[best].dw.splits;
+        for (int i = 0; i < 2; ++i) {
+            c[i].da.splits = splits_da;
+            c[i].dw.splits = splits_dw;
+            if (!da) c[i].da.out = nullptr;
+            if (!dw) c[i].dw.out = nullptr;
+            us[i] = cost_of(c[i].da, c[i].dw, c[i].size);
+        }
+        best = 2.0 * T * K * Nout < 3.2e10 || 1.05 * us[0] < us[1] ? 0 : 1;
+    }
+    Choice got = c[best];
+    got.da.out = got.dw.out = nullptr;
+    if (!da) got.da = Prod{};
+    if (!dw) got.dw = Prod{};
+    return got;
 }
 
 int64_t part_bytes(const Prod& p) { return p.splits > 1 ? p.splits * p.M * p.N * 4 : 0; }
@@ -499,19 +521,8 @@ using namespace engram;
 extern "C" int64_t engram_wkv_backward_workspace_bytes(int64_t T, int32_t K, int32_t Nout) {
     if (!shape_ok(T, K, Nout)) return -1;
     if (T == 0) return 0;
-    // what the call asking for both, or for either, needs at most
-    int64_t need = 0;
-    for (int ask = 1; ask <= 3; ++ask) {
-        const int size = tile_size(T, K, Nout, ask == 3);
-        Prod da = prod_of(T, K, Nout, size), dw = prod_of(Nout, K, T, size);
-        int asked;  // (no output is written here)
-        if (ask & 1) da.out = &asked;
-        if (ask & 2) dw.out = &asked;
-        split(da, dw, size);
-        const int64_t bytes = (da.out ? part_bytes(da) : 0) + (dw.out ? part_bytes(dw) : 0);
-        need = bytes > need ? bytes : need;
-    }
-    return need;
+    const Choice c = choose(T, K, Nout, true, true);
+    return part_bytes(c.da) + part_bytes(c.dw);  // (either alone needs its own of the two)
 }
 
 extern "C" int engram_wkv_backward(const uint16_t* dkv, const uint16_t* a, const uint16_t* w, uint16_t* da, void* dw,
@@ -536,21 +547,19 @@ extern "C" int engram_wkv_backward(const uint16_t* dkv, const uint16_t* a, const
         if (!dw || accumulate) return ENGRAM_OK;
         return launch_zero(dw, static_cast<int64_t>(Nout) * K * (dw_dtype == ENGRAM_F32 ? 4 : 2), s, what);
     }
-    const int size = tile_size(T, K, Nout, da && dw);
+    const Choice c = choose(T, K, Nout, da != nullptr, dw != nullptr);
     GradArgs g = {};
-    g.da = prod_of(T, K, Nout, size);
+    g.da = c.da;
     g.da.p = dkv;
     g.da.q = w;
     g.da.out = da;
-    g.dw = prod_of(Nout, K, T, size);
+    g.dw = c.dw;
     g.dw.p = dkv;
     g.dw.q = a;
     g.dw.out = dw;
     g.dw.out_f32 = dw_dtype == ENGRAM_F32;
     g.dw.accumulate = accumulate != 0;
-    split(g.da, g.dw, size);
-    if (!da) g.da = Prod{};
-    if (!dw) g.dw = Prod{};
+    const int size = c.size;
     const int64_t need = part_bytes(g.da) + part_bytes(g.dw);
     g.da.part = static_cast<float*>(workspace);
     g.dw.part = g.da.part + part_bytes(g.da) / 4;

@@ -650,8 +650,8 @@ int64_t engram_gate_output_backward_workspace_bytes(int64_t T, int32_t hc, int32
 /*
  * engram_wkv_backward -- the gradient of engram_wkv, kv = a * w^T:
  *   da = bf16(dkv * w);   dw = round(dkv^T * a [+ dw if accumulate]);  fp32 accumulation,
- * in an order set by the sizes and by which of the two are asked for: the same call gives
- * the same bits.
+ * in an order set by the sizes alone: the same bits from every call, whether or not the
+ * other of the two is asked for.
  *
  * dkv   uint16 [T, Nout] bf16 bits; 16-byte aligned
  * a     uint16 [T, K] bf16 bits (unused if dw is NULL); 16-byte aligned

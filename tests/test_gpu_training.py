@@ -460,6 +460,20 @@ def test_wkv_backward(gpu_device, T, K, N, dwt):
     _within(acc, want, tol + (ref.U16 if dwt == BF else 2 * ref.U32) * want.abs(), "accumulated dw")
 
 
+@pytest.mark.parametrize("T,K,N", [
+    (64, 1536, 25600), (251, 1536, 25600), (2048, 1536, 25600), (4000, 1536, 5120), (5984, 344, 9624), (5687, 584, 5416),
+    (8000, 456, 2000), (8192, 256, 1320), (300, 320, 600), (700, 1032, 12552), (1, 8, 8)])
+def test_wkv_backward_alone_gives_the_same_bits(gpu_device, T, K, N):
+    """Whether the other product is asked for changes neither's sum (the large shapes' splits differ between the two)."""
+    g = _eng()
+    gen = torch.Generator(device=gpu_device).manual_seed(T + K)
+    r = lambda *s: torch.empty(s, device=gpu_device).normal_(generator=gen).to(BF)  # noqa: E731
+    dkv, a, w = r(T, N), r(T, K), r(N, K)
+    da, dw = g.engram_wkv_backward(dkv, a, w)
+    assert torch.equal(g.engram_wkv_backward(dkv, None, w, need_dw=False)[0], da)
+    assert torch.equal(g.engram_wkv_backward(dkv, a, None, need_da=False)[1], dw)
+
+
 def test_wkv_backward_selects_rows(gpu_device):
     """One-hot operands: da picks a row of w, dw a row of a, exactly, at every tile and k-step position."""
     g, T, K, N = _eng(), 300, 320, 600

@@ -57,6 +57,26 @@ def test_embed(gpu_device, tdt, odt, n, R, D, idt, row_start):
     assert torch.equal(torch.nan_to_num(out.cpu().float()), torch.nan_to_num(want.float()))
 
 
+# (n, D) of at least 2^24 elements, from where a thread takes four rows; odd counts, every width's kernel; the last of each
+# width over 256 MB of output, which passes the caches
+@pytest.mark.parametrize("tdt,odt", [(BF, BF), (BF, F32), (F32, BF), (F32, F32)])
+@pytest.mark.parametrize("n,D", [
+    (699051, 24), (262145, 64), (2100003, 64), (233017, 72), (1048579, 128), (131073, 136), (550001, 256), (32767, 512),
+    (32768, 512), (63551, 264), (290003, 520), (3283, 5120), (30001, 5120), (2047, 8200), (17001, 8200)])
+def test_embed_of_many_rows(gpu_device, n, D, tdt, odt):
+    g, R = _eng(), 1003
+    gen = torch.Generator(device=gpu_device).manual_seed(n)
+    table = torch.empty((R, D), device=gpu_device).normal_(generator=gen).to(tdt)
+    ids = torch.randint(-1, R + 1, (n,), generator=gen, device=gpu_device)
+    out = torch.full((n + 7, D), NAN, dtype=odt, device=gpu_device)
+    g.engram_embed(ids, table, scale=1.7, out=out[:n])
+    assert out[n:].isnan().all()
+    want = (torch.cat([table, torch.zeros((1, D), dtype=tdt, device=gpu_device)]).float() * torch.tensor(1.7)).to(odt)
+    r = torch.where((ids < 0) | (ids >= R), R, ids)
+    for i in range(0, n, 1 << 18):
+        assert torch.equal(out[:n][i:i + (1 << 18)], want[r[i:i + (1 << 18)]]), i
+
+
 def test_embed_shapes_and_refusals(gpu_device):
     g = _eng()
     table = torch.ones((4, 16), dtype=BF, device=gpu_device)
@@ -144,6 +164,58 @@ def test_embed_grad_at_the_sorts_edges(gpu_device, n, kind):
 def test_embed_grad_many_tiles(gpu_device, n, R, D, kind):
     gen = torch.Generator().manual_seed(n)
     _check_grad(_eng(), _ids_of(kind, n, R, gen), _randn(gen, (n, D), BF), R, D, gpu_device, F32, what=kind)
+
+
+@pytest.mark.parametrize("kind", ["one", "distinct", "runs", "zipf"])
+@pytest.mark.parametrize("n,R,D", [
+    (512, 90, 16), (513, 90, 16), (512, 3988006, 8), (513, 3988006, 8), (524288, 60000, 8), (524289, 60000, 8),
+    (600001, 3988006, 8), (786433, 700, 8)])
+def test_embed_grad_where_its_forms_hand_over(gpu_device, n, R, D, kind):
+    """512 ids: one launch; 524,288: tiles of four ids a thread, past that eight."""
+    gen = torch.Generator().manual_seed(n + 1)
+    ids = _ids_of(kind, n, R, gen)
+    _check_grad(_eng(), ids, _randn(gen, (n, D), BF), R, D, gpu_device, F32, what=kind)
+
+
+@pytest.mark.parametrize("gdt,odt", [(BF, F32), (F32, BF)])
+@pytest.mark.parametrize("n,R,D", [(1400003, 50001, 32), (700001, 30001, 64), (355003, 90001, 128), (131101, 20001, 256),
+                                   (131101, 20001, 264)])
+def test_embed_grad_past_the_caches(gpu_device, n, R, D, gdt, odt):
+    """More than 256 MB moved: upstream and finished rows pass the caches, in both forms, for every count of lanes a row has.
+    References on the GPU, in 64 bits."""
+    g = _eng()
+    gen = torch.Generator(device=gpu_device).manual_seed(n)
+    ids = (R * torch.rand(n, generator=gen, device=gpu_device).double() ** 3).long()
+    ids[::17] = R
+    up = torch.empty((n, D), device=gpu_device).normal_(generator=gen).to(gdt)
+    want = torch.zeros((R + 1, D), dtype=torch.float64, device=gpu_device)
+    mag = torch.zeros_like(want)
+    want.index_add_(0, ids, up.double())
+    mag.index_add_(0, ids, up.double().abs())
+    want, mag = want[:R], mag[:R]
+    tol = ref.sum_tolerance(want, mag, int(torch.bincount(ids)[:R].max()), odt == BF)
+    dense = g.engram_embed_grad(ids, up, R, out_dtype=odt)
+    assert ((dense.double() - want).abs() <= tol).all()
+    unique, rows, count = g.engram_embed_grad_rows(ids, up, R, out_dtype=odt)
+    u, c = torch.unique(ids[ids < R]), int(count)
+    assert c == u.numel() and torch.equal(unique[:c], u) and (unique[c:] == -1).all()
+    assert torch.equal(rows[:c], dense[u]) and not rows[c:].any()
+
+
+@pytest.mark.parametrize("n", [100, 3000, 9000])
+def test_embed_grad_of_more_zeros_than_a_grid_holds(gpu_device, n):
+    """34.6 GB of gradient: what is past 32 GiB has a launch of its own, in each of the three forms."""
+    g, R, D = _eng(), 135000003, 64
+    pick = torch.tensor([0, 1, 134217727, 134217728, 134217729, R - 2, R - 1], device=gpu_device)
+    ids = pick.repeat(n)[:n]
+    up = torch.ones((n, D), dtype=BF, device=gpu_device)
+    grad = torch.full((R, D), NAN, device=gpu_device)
+    g.engram_embed_grad(ids, up, R, out=grad)
+    assert torch.equal(grad[pick, 0], torch.bincount(ids)[pick].float())
+    assert (grad[pick] == grad[pick, :1]).all()
+    grad[pick] = 0
+    for i in range(0, R, 1 << 24):
+        assert not grad[i:i + (1 << 24)].any(), i
 
 
 @pytest.mark.parametrize("n", [3, 900, 5000, 280000])

@@ -546,6 +546,36 @@ def test_wkv_backward_alone_gives_the_same_bits(gpu_device, T, K, N):
     assert torch.equal(g.engram_wkv_backward(dkv, a, None, need_da=False)[1], dw)
 
 
+@pytest.mark.parametrize("dwt", [F32, BF])
+@pytest.mark.parametrize("T,K,N", [
+    (251, 1536, 25600), (2049, 1544, 25608), (521, 1544, 25608),     # 256 x 256 tiles, da's sum split
+    (33001, 1032, 5128), (30011, 520, 8200), (70001, 1544, 1288),    # the same, dW's sum split, alone too
+    (60013, 248, 2056), (40003, 264, 5128),                          # 128 x 128 ones for dW alone and for both
+    (261, 6144, 25600), (131, 6152, 2568), (3001, 6144, 1288)])      # the released head_dim's reduction
+def test_wkv_backward_of_whole_numbers(gpu_device, T, K, N, dwt):
+    """Entries of -2 to 2: every sum (280,004 at most) is exact in float32 in any order, so one lost, doubled or misplaced
+    term of any tile, slab or part shows."""
+    g = _eng()
+    gen = torch.Generator(device=gpu_device).manual_seed(T + K)
+
+    def whole(*shape):
+        buf = torch.full((math.prod(shape) + 65536,), NAN, dtype=BF, device=gpu_device)  # what is read past it shows
+        buf[:-65536] = torch.randint(-2, 3, (math.prod(shape),), generator=gen, device=gpu_device).to(BF)
+        return buf[:-65536].view(shape)
+
+    dkv, a, w = whole(T, N), whole(T, K), whole(N, K)
+    da = torch.mm(dkv.double(), w.double())
+    dw = torch.mm(dkv.double().t().contiguous(), a.double())
+    assert da.abs().max() < 2 ** 24 and dw.abs().max() < 2 ** 24
+    got = g.engram_wkv_backward(dkv, a, w, dw_dtype=dwt)
+    assert torch.equal(got[0], da.to(BF)) and torch.equal(got[1], dw.to(dwt))
+    assert torch.equal(g.engram_wkv_backward(dkv, None, w, need_dw=False)[0], da.to(BF))
+    assert torch.equal(g.engram_wkv_backward(dkv, a, None, need_da=False, dw_dtype=dwt)[1], dw.to(dwt))
+    base = torch.randint(-9, 10, (N, K), generator=gen, device=gpu_device).to(dwt)
+    want = (dw + base.double()).to(dwt)
+    assert torch.equal(g.engram_wkv_backward(dkv, a, w, dw=base, accumulate=True)[1], want)
+
+
 def test_wkv_backward_selects_rows(gpu_device):
     """One-hot operands: da picks a row of w, dw a row of a, exactly, at every tile and k-step position."""
     g, T, K, N = _eng(), 300, 320, 600

@@ -413,6 +413,20 @@ def test_gate_backward(gpu_device, T, hc, dim, masked):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("hc", [1, 2, 4])
+@pytest.mark.parametrize("dim", [504, 1016, 2040, 2056, 2568, 5112, 5120, 5128, 8192])
+def test_gate_backward_at_every_width(gpu_device, hc, dim):
+    """Every count of copies that has a kernel of its own at every count of threads; some workgroups take two tokens."""
+    g, T = _eng(), 290
+    x, kv, q, k, dot, dout = _gate_inputs(T, hc, dim, dim + hc)
+    mask = torch.rand(T, generator=torch.Generator().manual_seed(dim)) < 0.8
+    mask[0], mask[256] = True, True  # (the first workgroup's two)
+    x[~mask], kv[~mask], dot[~mask] = NAN, NAN, NAN
+    d = lambda t: t.to(gpu_device)  # noqa: E731
+    got = g.engram_gate_output_backward(*[d(t) for t in (x, kv, q, k)], 1e-20, d(dot), d(dout), token_mask=d(mask))
+    _check_gate(got, ref.gate_backward(x, kv, q, k, 1e-20, dot, dout, mask), T, dim, f"{hc} {dim}")
+
+
 def test_gate_backward_all_masked_and_no_tokens(gpu_device):
     g = _eng()
     x, kv, q, k, dot, dout = [t.to(gpu_device) for t in _gate_inputs(6, 4, 64, 1)]

@@ -21,7 +21,7 @@
 //
 // Measured: the lookup of 65,536 rows of 5,120 bf16 140 us (808 MB, 5.8 TB/s); the dense gradient of 8,192 such rows over
 // 129,280 table rows in fp32 465 us (2.73 GB, 5.9 TB/s: 418 the zeros with the sort beneath them, 38 the fold, 8 the
-// join); the distinct rows of 1,572,864 hashed ids of 64 220 us (629 MB: 71 the sort, 8 the counts, 121 the fold, 15 the
+// join); the distinct rows of 1,572,864 hashed ids of 64 220 us (629 MB: 76 the sort, 8 the counts, 120 the fold, 15 the
 // join and the tail), of 196,608 ids 65 us, bound by its nine launches at 4 to 9 us each.
 #include "rows.h"
 

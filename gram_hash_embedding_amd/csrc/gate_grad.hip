@@ -13,8 +13,8 @@
 //
 // HBM-bound: per token (3 hc + 1) rows of dim are read and 2 hc + 1 written, every one once.  A workgroup holds a
 // whole token, one 16-byte piece of every row per thread: the rows stay in registers between the sums that need all
-// of a row and the outputs that need the sums, and the sum over tokens of dq and dk stays in registers over all of
-// the workgroup's tokens.  The next token's rows are asked for as this one's are used up, so loads are in flight over
+// of a row and the outputs that need the sums, and the sum over tokens of dq and dk stays in registers (in LDS for four
+// copies of more than 5,120 columns) over all of the workgroup's tokens.  The next token's rows are asked for as this one's are used up, so loads are in flight over
 // the barrier (one per token: the sums of the waves, in two LDS buffers taken in turn).  A second launch adds the
 // workgroups' sums in their order, so the same call gives the same bits.
 //

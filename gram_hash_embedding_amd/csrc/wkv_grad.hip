@@ -18,7 +18,8 @@
 //
 // Bound by the matrix cores where T is long: 8,192 x 1,536 x 25,600, both products, 1,053 us, 1.22 PFLOP/s (a large square
 // library product reaches 1.45-1.55 here; da alone 606 us, dW 584).  Below some 1,000 tokens by memory: W read and dW
-// written, 250 MB at 251 tokens in 85 us (da alone 45, dW 45: da waits on its slabs, one of which is in flight per workgroup).
+// written, 250 MB at 251 tokens in 85 us (64 where two sets of inputs in turn leave some of W in the Infinity Cache; da alone 47, dW 43: da
+// waits on its slabs, one of which is in flight per workgroup).
 #include <type_traits>
 
 #include "rows.h"

@@ -635,7 +635,8 @@ int engram_embed_grad_rows(const void* ids, int32_t id_bytes, int64_t T, int64_t
  * workspace  engram_gate_output_backward_workspace_bytes(T, hc, dim) bytes, 16-byte aligned,
  *            caller-owned scratch (no initialisation needed)
  * Limits: T >= 0; 1 <= hc <= 64; 8 <= dim <= 8192 and dim % 8 == 0 (hc 1, 2 and 4
- * keep a token's sums in registers; other counts go through the workspace).
+ * keep the sums over tokens in registers, hc 4 past 5,120 columns in LDS; other counts
+ * go through the workspace).
  * Too small a workspace -> ENGRAM_ERANGE.
  */
 int engram_gate_output_backward(const uint16_t* x, const uint16_t* kv, int64_t ld_kv, const uint16_t* q_weight,
@@ -672,8 +673,8 @@ int64_t engram_wkv_backward_workspace_bytes(int64_t T, int32_t K, int32_t Nout);
 
 /*
  * engram_grad_norm -- the 2-norm of `tensors` gradients taken as one vector:
- *   norm = sqrt(sum of the squares of all their elements), summed in fp32 and fp64 in a
- *   fixed order; 0 for no elements.
+ *   norm = sqrt(sum of the squares of all their elements), summed in fp64 in a fixed
+ *   order; 0 for no elements.
  *
  * grads  host array of device pointers to contiguous elements (aligned to their
  *        size; 16-byte aligned ones are read 16 bytes at a time)

@@ -31,6 +31,13 @@ and the gradients that train the module and its embeddings (training.py):
     engram_embed_grad, engram_embed_grad_rows -- its gradient by sorted ids, dense or as the distinct rows
     engram_gate_output_backward, engram_wkv_backward -- the gradients of engram_gate_output and engram_wkv
     engram_grad_norm, engram_clip_grads -- the norm of many gradients together, and clipping by it
+
+and its narrow formats (lowbit.py):
+
+    engram_mx4_quant, engram_mx4_pack_weight -- bf16 rows -> OCP MX fp4, and such weights in the products' layout
+    engram_wkv_mx4, engram_wkv_mx4_gate -- the wkv projection on 4-bit weights, plain and fused with the gate dot
+    engram_ckpt_save, engram_ckpt_load -- 8-bit checkpoints (OCP MX int8) of bf16 rows
+    engram_gate_output_ckpt, engram_gate_output_backward_ckpt -- the gate's training step with 8-bit checkpoints
 """
 from __future__ import annotations
 
@@ -93,9 +100,10 @@ def lib() -> ctypes.CDLL:
         L.engram_status_string.restype = ctypes.c_char_p
         L.engram_last_error.argtypes = []
         L.engram_last_error.restype = ctypes.c_char_p
-        from .training import declare
+        from . import lowbit, training
 
-        declare(L)
+        training.declare(L)
+        lowbit.declare(L)
         _lib = L
     return _lib
 
@@ -718,9 +726,11 @@ def engram_gate_residual(x, value, dot, token_mask=None, out=None, stream=None):
 
 from . import training as _training  # noqa: E402  (it uses the helpers above)
 from .training import *  # noqa: E402,F401,F403
+from . import lowbit as _lowbit  # noqa: E402
+from .lowbit import *  # noqa: E402,F401,F403
 
 __all__ = ["engram_hash", "engram_hash_gather_packed", "engram_gather_dequant", "engram_wkv", "engram_gate_dot", "engram_gate_output",
            "engram_wkv_gate", "engram_wkv_gate_layers", "engram_wkv_gate_layers_noalloc", "NOALLOC_SCRATCH_BYTES",
            "engram_wkv_gate_workspace_bytes", "engram_gather_dequant_fmt", "SCALE_FORMATS", "engram_mx_quant", "engram_gather_mx", "engram_wkv_mx", "engram_wkv_mx_gate", "engram_mx_scale_bytes", "engram_gate_residual", "engram_pack_table",
            "engram_gather_dequant_packed", "EngramError", "lib",
-           "LIB_PATH"] + _training.__all__
+           "LIB_PATH"] + _training.__all__ + _lowbit.__all__

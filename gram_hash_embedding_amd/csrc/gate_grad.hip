@@ -1,5 +1,7 @@
 // engram_gate_output_backward: the gradient of engram_gate_output (the gate pre-activation, the sigmoid gate and the
 // residual) with respect to the stream, the keys, the value and the two gate weights.
+// engram_gate_output_backward_ckpt: the same from the checkpoints of the stream, the keys and the value in 8 bits
+// (checkpoint.hip): the values they stand for, which bf16 holds exactly, in the same arithmetic.
 //
 // With h = x[t,c], key = kv[t,c], v the token's value row, w = q * k, d = the pre-activation the forward gave,
 // rh = rsqrt(mean h^2 + eps), rk = rsqrt(mean key^2 + eps), s = rh rk dim^-1/2 and up the gradient of the output:
@@ -23,6 +25,7 @@
 // 5,120 125 (4.7); 3 of 2,048 184 (3.1, the kernel for any count of copies, which takes a barrier a copy).
 #include <type_traits>
 
+#include "mx.h"
 #include "rows.h"
 
 namespace engram {
@@ -38,6 +41,10 @@ struct GateGradArgs {
     int64_t ld_kv;
     const uint16_t* q;
     const uint16_t* k;
+    const int8_t* xq;   // checkpoints instead of x and kv: [T, hc, dim], [T, hc + 1, dim], a scale per 32 columns of a row
+    const uint8_t* xs;
+    const int8_t* kvq;
+    const uint8_t* kvs;
     const float* dot;
     const uint16_t* up;
     const uint8_t* mask;
@@ -54,6 +61,53 @@ __device__ inline float wave_sum(float v) {
     for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
     return v;
 }
+
+// Where the rows of the stream (copy c of token t) and of the keys and the value (row c of token t, the value's being hc)
+// come from: eight consecutive elements of one, as they lie in memory until they are widened.
+struct FromBf16 {
+    Piece<Bf16> r;
+    __device__ inline void zero() { r.v = u32x4{0, 0, 0, 0}; }
+    template <bool kNt>
+    __device__ inline void get(const uint16_t* row, int piece) {
+        if constexpr (kNt) r.load_nt(row, piece);
+        else r.load(row, piece);
+    }
+    template <bool kNt>
+    __device__ inline void load_x(const GateGradArgs& p, int hc, int64_t t, int c, int piece) {
+        get<kNt>(p.x + (t * hc + c) * p.dim, piece);
+    }
+    template <bool kNt>
+    __device__ inline void load_kv(const GateGradArgs& p, int hc, int64_t t, int c, int piece) {
+        get<kNt>(p.kv + t * p.ld_kv + static_cast<int64_t>(c) * p.dim, piece);
+    }
+    __device__ inline void to(float (&f)[8]) const { r.to(f); }
+    __device__ inline void keep() { asm volatile("" : "+v"(r.v)); }
+};
+struct FromInt8 {
+    mx_u32x2 q;
+    uint32_t code;
+    __device__ inline void zero() {
+        q = mx_u32x2{0, 0};
+        code = 0;
+    }
+    template <bool kNt>
+    __device__ inline void get(const int8_t* rows, const uint8_t* scales, int64_t row, int dim, int piece) {
+        const mx_u32x2* at = reinterpret_cast<const mx_u32x2*>(rows + row * dim) + piece;
+        if constexpr (kNt) q = __builtin_nontemporal_load(at);
+        else q = *at;
+        code = scales[row * ((dim + 31) / 32) + (piece >> 2)];
+    }
+    template <bool kNt>
+    __device__ inline void load_x(const GateGradArgs& p, int hc, int64_t t, int c, int piece) {
+        get<kNt>(p.xq, p.xs, t * hc + c, p.dim, piece);
+    }
+    template <bool kNt>
+    __device__ inline void load_kv(const GateGradArgs& p, int hc, int64_t t, int c, int piece) {
+        get<kNt>(p.kvq, p.kvs, t * (hc + 1) + c, p.dim, piece);
+    }
+    __device__ inline void to(float (&f)[8]) const { mxint8_decode8(q, mxint8_unit(code), f); }
+    __device__ inline void keep() { asm volatile("" : "+v"(q), "+v"(code)); }
+};
 
 // the scalars of one (token, copy)
 struct Coef {
@@ -112,7 +166,7 @@ __device__ inline float wave_sum_last(float v) {
 // The LDS holds q * k (read for every token from L2 it cost 428 us where this takes 342, 8,192 x 4 x 5,120); of a workgroup
 // of more than 640 threads and four copies, whose registers do not hold rows and sums together, the sums instead, and q
 // and k come from L2 a copy ahead.
-template <int HC, int kMaxThreads>
+template <int HC, int kMaxThreads, class From>
 __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) {
     constexpr int kSums = 3 * HC, kReads = (kSums + 3) / 4;
     __shared__ float sums[2][4 * kReads][kMaxWaves];  // [sum][wave]; waves the workgroup lacks hold zeros
@@ -162,13 +216,14 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) 
     }
     __syncthreads();
     float acc[kSumsInLds ? 1 : HC][8] = {};
-    Piece<Bf16> hr[HC], kr[HC], ur[HC], vr;
+    From hr[HC], kr[HC], vr;
+    Piece<Bf16> ur[HC];
     auto load_copy = [&](int64_t t, int c) {
-        hr[c].load_nt(p.x + (t * HC + c) * p.dim, piece);
-        kr[c].load_nt(p.kv + t * p.ld_kv + static_cast<int64_t>(c) * p.dim, piece);
+        hr[c].template load_x<true>(p, HC, t, c, piece);
+        kr[c].template load_kv<true>(p, HC, t, c, piece);
         ur[c].load_nt(p.up + (t * HC + c) * p.dim, piece);
     };
-    auto load_value = [&](int64_t t) { vr.load_nt(p.kv + t * p.ld_kv + static_cast<int64_t>(HC) * p.dim, piece); };
+    auto load_value = [&](int64_t t) { vr.template load_kv<true>(p, HC, t, HC, piece); };
     // the first token from t on that takes part; the masked ones before it are done with on the way
     auto next = [&](int64_t t) {
         for (; t < p.T && p.mask && p.mask[t] == 0; t += gridDim.x)
@@ -177,9 +232,13 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) 
     };
     int turn = 0;
     int64_t t = next(blockIdx.x);
-    vr.v = u32x4{0, 0, 0, 0};
+    vr.zero();
 #pragma unroll
-    for (int c = 0; c < HC; ++c) hr[c].v = kr[c].v = ur[c].v = u32x4{0, 0, 0, 0};
+    for (int c = 0; c < HC; ++c) {
+        hr[c].zero();
+        kr[c].zero();
+        ur[c].v = u32x4{0, 0, 0, 0};
+    }
     if (live && t < p.T) {
         load_value(t);
 #pragma unroll
@@ -217,7 +276,11 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) 
         __syncthreads();
         // the rows as they were loaded: widened again below rather than held as floats over the barrier
 #pragma unroll
-        for (int c = 0; c < HC; ++c) asm volatile("" : "+v"(hr[c].v), "+v"(kr[c].v), "+v"(ur[c].v));
+        for (int c = 0; c < HC; ++c) {
+            hr[c].keep();
+            kr[c].keep();
+            asm volatile("" : "+v"(ur[c].v));
+        }
         // each 16 lanes add one sum over the waves: read j of lane l is sum 4 j + l / 16 of wave l % 16
         float part[kReads];
 #pragma unroll
@@ -297,6 +360,7 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs p) 
 
 // Any other number of copies: one copy after the other, the sums over tokens in the workgroup's own row of `part`
 // (each thread reads and writes only its piece).
+template <class From>
 __global__ __launch_bounds__(1024) void gate_grad_any_kernel(GateGradArgs p) {
     __shared__ float sums[2][kMaxWaves][3];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
@@ -314,18 +378,19 @@ __global__ __launch_bounds__(1024) void gate_grad_any_kernel(GateGradArgs p) {
             if (live) masked_token(p, t, piece);
             continue;
         }
-        const uint16_t* row = p.kv + t * p.ld_kv;
-        Piece<Bf16> r = {u32x4{0, 0, 0, 0}};
+        From f;
+        f.zero();
+        Piece<Bf16> r;
         float v[8], dv[8] = {};
-        if (live) r.load(row + static_cast<int64_t>(p.hc) * p.dim, piece);
-        r.to(v);
+        if (live) f.template load_kv<false>(p, p.hc, t, p.hc, piece);
+        f.to(v);
         for (int c = 0; c < p.hc; ++c) {
             float h[8] = {}, key[8] = {}, u[8] = {}, hh = 0.f, kk = 0.f, dg = 0.f;
             if (live) {
-                r.load(p.x + (t * p.hc + c) * p.dim, piece);
-                r.to(h);
-                r.load(row + static_cast<int64_t>(c) * p.dim, piece);
-                r.to(key);
+                f.template load_x<false>(p, p.hc, t, c, piece);
+                f.to(h);
+                f.template load_kv<false>(p, p.hc, t, c, piece);
+                f.to(key);
                 r.load(p.up + (t * p.hc + c) * p.dim, piece);
                 r.to(u);
             }
@@ -413,15 +478,15 @@ __global__ __launch_bounds__(1024) void gate_grad_sum_kernel(const float* part, 
     dk[col] = s * __uint_as_float(static_cast<uint32_t>(q[col]) << 16);
 }
 
-template <int HC>
+template <int HC, class From>
 void launch_gate_grad(const GateGradArgs& p, int64_t groups, int threads, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(groups)), block(threads);
-    if (threads <= 64) hipLaunchKernelGGL((gate_grad_kernel<HC, 64>), grid, block, 0, s, p);
-    else if (threads <= 128) hipLaunchKernelGGL((gate_grad_kernel<HC, 128>), grid, block, 0, s, p);
-    else if (threads <= 256) hipLaunchKernelGGL((gate_grad_kernel<HC, 256>), grid, block, 0, s, p);
-    else if (threads <= 384) hipLaunchKernelGGL((gate_grad_kernel<HC, 384>), grid, block, 0, s, p);
-    else if (threads <= 640) hipLaunchKernelGGL((gate_grad_kernel<HC, 640>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((gate_grad_kernel<HC, 1024>), grid, block, 0, s, p);
+    if (threads <= 64) hipLaunchKernelGGL((gate_grad_kernel<HC, 64, From>), grid, block, 0, s, p);
+    else if (threads <= 128) hipLaunchKernelGGL((gate_grad_kernel<HC, 128, From>), grid, block, 0, s, p);
+    else if (threads <= 256) hipLaunchKernelGGL((gate_grad_kernel<HC, 256, From>), grid, block, 0, s, p);
+    else if (threads <= 384) hipLaunchKernelGGL((gate_grad_kernel<HC, 384, From>), grid, block, 0, s, p);
+    else if (threads <= 640) hipLaunchKernelGGL((gate_grad_kernel<HC, 640, From>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((gate_grad_kernel<HC, 1024, From>), grid, block, 0, s, p);
 }
 
 int threads_of(int dim) { return (dim / 8 + 63) / 64 * 64; }
@@ -439,6 +504,76 @@ bool shape_ok(int64_t T, int32_t hc, int32_t dim) {
     return T >= 0 && hc >= 1 && hc <= 64 && dim >= 8 && dim % 8 == 0 && dim <= kMaxDim;
 }
 
+// the two launches of either entry point
+template <class From>
+int launch_backward(GateGradArgs p, float* dq, float* dk, hipStream_t s, const char* what) {
+    p.inv_dim = 1.0f / static_cast<float>(p.dim);
+    p.rsqrt_dim = static_cast<float>(1.0 / __builtin_sqrt(static_cast<double>(p.dim)));
+    const int64_t groups = groups_of(p.T, p.hc, p.dim);
+    const int threads = threads_of(p.dim);
+    if (p.T > 0) {
+        if (p.hc == 4) launch_gate_grad<4, From>(p, groups, threads, s);
+        else if (p.hc == 2) launch_gate_grad<2, From>(p, groups, threads, s);
+        else if (p.hc == 1) launch_gate_grad<1, From>(p, groups, threads, s);
+        else hipLaunchKernelGGL(gate_grad_any_kernel<From>, dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s, p);
+    }
+    const int cols = p.hc * p.dim;
+    // few columns: fewer of them per workgroup, so that there are workgroups enough
+    const int rows = static_cast<int>(groups);
+    if (cols >= 64 * kCUs)
+        hipLaunchKernelGGL(gate_grad_sum_kernel<64>, dim3((cols + 63) / 64), dim3(1024), 0, s, p.part, rows, cols, p.q, p.k, dq,
+                           dk);
+    else
+        hipLaunchKernelGGL(gate_grad_sum_kernel<16>, dim3((cols + 15) / 16), dim3(1024), 0, s, p.part, rows, cols, p.q, p.k, dq,
+                           dk);
+    return check_launch(what);
+}
+
+// What either entry point asks of its sizes, and of its pointers (`rows_null`, `rows_misaligned`: of the rows it reads): a
+// status, with the reason left for engram_last_error.
+int check_sizes(const GateGradArgs& p, const char* what) {
+    if (p.T < 0) return fail(ENGRAM_EINVAL, "%s: T < 0", what);
+    if (p.hc < 1 || p.hc > 64) return fail(ENGRAM_EINVAL, "%s: hc=%d outside [1, 64]", what, p.hc);
+    if (p.dim < 8 || p.dim % 8 != 0 || p.dim > kMaxDim)
+        return fail(ENGRAM_EINVAL, "%s: dim=%d must be a multiple of 8 in [8, %d]", what, p.dim, kMaxDim);
+    return ENGRAM_OK;
+}
+int check_pointers(const GateGradArgs& p, const float* dq, const float* dk, bool rows_null, bool rows_misaligned,
+                   int64_t workspace_bytes, const char* what) {
+    if (!p.q || !p.k || !dq || !dk) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
+    if (!aligned(p.q, 16) || !aligned(p.k, 16) || !aligned(dq, 4) || !aligned(dk, 4))
+        return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
+    if (p.T == 0) return ENGRAM_OK;
+    if (rows_null || !p.dot || !p.up || !p.dx || !p.dkv || !p.part) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
+    if (rows_misaligned || !aligned(p.up, 16) || !aligned(p.dx, 16) || !aligned(p.dkv, 16) || !aligned(p.dot, 4) ||
+        !aligned(p.part, 16))
+        return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
+    const int64_t need = groups_of(p.T, p.hc, p.dim) * p.hc * p.dim * 4;
+    if (workspace_bytes < need)
+        return fail(ENGRAM_ERANGE, "%s: workspace of %lld bytes, needs %lld", what, (long long)workspace_bytes,
+                    (long long)need);
+    return ENGRAM_OK;
+}
+
+GateGradArgs common_args(const uint16_t* q_weight, const uint16_t* k_weight, float eps, const float* dot, const uint16_t* dout,
+                         const uint8_t* token_mask, uint16_t* dx, uint16_t* dkv, void* workspace, int64_t T, int32_t hc,
+                         int32_t dim) {
+    GateGradArgs p = {};
+    p.q = q_weight;
+    p.k = k_weight;
+    p.dot = dot;
+    p.up = dout;
+    p.mask = token_mask;
+    p.dx = dx;
+    p.dkv = dkv;
+    p.part = static_cast<float*>(workspace);
+    p.T = T;
+    p.hc = hc;
+    p.dim = dim;
+    p.eps = eps;
+    return p;
+}
+
 }  // namespace
 }  // namespace engram
 
@@ -454,59 +589,34 @@ extern "C" int engram_gate_output_backward(const uint16_t* x, const uint16_t* kv
                                            void* workspace, int64_t workspace_bytes, int64_t T, int32_t hc, int32_t dim,
                                            void* stream) {
     const char* what = "engram_gate_output_backward";
-    if (T < 0) return fail(ENGRAM_EINVAL, "%s: T < 0", what);
-    if (hc < 1 || hc > 64) return fail(ENGRAM_EINVAL, "%s: hc=%d outside [1, 64]", what, hc);
-    if (dim < 8 || dim % 8 != 0 || dim > kMaxDim)
-        return fail(ENGRAM_EINVAL, "%s: dim=%d must be a multiple of 8 in [8, %d]", what, dim, kMaxDim);
+    GateGradArgs p = common_args(q_weight, k_weight, eps, dot, dout, token_mask, dx, dkv, workspace, T, hc, dim);
+    int rc = check_sizes(p, what);
+    if (rc != ENGRAM_OK) return rc;
     if (ld_kv < static_cast<int64_t>(hc + 1) * dim || ld_kv % 8 != 0)
         return fail(ENGRAM_EINVAL, "%s: ld_kv=%lld must be >= (hc+1)*dim and a multiple of 8", what, (long long)ld_kv);
-    if (!q_weight || !k_weight || !dq || !dk) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
-    if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(dq, 4) || !aligned(dk, 4))
-        return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
-    if (T > 0) {
-        if (!x || !kv || !dot || !dout || !dx || !dkv || !workspace) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
-        if (!aligned(x, 16) || !aligned(kv, 16) || !aligned(dout, 16) || !aligned(dx, 16) || !aligned(dkv, 16) ||
-            !aligned(dot, 4) || !aligned(workspace, 16))
-            return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
-    }
-    const int64_t groups = groups_of(T, hc, dim);
-    if (T > 0 && workspace_bytes < groups * hc * dim * 4)
-        return fail(ENGRAM_ERANGE, "%s: workspace of %lld bytes, needs %lld", what, (long long)workspace_bytes,
-                    (long long)(groups * hc * dim * 4));
-    hipStream_t s = as_stream(stream);
-    GateGradArgs p = {};
+    rc = check_pointers(p, dq, dk, !x || !kv, !aligned(x, 16) || !aligned(kv, 16), workspace_bytes, what);
+    if (rc != ENGRAM_OK) return rc;
     p.x = x;
     p.kv = kv;
     p.ld_kv = ld_kv;
-    p.q = q_weight;
-    p.k = k_weight;
-    p.dot = dot;
-    p.up = dout;
-    p.mask = token_mask;
-    p.dx = dx;
-    p.dkv = dkv;
-    p.part = static_cast<float*>(workspace);
-    p.T = T;
-    p.hc = hc;
-    p.dim = dim;
-    p.eps = eps;
-    p.inv_dim = 1.0f / static_cast<float>(dim);
-    p.rsqrt_dim = static_cast<float>(1.0 / __builtin_sqrt(static_cast<double>(dim)));
-    const int threads = threads_of(dim);
-    if (T > 0) {
-        if (hc == 4) launch_gate_grad<4>(p, groups, threads, s);
-        else if (hc == 2) launch_gate_grad<2>(p, groups, threads, s);
-        else if (hc == 1) launch_gate_grad<1>(p, groups, threads, s);
-        else hipLaunchKernelGGL(gate_grad_any_kernel, dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s, p);
-    }
-    const int cols = hc * dim;
-    // few columns: fewer of them per workgroup, so that there are workgroups enough
-    const int rows = static_cast<int>(groups);
-    if (cols >= 64 * kCUs)
-        hipLaunchKernelGGL(gate_grad_sum_kernel<64>, dim3((cols + 63) / 64), dim3(1024), 0, s, p.part, rows, cols, q_weight,
-                           k_weight, dq, dk);
-    else
-        hipLaunchKernelGGL(gate_grad_sum_kernel<16>, dim3((cols + 15) / 16), dim3(1024), 0, s, p.part, rows, cols, q_weight,
-                           k_weight, dq, dk);
-    return check_launch(what);
+    return launch_backward<FromBf16>(p, dq, dk, as_stream(stream), what);
+}
+
+extern "C" int engram_gate_output_backward_ckpt(const int8_t* x_q, const uint8_t* x_scale, const int8_t* kv_q,
+                                                const uint8_t* kv_scale, const uint16_t* q_weight, const uint16_t* k_weight,
+                                                float eps, const float* dot, const uint16_t* dout, const uint8_t* token_mask,
+                                                uint16_t* dx, uint16_t* dkv, float* dq, float* dk, void* workspace,
+                                                int64_t workspace_bytes, int64_t T, int32_t hc, int32_t dim, void* stream) {
+    const char* what = "engram_gate_output_backward_ckpt";
+    GateGradArgs p = common_args(q_weight, k_weight, eps, dot, dout, token_mask, dx, dkv, workspace, T, hc, dim);
+    int rc = check_sizes(p, what);
+    if (rc == ENGRAM_OK)
+        rc = check_pointers(p, dq, dk, !x_q || !x_scale || !kv_q || !kv_scale, !aligned(x_q, 8) || !aligned(kv_q, 8),
+                            workspace_bytes, what);
+    if (rc != ENGRAM_OK) return rc;
+    p.xq = x_q;
+    p.xs = x_scale;
+    p.kvq = kv_q;
+    p.kvs = kv_scale;
+    return launch_backward<FromInt8>(p, dq, dk, as_stream(stream), what);
 }

@@ -1,0 +1,373 @@
+// The `wkv` Linear with 4-bit block-scaled weights, in the OCP microscaling (MX) fp4 format: E2M1 elements, one E8M0
+// scale per 32 consecutive input columns of a row.
+//
+//   engram_mx4_quant        -- bf16 rows -> MXFP4 (activations, and the weights' one-off conversion)
+//   engram_mx4_pack_weight  -- MXFP4 weights -> the layout that the products read (one-off)
+//   engram_wkv_mx4          -- kv = A * W^T, A in MXFP8 or MXFP4, with v_mfma_scale_f32_16x16x128_f8f6f4
+//   engram_wkv_mx4_gate     -- the same fused with the gate pre-activation (Engram.forward's rstd and dot)
+//
+// Weight layout: uint8 [ceil(N/64)][K/128][4352], a record for 64 rows and 128 columns: four W operands of the matrix
+// instruction as its lanes hold them, 1 KB each (operand j: rows 16 j .. 16 j + 15; lane l = 16 c + r has the 16 bytes of row
+// 16 j + r, columns 32 c .. 32 c + 31, the even column in the low half of a byte), then a 32-bit word per lane with its scale
+// in each operand (byte j: row 16 j + r, block c).  So a wave reads a W operand with one load a lane, 1 KB in a row, straight
+// into registers, and the scales of four with one load; the instruction picks a scale's byte by its operand selector.
+//
+// The instruction's lanes, measured on gfx950: of a 4-bit operand lane l holds row l % 16, columns 32 (l / 16) .. +31 (16
+// bytes); of an 8-bit one columns 16 (l / 16) .. +15 and 64 + 16 (l / 16) .. +15 (32 bytes); the scale operand of lane l is
+// that of row l % 16 and block l / 16 in either format.  Lane l of the result holds rows 4 (l / 16) .. +3 of column l % 16.
+// W is the first operand, so a lane has four consecutive outputs of one token.
+#include <type_traits>
+
+#include "common.h"
+#include "mx.h"
+
+namespace engram {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kStepCols = 128;    // columns of one matrix instruction
+constexpr int kGroupRows = 64;    // weight rows of a record
+constexpr int kRecord = 4352;     // bytes of a record: 4 x 1,024 of elements, 256 of scales
+constexpr int kFp8 = 0, kFp4 = 4; // the instruction's format selectors
+
+struct Mx4Args {
+    const uint8_t* a;    // [M, K] E4M3 or [M, K/2] E2M1 pairs
+    const uint8_t* as;   // [K/128][M4][4] E8M0
+    const uint8_t* w;    // packed records
+    uint16_t* kv;        // [M, ld_out] bf16: the columns from n_key on
+    int64_t M, M4, ld_out;
+    int N, steps;        // columns, K / 128
+    // the fused gate: columns below n_key are keys, reduced against the stream and not stored
+    const uint16_t* x;   // [M, hc, dim] bf16
+    const uint16_t* q;   // [hc, dim] bf16
+    const uint16_t* k;
+    float* part;         // [hc][dim/128][3][M]: per 128 columns sum(h w key), sum(key^2), sum(h^2)
+    int dim, n_key;
+};
+
+__device__ inline uint32_t pack_bf16(float lo, float hi) {
+    const bf16x2 v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};  // to nearest even
+    return __builtin_bit_cast(uint32_t, v);
+}
+__device__ inline bf16x2 as_pair(uint32_t w) { return __builtin_bit_cast(bf16x2, w); }
+__device__ inline float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ inline float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// a token operand of the matrix instruction
+template <bool kA8>
+struct AFrag;
+template <>
+struct AFrag<true> {
+    i32x4 lo, hi;
+    __device__ inline i32x8 get() const { return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}; }
+};
+template <>
+struct AFrag<false> {
+    i32x4 lo;
+    __device__ inline i32x8 get() const { return i32x8{lo[0], lo[1], lo[2], lo[3], 0, 0, 0, 0}; }
+};
+
+// acc += (W operand, scales in byte kSel of sw) x (token operand, scale in byte 0 of sa)
+template <bool kA8, int kSel>
+__device__ inline f32x4 mfma(const i32x4& w, int sw, const AFrag<kA8>& a, int sa, f32x4 acc) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(i32x8{w[0], w[1], w[2], w[3], 0, 0, 0, 0}, a.get(), acc, kFp4,
+                                                            kA8 ? kFp8 : kFp4, kSel, sw, 0, sa);
+}
+
+// ---- the sums of a (token, 4 columns) piece of a key row against the stream
+struct GateSums {
+    float hwk, kk, hh;
+};
+__device__ inline void gate_add(GateSums& s, const f32x4& acc, u32x2 h, u32x2 q, u32x2 k) {
+    // the product is a bf16 tensor before it is used, as the other forms of the projection round it
+    const uint32_t k01 = pack_bf16(acc[0], acc[1]), k23 = pack_bf16(acc[2], acc[3]);
+    const float key[4] = {lo_bf16(k01), hi_bf16(k01), lo_bf16(k23), hi_bf16(k23)};
+    const float hv[4] = {lo_bf16(h[0]), hi_bf16(h[0]), lo_bf16(h[1]), hi_bf16(h[1])};
+    const float w[4] = {lo_bf16(q[0]) * lo_bf16(k[0]), hi_bf16(q[0]) * hi_bf16(k[0]), lo_bf16(q[1]) * lo_bf16(k[1]),
+                        hi_bf16(q[1]) * hi_bf16(k[1])};  // exact: bf16 * bf16 fits fp32
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        s.hwk += hv[e] * w[e] * key[e];
+        s.kk += key[e] * key[e];
+        s.hh += hv[e] * hv[e];
+    }
+}
+
+// ---- few tokens: a wave per 16 weight rows and 16 MI tokens, every operand straight from memory to registers, kDepth steps
+// of 128 columns in flight.  A workgroup has 64 rows (a gate launch: 128, whose sums meet in LDS).
+template <bool kA8, int MI, bool kGate>
+__global__ __launch_bounds__(kGate ? 512 : 256) void mx4_direct_kernel(Mx4Args p, int groups_n) {
+    constexpr int kDepth = 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, r = lane & 15, j = wave & 3;
+    const int bn = static_cast<int>(blockIdx.x % groups_n);
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x / groups_n) * (16 * MI);
+    const int group = (kGate ? 2 : 1) * bn + (wave >> 2);
+    const uint8_t* w = p.w + static_cast<int64_t>(group) * p.steps * kRecord;
+    const uint8_t* a[MI];
+    const uint8_t* as[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int64_t m = min(m0 + 16 * i + r, p.M - 1);  // rows past the last repeat it; they are not stored
+        a[i] = p.a + m * p.steps * (kA8 ? 128 : 64) + 16 * g;
+        as[i] = p.as + m * 4 + g;
+    }
+    i32x4 wf[kDepth];
+    AFrag<kA8> af[kDepth][MI];
+    int sw[kDepth], sa[kDepth][MI];
+    auto load = [&](int d, int s) {
+        const uint8_t* rec = w + static_cast<int64_t>(s) * kRecord;
+        wf[d] = *reinterpret_cast<const i32x4*>(rec + 1024 * j + 16 * lane);
+        sw[d] = rec[4096 + 4 * lane + j];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const uint8_t* row = a[i] + static_cast<int64_t>(s) * (kA8 ? 128 : 64);
+            af[d][i].lo = *reinterpret_cast<const i32x4*>(row);
+            if constexpr (kA8) af[d][i].hi = *reinterpret_cast<const i32x4*>(row + 64);
+            sa[d][i] = as[i][static_cast<int64_t>(s) * p.M4 * 4];
+        }
+    };
+    f32x4 acc[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) acc[i] = f32x4{};
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load(d, min(d, p.steps - 1));
+    for (int s0 = 0; s0 < p.steps; s0 += kDepth) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            if (s0 + d < p.steps) {
+#pragma unroll
+                for (int i = 0; i < MI; ++i) acc[i] = mfma<kA8, 0>(wf[d], sw[d], af[d][i], sa[d][i], acc[i]);
+            }
+            load(d, min(s0 + d + kDepth, p.steps - 1));
+        }
+    }
+    const int n = kGroupRows * group + 16 * j + 4 * g;  // the lane's four columns
+    if (!kGate || n >= p.n_key) {  // (a workgroup's columns are all keys or none)
+        if (n >= p.N) return;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int64_t m = m0 + 16 * i + r;
+            if (m < p.M)
+                *reinterpret_cast<u32x2*>(p.kv + m * p.ld_out + (n - p.n_key)) =
+                    u32x2{pack_bf16(acc[i][0], acc[i][1]), pack_bf16(acc[i][2], acc[i][3])};
+        }
+        return;
+    }
+    if constexpr (kGate) {
+        __shared__ float sums[3][8][16 * MI];
+        const u32x2 q = *reinterpret_cast<const u32x2*>(p.q + n), k = *reinterpret_cast<const u32x2*>(p.k + n);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int64_t m = min(m0 + 16 * i + r, p.M - 1);
+            GateSums s = {0.f, 0.f, 0.f};
+            gate_add(s, acc[i], *reinterpret_cast<const u32x2*>(p.x + m * p.n_key + n), q, k);
+            s.hwk += __shfl_xor(s.hwk, 16, 64);
+            s.kk += __shfl_xor(s.kk, 16, 64);
+            s.hh += __shfl_xor(s.hh, 16, 64);
+            s.hwk += __shfl_xor(s.hwk, 32, 64);
+            s.kk += __shfl_xor(s.kk, 32, 64);
+            s.hh += __shfl_xor(s.hh, 32, 64);
+            if (g == 0) {
+                sums[0][wave][16 * i + r] = s.hwk;
+                sums[1][wave][16 * i + r] = s.kk;
+                sums[2][wave][16 * i + r] = s.hh;
+            }
+        }
+        __syncthreads();
+        const int tid = threadIdx.x;
+        if (tid < 3 * 16 * MI) {
+            const int which = tid / (16 * MI), t = tid % (16 * MI);
+            float v = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v += sums[which][e][t];
+            if (m0 + t < p.M) p.part[(static_cast<int64_t>(bn) * 3 + which) * p.M + m0 + t] = v;
+        }
+    }
+}
+
+// ---- quantisation of bf16 rows: a thread has 8 consecutive columns, the 4 threads of a block find its largest magnitude (as
+// bit patterns, whose order is the magnitudes').  floor(log2 amax) is the pattern's exponent field less the bias; E2M1's
+// largest exponent is 2, so the shared scale's code is the field less 2, or 0 where that is below E8M0's range (fields 0, of
+// zeros and subnormals, to 2).  v_cvt_scalef32_pk_fp4_bf16 divides by the scale, rounds to nearest even and saturates at 6 --
+// checked on every bf16 pattern.  A block with an infinity or a NaN, which E2M1 has not, takes the NaN scale 0xFF and zeros.
+__global__ __launch_bounds__(256) void mx4_quant_kernel(const uint16_t* x, int64_t rows, int K, int64_t rows4, uint8_t* q,
+                                                        uint8_t* scale) {
+    const int64_t gid = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int per_row = K / 8;
+    const int64_t r = gid / per_row;
+    const int c8 = static_cast<int>(gid - r * per_row);
+    const bool ok = r < rows;
+    u32x4 v = {0, 0, 0, 0};
+    if (ok) v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + r * K) + c8);
+    // the 4 threads of a block are lanes 4 b .. 4 b + 3 of the wave (K / 8 is a multiple of 4)
+    const uint32_t field = block_top(bf16_top8(v)) >> 7;
+    const uint32_t code = field == 255 ? 255u : field > 2 ? field - 2 : 0u;
+    const float by = __uint_as_float(code == 0 ? 0x00400000u : code << 23);  // 2^(code - 127)
+    uint32_t e = 0;
+    e = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(e, as_pair(v[0]), by, 0);
+    e = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(e, as_pair(v[1]), by, 1);
+    e = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(e, as_pair(v[2]), by, 2);
+    e = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(e, as_pair(v[3]), by, 3);
+    if (!ok) return;
+    *reinterpret_cast<uint32_t*>(q + r * (K / 2) + 4 * c8) = field == 255 ? 0u : e;
+    if ((c8 & 3) == 0) scale[mx_scale_offset(r, c8 / 4, rows4)] = static_cast<uint8_t>(code);
+}
+
+// a workgroup per record
+__global__ __launch_bounds__(256) void mx4_pack_kernel(const uint8_t* q, const uint8_t* scale, int N, int steps, int64_t rows4,
+                                                       uint8_t* packed) {
+    const int s = static_cast<int>(blockIdx.x % steps), group = static_cast<int>(blockIdx.x / steps);
+    uint8_t* rec = packed + static_cast<int64_t>(blockIdx.x) * kRecord;
+    const int t = threadIdx.x;
+    {
+        const int j = t >> 6, c = (t >> 4) & 3, r = t & 15;
+        const int64_t n = static_cast<int64_t>(group) * kGroupRows + 16 * j + r;
+        u32x4 v = {0, 0, 0, 0};
+        if (n < N) v = *reinterpret_cast<const u32x4*>(q + (n * steps + s) * 64 + 16 * c);
+        *reinterpret_cast<u32x4*>(rec + 16 * t) = v;
+    }
+    {
+        const int c = t >> 6, r = (t >> 2) & 15, j = t & 3;
+        const int64_t n = static_cast<int64_t>(group) * kGroupRows + 16 * j + r;
+        rec[4096 + t] = n < N ? scale[(static_cast<int64_t>(s) * rows4 + n) * 4 + c] : 0;
+    }
+}
+
+constexpr int64_t kMostGroups = (1 << 23) - 1;  // workgroups of a launch: its threads have to stay under 2^32
+
+template <bool kA8, bool kGate>
+int launch_direct(const Mx4Args& p, hipStream_t stream, const char* what) {
+    const int groups_n = (p.N + (kGate ? 128 : 64) - 1) / (kGate ? 128 : 64);
+    const int mi = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
+    const int64_t groups = (p.M + 16 * mi - 1) / (16 * mi) * groups_n;
+    if (groups > kMostGroups) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
+    const dim3 grid(static_cast<unsigned>(groups)), block(kGate ? 512 : 256);
+    if (mi == 1) hipLaunchKernelGGL((mx4_direct_kernel<kA8, 1, kGate>), grid, block, 0, stream, p, groups_n);
+    else if (mi == 2) hipLaunchKernelGGL((mx4_direct_kernel<kA8, 2, kGate>), grid, block, 0, stream, p, groups_n);
+    else hipLaunchKernelGGL((mx4_direct_kernel<kA8, 4, kGate>), grid, block, 0, stream, p, groups_n);
+    return check_launch(what);
+}
+
+constexpr int kMaxK = 1 << 20, kMaxN = 1 << 22;
+
+// what is wrong with the operands' sizes, or null
+const char* bad_shape(int64_t T, int32_t a_bits, int32_t K, int32_t N) {
+    if (T < 0) return "T < 0";
+    if (a_bits != 4 && a_bits != 8) return "a_bits must be 4 or 8";
+    if (K < kStepCols || K % kStepCols != 0 || K > kMaxK) return "K must be a multiple of 128 in [128, 2^20]";
+    if (N < 8 || N % 8 != 0 || N > kMaxN) return "the columns must be a multiple of 8 in [8, 2^22]";
+    return nullptr;
+}
+
+}  // namespace
+}  // namespace engram
+
+using namespace engram;
+
+extern "C" int engram_mx4_quant(const uint16_t* x, int64_t rows, int32_t K, uint8_t* q, uint8_t* scale, void* stream) {
+    const char* what = "engram_mx4_quant";
+    if (rows < 0) return fail(ENGRAM_EINVAL, "%s: rows < 0", what);
+    if (K < kStepCols || K % kStepCols != 0)
+        return fail(ENGRAM_EINVAL, "%s: K=%d must be a positive multiple of %d", what, K, kStepCols);
+    if (rows == 0) return ENGRAM_OK;
+    if (!x || !q || !scale) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
+    if (!aligned(x, 16) || !aligned(q, 4)) return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
+    if (rows > kMostGroups * 256 / (K / 8)) return fail(ENGRAM_EINVAL, "%s: too many rows", what);
+    const int64_t blocks = (rows * (K / 8) + 255) / 256;
+    hipLaunchKernelGGL(mx4_quant_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, as_stream(stream), x, rows, K,
+                       (rows + 3) / 4 * 4, q, scale);
+    return check_launch(what);
+}
+
+extern "C" int64_t engram_mx4_weight_bytes(int32_t Nout, int32_t K) {
+    if (bad_shape(0, 4, K, Nout)) return -1;
+    return static_cast<int64_t>((Nout + kGroupRows - 1) / kGroupRows) * (K / kStepCols) * kRecord;
+}
+
+extern "C" int engram_mx4_pack_weight(const uint8_t* q, const uint8_t* scale, int32_t Nout, int32_t K, uint8_t* packed,
+                                      void* stream) {
+    const char* what = "engram_mx4_pack_weight";
+    if (const char* bad = bad_shape(0, 4, K, Nout)) return fail(ENGRAM_EINVAL, "%s: %s", what, bad);
+    if (!q || !scale || !packed) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
+    if (!aligned(q, 16) || !aligned(packed, 16)) return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
+    const int64_t records = engram_mx4_weight_bytes(Nout, K) / kRecord;
+    if (records > kMostGroups) return fail(ENGRAM_EINVAL, "%s: weights too large", what);
+    hipLaunchKernelGGL(mx4_pack_kernel, dim3(static_cast<unsigned>(records)), dim3(256), 0, as_stream(stream), q, scale, Nout,
+                       K / kStepCols, (static_cast<int64_t>(Nout) + 3) / 4 * 4, packed);
+    return check_launch(what);
+}
+
+extern "C" int engram_wkv_mx4(const uint8_t* a, const uint8_t* a_scale, int32_t a_bits, const uint8_t* w, uint16_t* kv,
+                              int64_t T, int32_t K, int32_t Nout, void* stream) {
+    const char* what = "engram_wkv_mx4";
+    if (const char* bad = bad_shape(T, a_bits, K, Nout)) return fail(ENGRAM_EINVAL, "%s: %s", what, bad);
+    if (T == 0) return ENGRAM_OK;
+    if (!a || !a_scale || !w || !kv) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
+    if (!aligned(a, 16) || !aligned(a_scale, 16) || !aligned(w, 16) || !aligned(kv, 16))
+        return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
+    Mx4Args p = {};
+    p.a = a;
+    p.as = a_scale;
+    p.w = w;
+    p.kv = kv;
+    p.M = T;
+    p.M4 = (T + 3) / 4 * 4;
+    p.ld_out = Nout;
+    p.N = Nout;
+    p.steps = K / kStepCols;
+    return a_bits == 8 ? launch_direct<true, false>(p, as_stream(stream), what)
+                       : launch_direct<false, false>(p, as_stream(stream), what);
+}
+
+extern "C" int engram_wkv_mx4_gate(const uint8_t* a, const uint8_t* a_scale, int32_t a_bits, const uint8_t* w,
+                                   const uint16_t* x, const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                                   uint16_t* value, int64_t ld_value, float* dot, void* workspace, int64_t workspace_bytes,
+                                   int64_t T, int32_t K, int32_t hc, int32_t dim, void* stream) {
+    const char* what = "engram_wkv_mx4_gate";
+    if (hc < 1 || hc > 64) return fail(ENGRAM_EINVAL, "%s: hc=%d outside [1, 64]", what, hc);
+    if (dim < 256 || dim % 256 != 0)
+        return fail(ENGRAM_EINVAL, "%s: dim=%d must be a positive multiple of 256", what, dim);
+    if (static_cast<int64_t>(hc + 1) * dim > kMaxN)
+        return fail(ENGRAM_EINVAL, "%s: (hc + 1) * dim = %lld exceeds 2^22", what, static_cast<long long>(hc + 1) * dim);
+    const int N = (hc + 1) * dim;
+    if (const char* bad = bad_shape(T, a_bits, K, N)) return fail(ENGRAM_EINVAL, "%s: %s", what, bad);
+    if (ld_value < dim || ld_value % 8 != 0)
+        return fail(ENGRAM_EINVAL, "%s: ld_value=%lld must be >= dim and a multiple of 8", what, (long long)ld_value);
+    const int64_t need = engram_wkv_gate_workspace_bytes(T, hc, dim);
+    if (workspace_bytes < need)
+        return fail(ENGRAM_ERANGE, "%s: workspace of %lld bytes, %lld needed", what, (long long)workspace_bytes,
+                    (long long)need);
+    if (T == 0) return ENGRAM_OK;
+    if (!a || !a_scale || !w || !x || !q_weight || !k_weight || !value || !dot || !workspace)
+        return fail(ENGRAM_EINVAL, "%s: null pointer", what);
+    if (!aligned(a, 16) || !aligned(a_scale, 16) || !aligned(w, 16) || !aligned(x, 16) || !aligned(q_weight, 16) ||
+        !aligned(k_weight, 16) || !aligned(value, 16) || !aligned(dot, 4) || !aligned(workspace, 16))
+        return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
+    Mx4Args p = {};
+    p.a = a;
+    p.as = a_scale;
+    p.w = w;
+    p.kv = value;
+    p.M = T;
+    p.M4 = (T + 3) / 4 * 4;
+    p.ld_out = ld_value;
+    p.N = N;
+    p.steps = K / kStepCols;
+    p.x = x;
+    p.q = q_weight;
+    p.k = k_weight;
+    p.part = static_cast<float*>(workspace);
+    p.dim = dim;
+    p.n_key = hc * dim;
+    const int rc = a_bits == 8 ? launch_direct<true, true>(p, as_stream(stream), what)
+                               : launch_direct<false, true>(p, as_stream(stream), what);
+    if (rc != ENGRAM_OK) return rc;
+    float* dots[1] = {dot};
+    return launch_gate_finalize(static_cast<const float*>(workspace), 0, dots, 1, T, hc, dim, eps, as_stream(stream), what);
+}

@@ -15,20 +15,22 @@ that order.
 Training runs the same layers back: `EngramForward.backward` takes a layer's output gradient through the gate and the
 residual (engram_gate_output_backward), the projection (engram_wkv_backward) and the lookup (engram_embed_grad_rows) to
 the gradients of its stream, its weights and the table rows its ids reach; `clip_grads` clips a list of those and any
-other gradients by their common norm (engram_grad_norm, engram_clip_grads).
+other gradients by their common norm (engram_grad_norm, engram_clip_grads).  A layer run with `checkpoint=True` keeps what
+its gradient reads in 8 bits (engram_gate_output_ckpt) instead of the stream and the projection's output.
 """
 from __future__ import annotations
 
 import dataclasses
 from typing import List, Optional
 
-from . import (engram_clip_grads, engram_embed_grad_rows, engram_embed_grad_workspace_bytes, engram_gate_dot,
-               engram_gate_output, engram_gate_output_backward, engram_gate_output_backward_workspace_bytes,
+from . import (GateCheckpoint, engram_clip_grads, engram_embed_grad_rows, engram_embed_grad_workspace_bytes, engram_gate_dot,
+               engram_gate_output, engram_gate_output_backward, engram_gate_output_backward_ckpt,
+               engram_gate_output_backward_workspace_bytes, engram_gate_output_ckpt,
                engram_gate_residual, engram_gather_dequant,
                engram_gather_dequant_packed, engram_gather_mx, engram_grad_norm, engram_hash, engram_hash_gather_packed,
-               engram_mx_quant, engram_wkv, engram_wkv_gate, engram_wkv_gate_layers,
+               engram_mx4_quant, engram_mx_quant, engram_wkv, engram_wkv_gate, engram_wkv_gate_layers,
                engram_wkv_backward, engram_wkv_backward_workspace_bytes, engram_wkv_gate_workspace_bytes, engram_wkv_mx,
-               engram_wkv_mx_gate)
+               engram_wkv_mx4, engram_wkv_mx4_gate, engram_wkv_mx_gate)
 
 
 @dataclasses.dataclass
@@ -58,6 +60,17 @@ class LayerWeights:
     packed: "Optional[torch.Tensor]" = None  # uint8 [R, 2*D]: the same table as one record per row (engram_pack_table)
     # the wkv weight in the fp8 block-scaled (OCP MX) form: (E4M3 bytes [Nout, K], E8M0 scales), for fp8=True
     wkv_mx: "Optional[tuple]" = None
+    # the wkv weight in OCP MX fp4, packed (engram_mx4_quant, then engram_mx4_pack_weight), for fp4=True
+    wkv_mx4: "Optional[torch.Tensor]" = None
+
+
+@dataclasses.dataclass
+class LayerCheckpoint:
+    """What EngramForward.layer keeps of a layer for its gradient under `checkpoint=True` (tensors of its own: several calls'
+    checkpoints may live at once).  The rows that the projection read are not kept: they are gathered again."""
+
+    rows: GateCheckpoint           # the stream, the keys and the value in 8 bits
+    dot: "torch.Tensor"            # float32 [T, hc]
 
 
 @dataclasses.dataclass
@@ -166,16 +179,12 @@ class EngramForward:
                 hash_ids, lw.weight, lw.scale, lw.block_size, lw.row_start, layer=e, out=a))
         return a
 
-    def layer_fp8(self, e: int, hash_ids, x, events=None, packed=False, a=None, fused=False, gather_mx=False):
-        """(a bf16 [T, C*D], kv bf16 [T, Nout], dot fp32 [T, hc]) of layer e with the fp8 block-scaled projection:
-        the gathered rows quantised to MX fp8 (engram_mx_quant), engram_wkv_mx against the layer's MX weights,
-        then engram_gate_dot; with `fused`, (a, value bf16 [T, dim], dot) from engram_wkv_mx_gate instead.
-        With `gather_mx` (and no `a`), the gather writes the MX rows itself (engram_gather_mx) and `a` is None."""
+    def _mx_rows(self, e, hash_ids, events, packed, a, gather_mx):
+        """(a, MX fp8 rows [T, K], their scales) of layer e: the bf16 rows `a` (gathered here if not given) quantised, or,
+        with `gather_mx` and no `a`, the MX rows straight from the table, a staying None."""
         import torch
 
         lw = self.layers[e]
-        if lw.wkv_mx is None:
-            raise ValueError(f"layer {e} has no fp8 (MX) projection weights")
         T = hash_ids.shape[0] * hash_ids.shape[1]
         dev = hash_ids.device
         K = self.C * lw.weight.shape[1]
@@ -196,6 +205,68 @@ class EngramForward:
             if a is None:
                 a = self.gather(e, hash_ids, events, packed)
             self._timed(events, "mx_quant", lambda: engram_mx_quant(a.view(T, K), q=aq, scale=asc))
+        return a, aq, asc
+
+    def layer_fp4(self, e: int, hash_ids, x, events=None, token_mask=None, output=False, fused=False, packed=False, a=None,
+                  gather_mx=False, a_bits=8):
+        """`layer` with the layer's 4-bit weights (LayerWeights.wkv_mx4): the rows in MX fp8 (as layer_fp8 has them: from
+        the gather itself with `gather_mx`), or with a_bits=4 rounded to MX fp4 (engram_mx4_quant), times the MX fp4 weights
+        (engram_wkv_mx4, or with `fused` engram_wkv_mx4_gate).  Returns what `layer` returns; a is None where the gather
+        wrote MX rows."""
+        import torch
+
+        lw = self.layers[e]
+        if lw.wkv_mx4 is None:
+            raise ValueError(f"layer {e} has no 4-bit (MX) projection weights")
+        if a_bits not in (4, 8):
+            raise ValueError("a_bits must be 4 or 8")
+        if a_bits == 4 and gather_mx:
+            raise ValueError("the gather writes MX fp8 rows, not MX fp4")
+        T = hash_ids.shape[0] * hash_ids.shape[1]
+        dev = hash_ids.device
+        K = self.C * lw.weight.shape[1]
+        if a_bits == 8:
+            a, aq, asc = self._mx_rows(e, hash_ids, events, packed, a, gather_mx)
+        else:
+            if a is None:
+                a = self.gather(e, hash_ids, events, packed)
+            aq = self._buf(("a_mx4", e), (T, K // 2), torch.uint8, dev)
+            asc = self._buf(("a_mx4_scale", e), (K // 128, (T + 3) // 4 * 4, 4), torch.uint8, dev)
+            self._timed(events, "mx4_quant", lambda: engram_mx4_quant(a.view(T, K), q=aq, scale=asc))
+        x3 = x.reshape(T, x.shape[-2], x.shape[-1])
+        hc, dim = x3.shape[1], x3.shape[2]
+        dot = self._buf(("dot", e), (T, hc), torch.float32, dev)
+        out = self._buf(("out", e), tuple(x.shape), torch.bfloat16, dev) if output else None
+        if fused:
+            kv = self._buf(("value", e), (T, dim), torch.bfloat16, dev)
+            ws = self._buf("workspace", (engram_wkv_gate_workspace_bytes(T, hc, dim),), torch.uint8, dev)
+            self._timed(events, "wkv_mx4_gate", lambda: engram_wkv_mx4_gate(
+                aq, asc, lw.wkv_mx4, x3, lw.q_weight, lw.k_weight, self.eps, value=kv, dot=dot, workspace=ws))
+            if output:
+                self._timed(events, "gate_residual", lambda: engram_gate_residual(x, kv, dot, token_mask, out=out))
+        else:
+            kv = self._buf(("kv", e), (T, (hc + 1) * dim), torch.bfloat16, dev)
+            self._timed(events, "wkv_mx4", lambda: engram_wkv_mx4(aq, asc, lw.wkv_mx4, out=kv))
+            if output:
+                self._timed(events, "gate_output", lambda: engram_gate_output(
+                    x, kv, lw.q_weight, lw.k_weight, self.eps, token_mask, out=out, dot=dot))
+            else:
+                self._timed(events, "gate_dot", lambda: engram_gate_dot(x3, kv, lw.q_weight, lw.k_weight, self.eps, out=dot))
+        return (a, kv, dot, out) if output else (a, kv, dot)
+
+    def layer_fp8(self, e: int, hash_ids, x, events=None, packed=False, a=None, fused=False, gather_mx=False):
+        """(a bf16 [T, C*D], kv bf16 [T, Nout], dot fp32 [T, hc]) of layer e with the fp8 block-scaled projection:
+        the gathered rows quantised to MX fp8 (engram_mx_quant), engram_wkv_mx against the layer's MX weights,
+        then engram_gate_dot; with `fused`, (a, value bf16 [T, dim], dot) from engram_wkv_mx_gate instead.
+        With `gather_mx` (and no `a`), the gather writes the MX rows itself (engram_gather_mx) and `a` is None."""
+        import torch
+
+        lw = self.layers[e]
+        if lw.wkv_mx is None:
+            raise ValueError(f"layer {e} has no fp8 (MX) projection weights")
+        T = hash_ids.shape[0] * hash_ids.shape[1]
+        dev = hash_ids.device
+        a, aq, asc = self._mx_rows(e, hash_ids, events, packed, a, gather_mx)
         if fused:
             x3 = x.reshape(T, x.shape[-2], x.shape[-1])
             hc, dim = x3.shape[1], x3.shape[2]
@@ -214,13 +285,14 @@ class EngramForward:
         return a, kv, dot
 
     def layer(self, e: int, hash_ids, x, events=None, token_mask=None, output=False, fused=False, packed=False,
-              a=None):
+              a=None, checkpoint=False):
         """(a bf16 [T, C*D], kv bf16 [T, Nout], dot fp32 [T, hc]) of layer e for x [T, hc, dim]
         (or [B, L, hc, dim]); with `output`, also the layer's output stream bf16 (x's shape), where
         token_mask [B, L] (False = pass through) shuts the gate.  With `fused`, the second tensor is
         the value bf16 [T, dim] alone (the keys are never stored).  With `packed`, the rows come from
         the layer's packed table (same values, one record per row).  With `a` (the layer's rows, already
-        gathered by `hash_gather`), no gather is launched.
+        gathered by `hash_gather`), no gather is launched.  With `output` and `checkpoint`, (LayerCheckpoint, the output
+        stream): what `backward` needs, in 8 bits, in place of a, kv and dot (kv is then a buffer that the layers share).
 
         The tensors are this object's buffers for layer e: the next call for the same layer
         overwrites them."""
@@ -229,8 +301,17 @@ class EngramForward:
         lw = self.layers[e]
         T = hash_ids.shape[0] * hash_ids.shape[1]
         dev = hash_ids.device
+        if checkpoint and (fused or not output):
+            raise ValueError("a checkpoint is of the layer's output, from the unfused projection")
         if a is None:
             a = self.gather(e, hash_ids, events, packed)
+        if checkpoint:
+            kv = self._buf("kv", (T, lw.wkv.shape[0]), torch.bfloat16, dev)
+            self._timed(events, "wkv", lambda: engram_wkv(a.view(T, -1), lw.wkv, out=kv))
+            out = self._buf(("out", e), tuple(x.shape), torch.bfloat16, dev)
+            _, dot, rows = self._timed(events, "gate_output_ckpt", lambda: engram_gate_output_ckpt(
+                x, kv, lw.q_weight, lw.k_weight, self.eps, token_mask, out=out))
+            return LayerCheckpoint(rows, dot), out
         x3 = x.reshape(T, x.shape[-2], x.shape[-1])
         dot = self._buf(("dot", e), (T, x3.shape[1]), torch.float32, dev)
         if fused:
@@ -254,16 +335,22 @@ class EngramForward:
         self._timed(events, "gate_dot", lambda: engram_gate_dot(x3, kv, lw.q_weight, lw.k_weight, self.eps, out=dot))
         return a, kv, dot
 
-    def backward(self, e: int, hash_ids, x, a, kv, dot, dout, token_mask=None, events=None, dx=None):
+    def backward(self, e: int, hash_ids, x=None, a=None, kv=None, dot=None, dout=None, token_mask=None, events=None,
+                 dx=None, checkpoint=None, packed=False):
         """LayerGrads of layer e from `dout`, the gradient of the output stream of `layer(e, hash_ids, x, token_mask=...,
-        output=True)`, and what that call returned: a, kv and dot.  `dx` (dout itself is allowed) receives the stream's
-        gradient; by default it is a new tensor."""
+        output=True)`, and what that call returned: a, kv and dot -- or, of a call with checkpoint=True, its LayerCheckpoint
+        (x, kv and dot are then not read, and `a` is gathered again, from the packed table with `packed`, unless given).
+        `dx` (dout itself is allowed) receives the stream's gradient; by default it is a new tensor."""
         import torch
 
         lw = self.layers[e]
         T = hash_ids.shape[0] * hash_ids.shape[1]
         dev = hash_ids.device
-        hc, dim = x.shape[-2], x.shape[-1]
+        if dout is None:
+            raise ValueError("backward needs dout")
+        hc, dim = dout.shape[-2], dout.shape[-1]
+        if checkpoint is not None and a is None:
+            a = self.gather(e, hash_ids, events, packed)
         D, N = lw.weight.shape[1], lw.wkv.shape[0]
         K, n = self.C * D, T * self.C
         ws = self._buf("backward_workspace", (max(16, engram_gate_output_backward_workspace_bytes(T, hc, dim),
@@ -279,9 +366,15 @@ class EngramForward:
         rows = self._buf(("rows", e), (n, D), torch.float32, dev)
         count = self._buf(("row_count", e), (1,), torch.int32, dev)
         if dx is None:
-            dx = torch.empty_like(x)
-        self._timed(events, "gate_output_backward", lambda: engram_gate_output_backward(
-            x, kv, lw.q_weight, lw.k_weight, self.eps, dot, dout, token_mask, dx=dx, dkv=dkv, dq=dq, dk=dk, workspace=ws))
+            dx = torch.empty_like(dout)
+        if checkpoint is not None:
+            self._timed(events, "gate_output_backward_ckpt", lambda: engram_gate_output_backward_ckpt(
+                checkpoint.rows, lw.q_weight, lw.k_weight, self.eps, checkpoint.dot, dout, token_mask, dx=dx, dkv=dkv, dq=dq,
+                dk=dk, workspace=ws))
+        else:
+            self._timed(events, "gate_output_backward", lambda: engram_gate_output_backward(
+                x, kv, lw.q_weight, lw.k_weight, self.eps, dot, dout, token_mask, dx=dx, dkv=dkv, dq=dq, dk=dk,
+                workspace=ws))
         self._timed(events, "wkv_backward", lambda: engram_wkv_backward(dkv, a.view(T, K), lw.wkv, da=da, dw=dw,
                                                                         workspace=ws))
         self._timed(events, "embed_grad_rows", lambda: engram_embed_grad_rows(
@@ -290,15 +383,18 @@ class EngramForward:
         return LayerGrads(dx, dw, dq, dk, ids, rows, count)
 
     def step(self, input_ids, start_pos: int, xs, token_mask=None, events=None, output=False, fused=False,
-             packed=False, hash_gather=False, all_layers=False, fp8=False, gather_mx=False):
+             packed=False, hash_gather=False, all_layers=False, fp8=False, gather_mx=False, fp4=False, a_bits=8):
         """One forward over all engram layers; xs[e] is layer e's residual stream [B, L, hc, dim]
         (or one tensor shared by all layers).  Returns the per-layer gate pre-activations, or with
         `output` the per-layer output streams (the pre-activations are then in the "dot" buffers).
         With `hash_gather`, the hash and every layer's packed gather are one launch; with `all_layers`
         (fused only), every layer's projection and gate pre-activation are one launch (their tiles share
         the CUs); with `fp8`, the projection is the fp8 block-scaled form (layer_fp8, fused or not; pre-activations
-        only), and with `gather_mx` its gathers write MX fp8 rows directly.
+        only), and with `gather_mx` its gathers write MX fp8 rows directly; with `fp4`, the projection's weights are the
+        4-bit ones (layer_fp4), its rows in MX fp8 or, with a_bits=4, in MX fp4.
         `events`: optional dict that collects (start, end) timing events per entry point."""
+        if fp8 and fp4:
+            raise ValueError("the projection's weights are the 8-bit ones or the 4-bit ones")
         if hash_gather:
             ids, rows = self.hash_gather(input_ids, start_pos, token_mask, events)
         else:
@@ -308,6 +404,11 @@ class EngramForward:
                 raise ValueError("the fp8 projection runs up to the pre-activation, one launch per layer")
             return [self.layer_fp8(e, ids, xs[e] if isinstance(xs, (list, tuple)) else xs, events, packed,
                                    rows[e], fused=fused, gather_mx=gather_mx)[-1] for e in range(self.E)]
+        if fp4:
+            if all_layers:
+                raise ValueError("the projection on 4-bit weights runs one launch per layer")
+            return [self.layer_fp4(e, ids, xs[e] if isinstance(xs, (list, tuple)) else xs, events, token_mask, output, fused,
+                                   packed, rows[e], gather_mx, a_bits)[-1] for e in range(self.E)]
         if all_layers:
             if not fused:
                 raise ValueError("all_layers needs the fused projection")
@@ -362,4 +463,4 @@ def _numel(shape) -> int:
     return n
 
 
-__all__ = ["HashState", "LayerWeights", "LayerGrads", "EngramForward", "clip_grads"]
+__all__ = ["HashState", "LayerWeights", "LayerCheckpoint", "LayerGrads", "EngramForward", "clip_grads"]

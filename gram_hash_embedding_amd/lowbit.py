@@ -1,0 +1,310 @@
+"""The module in narrow formats: the ctypes binding of libengram.so's 4-bit weights and 8-bit checkpoints
+(include/engram.h), under the same rules as the rest of the package -- GPU tensors in, dtype / shape / contiguity checked,
+no fallback.
+
+    engram_mx4_quant        -- bf16 rows -> OCP MX fp4 (E2M1 + E8M0 scale per 32 columns)
+    engram_mx4_pack_weight  -- MX fp4 weights -> the layout the products read (one-off)
+    engram_wkv_mx4          -- the wkv projection of MX fp8 or MX fp4 rows on MX fp4 weights
+    engram_wkv_mx4_gate     -- engram_wkv_mx4 fused with the gate dot (keys reduced in the projection)
+    engram_ckpt_save, engram_ckpt_load -- bf16 rows to 8-bit checkpoints (OCP MX int8) and back
+    engram_gate_output_ckpt -- engram_gate_output keeping its stream, keys and value in 8 bits
+    engram_gate_output_backward_ckpt -- engram_gate_output_backward from what was kept
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+from . import _check, engram_mx_scale_bytes, engram_wkv_gate_workspace_bytes, lib
+from . import training as _t
+
+RECORD_BYTES = 4352  # of the weight layout: 64 rows x 128 columns
+
+
+def declare(L: ctypes.CDLL) -> None:
+    """Argument and result types of these entry points."""
+    i64, i32, p, f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
+    L.engram_mx4_quant.argtypes = [p, i64, i32, p, p, p]
+    L.engram_mx4_weight_bytes.argtypes = [i32, i32]
+    L.engram_mx4_weight_bytes.restype = i64
+    L.engram_mx4_pack_weight.argtypes = [p, p, i32, i32, p, p]
+    L.engram_wkv_mx4.argtypes = [p, p, i32, p, p, i64, i32, i32, p]
+    L.engram_wkv_mx4_gate.argtypes = [p, p, i32, p, p, p, p, f32, p, i64, p, p, i64, i64, i32, i32, i32, p]
+    L.engram_ckpt_save.argtypes = [p, i64, i32, p, p, p]
+    L.engram_ckpt_load.argtypes = [p, p, i64, i32, p, p]
+    L.engram_gate_output_ckpt.argtypes = [p, p, i64, p, p, f32, p, p, p, p, p, p, p, i64, i32, i32, p]
+    L.engram_gate_output_backward_ckpt.argtypes = [p, p, p, p, p, p, f32, p, p, p, p, p, p, p, p, i64, i64, i32, i32, p]
+
+
+class GateCheckpoint(NamedTuple):
+    """What engram_gate_output_ckpt keeps of its rows."""
+
+    x: "torch.Tensor"          # int8 [T, hc, dim]
+    x_scale: "torch.Tensor"    # uint8 [T, hc, ceil(dim / 32)]
+    kv: "torch.Tensor"         # int8 [T, hc + 1, dim]: the keys, then the value
+    kv_scale: "torch.Tensor"   # uint8 [T, hc + 1, ceil(dim / 32)]
+
+
+def _scale_shape(rows: int, K: int):
+    return (K // 128, (rows + 3) // 4 * 4, 4)
+
+
+def engram_mx4_quant(x, q=None, scale=None, stream=None):
+    """(q uint8 [rows, K/2], scale uint8 [K/128, ceil4(rows), 4]): bf16 rows x [rows, K] in OCP MX fp4 (E2M1, two elements
+    a byte, the even column in the low half; an E8M0 scale per 32 columns in the layout of engram_mx_quant's)."""
+    on = _t._On(stream, x, "x")
+    torch = _t.torch
+    xp = on.ptr(x, "x", torch.bfloat16, 2)
+    rows, K = x.shape
+    need = engram_mx_scale_bytes(rows, K)
+    if q is None:
+        q = on.empty((rows, K // 2), torch.uint8)
+    elif q.shape != (rows, K // 2):
+        raise ValueError("q must be [rows, K/2]")
+    if scale is None:
+        scale = on.empty(_scale_shape(rows, K), torch.uint8)
+    elif scale.numel() != need:
+        raise ValueError(f"scale must hold {need} bytes")
+    _check(lib().engram_mx4_quant(xp, rows, K, on.ptr(q, "q", torch.uint8), on.ptr(scale, "scale", torch.uint8), on.handle))
+    return q, scale
+
+
+def engram_mx4_weight_bytes(nout: int, K: int) -> int:
+    n = lib().engram_mx4_weight_bytes(int(nout), int(K))
+    if n < 0:
+        raise ValueError(f"engram_wkv_mx4: Nout={nout} K={K} outside the limits")
+    return n
+
+
+def engram_mx4_pack_weight(q, scale, out=None, stream=None):
+    """Weights uint8 [ceil(Nout / 64), K / 128, 4352] in the layout the products read, from MX fp4 rows q uint8 [Nout, K/2]
+    and their scales (engram_mx4_quant's).  A one-off conversion."""
+    on = _t._On(stream, q, "q")
+    u8 = _t.torch.uint8
+    qp = on.ptr(q, "q", u8, 2)
+    N, K = q.shape[0], 2 * q.shape[1]
+    engram_mx4_weight_bytes(N, K)
+    if scale.numel() != engram_mx_scale_bytes(N, K):
+        raise ValueError("scale must be the MX scale array of q")
+    shape = ((N + 63) // 64, K // 128, RECORD_BYTES)
+    if out is None:
+        out = on.empty(shape, u8)
+    elif tuple(out.shape) != shape:
+        raise ValueError(f"out must be {shape}")
+    _check(lib().engram_mx4_pack_weight(qp, on.ptr(scale, "scale", u8), N, K, on.ptr(out, "out", u8), on.handle))
+    return out
+
+
+def _operands(on, a, a_scale, w):
+    """(a address, scale address, bits, weight address, T, K, rows of the weight's records)."""
+    u8 = _t.torch.uint8
+    if a.dtype == _t.torch.float8_e4m3fn:
+        a = a.view(u8)
+    ap, wp = on.ptr(a, "a", u8, 2), on.ptr(w, "w", u8, 3)
+    if w.shape[2] != RECORD_BYTES:
+        raise ValueError("w must be packed weights (engram_mx4_pack_weight)")
+    T, K = a.shape[0], 128 * w.shape[1]
+    if a.shape[1] not in (K, K // 2):
+        raise ValueError(f"a must be [T, K={K}] (MX fp8) or [T, K/2] (MX fp4), got {tuple(a.shape)}")
+    if a_scale.numel() != engram_mx_scale_bytes(T, K):
+        raise ValueError("a_scale must be the MX scale array of a")
+    return ap, on.ptr(a_scale, "a_scale", u8), 8 if a.shape[1] == K else 4, wp, T, K, 64 * w.shape[0]
+
+
+def engram_wkv_mx4(a, a_scale, w, nout=None, out=None, stream=None):
+    """kv bf16 [T, nout] of rows a -- MX fp8 (uint8 or float8_e4m3fn [T, K]: engram_mx_quant's, engram_gather_mx's) or MX fp4
+    (uint8 [T, K/2]: engram_mx4_quant's) with their scales -- on packed MX fp4 weights w.  nout: out's columns, or by default
+    all of the weight's rows, counted in whole records of 64."""
+    on = _t._On(stream, a, "a")
+    ap, sp, bits, wp, T, K, rows = _operands(on, a, a_scale, w)
+    if nout is None:
+        nout = rows if out is None else out.shape[-1]
+    if not rows - 64 < nout <= rows:
+        raise ValueError(f"nout={nout} is not the row count of weights of {rows // 64} records")
+    if out is None:
+        out = on.empty((T, nout), _t.torch.bfloat16)
+    elif tuple(out.shape) != (T, nout):
+        raise ValueError("out must be [T, nout]")
+    _check(lib().engram_wkv_mx4(ap, sp, bits, wp, on.ptr(out, "out", _t.torch.bfloat16, 2), T, K, nout, on.handle))
+    return out
+
+
+def engram_wkv_mx4_gate(a, a_scale, w, x, q_weight, k_weight, eps, value=None, dot=None, workspace=None, stream=None):
+    """(value bf16 [T, dim], dot float32 [T, hc]) from rows a with their scales and packed MX fp4 weights w of (hc+1)*dim
+    rows (as engram_wkv_mx4 takes them) and the stream x bf16 [T, hc, dim] (or [B, L, hc, dim]); `value`, `dot` and
+    `workspace` as engram_wkv_gate."""
+    on = _t._On(stream, a, "a")
+    torch = _t.torch
+    bf, f32 = torch.bfloat16, torch.float32
+    ap, sp, bits, wp, T, K, rows = _operands(on, a, a_scale, w)
+    hc, dim = x.shape[-2:]
+    if x.dim() < 3 or x.numel() != T * hc * dim:
+        raise ValueError("x must be [T, hc, dim] (or [B, L, hc, dim]) with a's T")
+    if rows != (hc + 1) * dim:
+        raise ValueError("w must have (hc+1)*dim rows")
+    if q_weight.shape != (hc, dim) or k_weight.shape != (hc, dim):
+        raise ValueError("q_weight and k_weight must be [hc, dim]")
+    if value is None:
+        value = on.empty((T, dim), bf)
+    if value.dim() != 2 or value.shape[0] != T or value.shape[1] < dim or value.stride(1) != 1:
+        raise ValueError("value must be [T, >= dim] with unit column stride")
+    if value.dtype != bf or value.get_device() != on.index:
+        raise TypeError("value must be a bf16 tensor of the call's GPU")
+    if dot is None:
+        dot = on.empty((T, hc), f32)
+    elif dot.shape != (T, hc):
+        raise ValueError("dot must be [T, hc]")
+    _ws, sw, sn = on.workspace(workspace, engram_wkv_gate_workspace_bytes(T, hc, dim))
+    _check(lib().engram_wkv_mx4_gate(ap, sp, bits, wp, on.ptr(x, "x", bf), on.ptr(q_weight, "q_weight", bf),
+                                     on.ptr(k_weight, "k_weight", bf), float(eps), value.data_ptr(), value.stride(0),
+                                     on.ptr(dot, "dot", f32), sw, sn, T, K, hc, dim, on.handle))
+    return value, dot
+
+
+def engram_ckpt_save(x, q=None, scale=None, stream=None):
+    """(q int8 of x's shape, scale uint8 [..., ceil(D/32)]): the rows of bf16 x [..., D] in OCP MX int8."""
+    on = _t._On(stream, x, "x")
+    torch = _t.torch
+    xp = on.ptr(x, "x", torch.bfloat16)
+    if x.dim() < 1:
+        raise ValueError("x must have a dimension")
+    D = x.shape[-1]
+    rows, shape = _rows(x.shape), (*x.shape[:-1], (D + 31) // 32)
+    if q is None:
+        q = on.empty(x.shape, torch.int8)
+    elif q.shape != x.shape:
+        raise ValueError("q must have x's shape")
+    if scale is None:
+        scale = on.empty(shape, torch.uint8)
+    elif scale.shape != shape:
+        raise ValueError(f"scale must be {tuple(shape)}")
+    _check(lib().engram_ckpt_save(xp, rows, D, on.ptr(q, "q", torch.int8), on.ptr(scale, "scale", torch.uint8), on.handle))
+    return q, scale
+
+
+def engram_ckpt_load(q, scale, out=None, stream=None):
+    """bf16 rows of q's shape: exactly what the checkpoint (engram_ckpt_save's q and scale) stands for."""
+    on = _t._On(stream, q, "q")
+    torch = _t.torch
+    qp = on.ptr(q, "q", torch.int8)
+    if q.dim() < 1 or scale.shape != (*q.shape[:-1], (q.shape[-1] + 31) // 32):
+        raise ValueError("scale must hold a byte per 32 columns of each row of q")
+    if out is None:
+        out = on.empty(q.shape, torch.bfloat16)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _check(lib().engram_ckpt_load(qp, on.ptr(scale, "scale", torch.uint8), _rows(q.shape), q.shape[-1],
+                                  on.ptr(out, "out", torch.bfloat16), on.handle))
+    return out
+
+
+def _rows(shape) -> int:
+    n = 1
+    for d in shape[:-1]:
+        n *= d
+    return n
+
+
+def _mask(on, token_mask, T):
+    if token_mask is None:
+        return None
+    if token_mask.numel() != T:
+        raise ValueError("token_mask must hold one entry per token")
+    if token_mask.dtype == _t.torch.bool:
+        token_mask = token_mask.view(_t.torch.uint8)
+    return on.ptr(token_mask, "token_mask", _t.torch.uint8)
+
+
+def _ckpt_shapes(T, hc, dim):
+    nb = (dim + 31) // 32
+    return (T, hc, dim), (T, hc, nb), (T, hc + 1, dim), (T, hc + 1, nb)
+
+
+def engram_gate_output_ckpt(x, kv, q_weight, k_weight, eps, token_mask=None, out=None, dot=None, checkpoint=None,
+                            stream=None):
+    """(out, dot, GateCheckpoint): engram_gate_output of x bf16 [T, hc, dim] (or [B, L, hc, dim]) and kv [T, >= (hc+1)*dim],
+    with x, the keys and the value kept in 8 bits (engram_ckpt_save's, of their rows of dim) for
+    engram_gate_output_backward_ckpt.  out (x's shape), dot (float32 [T, hc]) and `checkpoint` are allocated if not given."""
+    on = _t._On(stream, x, "x")
+    torch = _t.torch
+    bf, f32 = torch.bfloat16, torch.float32
+    if x.dim() < 3:
+        raise ValueError("x must be [T, hc, dim] (or [B, L, hc, dim])")
+    hc, dim = x.shape[-2:]
+    T = x.numel() // (hc * dim) if hc * dim else 0
+    if kv.dim() != 2 or kv.shape[0] != T or kv.shape[1] < (hc + 1) * dim:
+        raise ValueError("kv must be [T, >= (hc+1)*dim]")
+    if q_weight.shape != (hc, dim) or k_weight.shape != (hc, dim):
+        raise ValueError("q_weight and k_weight must be [hc, dim]")
+    mp = _mask(on, token_mask, T)
+    if out is None:
+        out = on.empty(x.shape, bf)
+    elif out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    if dot is None:
+        dot = on.empty((T, hc), f32)
+    elif dot.shape != (T, hc):
+        raise ValueError("dot must be [T, hc]")
+    shapes = _ckpt_shapes(T, hc, dim)
+    if checkpoint is None:
+        checkpoint = GateCheckpoint(*(on.empty(s, torch.uint8 if i % 2 else torch.int8) for i, s in enumerate(shapes)))
+    c = _checkpoint(on, checkpoint, shapes)
+    _check(lib().engram_gate_output_ckpt(
+        on.ptr(x, "x", bf), on.ptr(kv, "kv", bf, 2), kv.shape[1], on.ptr(q_weight, "q_weight", bf),
+        on.ptr(k_weight, "k_weight", bf), float(eps), mp, on.ptr(out, "out", bf), on.ptr(dot, "dot", f32), *c, T, hc, dim,
+        on.handle))
+    return out, dot, checkpoint
+
+
+def _checkpoint(on, checkpoint, shapes):
+    """The addresses of a checkpoint's four tensors."""
+    names = GateCheckpoint._fields
+    for t, s, name in zip(checkpoint, shapes, names):
+        if tuple(t.shape) != s:
+            raise ValueError(f"checkpoint.{name} must be {s}, got {tuple(t.shape)}")
+    return [on.ptr(t, f"checkpoint.{name}", _t.torch.uint8 if i % 2 else _t.torch.int8)
+            for i, (t, name) in enumerate(zip(checkpoint, names))]
+
+
+def engram_gate_output_backward_ckpt(checkpoint, q_weight, k_weight, eps, dot, dout, token_mask=None, dx=None, dkv=None,
+                                     dq=None, dk=None, workspace=None, stream=None):
+    """(dx bf16 of dout's shape, dkv bf16 [T, (hc+1)*dim], dq, dk float32 [hc, dim]) from dout bf16 [T, hc, dim] (or [B, L,
+    hc, dim]) and what engram_gate_output_ckpt kept: engram_gate_output_backward of the x and kv that engram_ckpt_load gives,
+    bit for bit.  `dx` may be dout itself."""
+    on = _t._On(stream, dout, "dout")
+    bf, f32 = _t.torch.bfloat16, _t.torch.float32
+    if dout.dim() < 3:
+        raise ValueError("dout must be [T, hc, dim] (or [B, L, hc, dim])")
+    hc, dim = dout.shape[-2:]
+    T = dout.numel() // (hc * dim) if hc * dim else 0
+    c = _checkpoint(on, checkpoint, _ckpt_shapes(T, hc, dim))
+    if q_weight.shape != (hc, dim) or k_weight.shape != (hc, dim):
+        raise ValueError("q_weight and k_weight must be [hc, dim]")
+    if dot.shape != (T, hc):
+        raise ValueError("dot must be [T, hc]")
+    mp = _mask(on, token_mask, T)
+    if dx is None:
+        dx = on.empty(dout.shape, bf)
+    elif dx.shape != dout.shape:
+        raise ValueError("dx must have dout's shape")
+    if dkv is None:
+        dkv = on.empty((T, (hc + 1) * dim), bf)
+    elif dkv.shape != (T, (hc + 1) * dim):
+        raise ValueError("dkv must be [T, (hc+1)*dim]")
+    if dq is None:
+        dq = on.empty((hc, dim), f32)
+    if dk is None:
+        dk = on.empty((hc, dim), f32)
+    if dq.shape != (hc, dim) or dk.shape != (hc, dim):
+        raise ValueError("dq and dk must be [hc, dim]")
+    _ws, wp, wn = on.workspace(workspace, _t.engram_gate_output_backward_workspace_bytes(T, hc, dim))
+    _check(lib().engram_gate_output_backward_ckpt(
+        *c, on.ptr(q_weight, "q_weight", bf), on.ptr(k_weight, "k_weight", bf), float(eps), on.ptr(dot, "dot", f32),
+        on.ptr(dout, "dout", bf), mp, on.ptr(dx, "dx", bf), on.ptr(dkv, "dkv", bf), on.ptr(dq, "dq", f32),
+        on.ptr(dk, "dk", f32), wp, wn, T, hc, dim, on.handle))
+    return dx, dkv, dq, dk
+
+
+__all__ = ["GateCheckpoint", "engram_mx4_quant", "engram_mx4_weight_bytes", "engram_mx4_pack_weight", "engram_wkv_mx4",
+           "engram_wkv_mx4_gate", "engram_ckpt_save", "engram_ckpt_load", "engram_gate_output_ckpt",
+           "engram_gate_output_backward_ckpt"]

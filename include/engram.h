@@ -41,6 +41,13 @@
  *   engram_wkv_mx          -- the projection on MX fp8 operands
  *   engram_wkv_mx_gate     -- engram_wkv_mx fused with the gate pre-activation
  *
+ * its form with 4-bit weights (OCP MX fp4):
+ *
+ *   engram_mx4_quant       -- bf16 rows to MX fp4 (E2M1 + an E8M0 scale per 32 columns)
+ *   engram_mx4_pack_weight -- MX fp4 weights to the layout the products read (one-off)
+ *   engram_wkv_mx4         -- the projection of MX fp8 or MX fp4 rows on MX fp4 weights
+ *   engram_wkv_mx4_gate    -- engram_wkv_mx4 fused with the gate pre-activation
+ *
  * and the gradients that train the module and its embeddings:
  *
  *   engram_embed           -- rows of a trainable (bf16 or float32) table by id, scaled
@@ -51,6 +58,14 @@
  *   engram_wkv_backward    -- the gradient of engram_wkv
  *   engram_grad_norm, engram_clip_grads
  *                          -- the 2-norm of many gradients together, and clipping by it
+ *
+ * with 8-bit checkpoints (OCP MX int8) of what the backward pass reads again:
+ *
+ *   engram_ckpt_save, engram_ckpt_load
+ *                          -- bf16 rows to MX int8 and back
+ *   engram_gate_output_ckpt -- engram_gate_output keeping its stream, keys and value
+ *   engram_gate_output_backward_ckpt
+ *                          -- engram_gate_output_backward from what was kept
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -518,6 +533,83 @@ int engram_wkv_mx_gate(const uint8_t* a, const uint8_t* a_scale, const uint8_t* 
                        int64_t T, int32_t K, int32_t hc, int32_t dim, void* stream);
 
 /*
+ * The wkv Linear with 4-bit weights, in the OCP MX fp4 format: E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives; two a byte, the even column in the low half), and for every 32 consecutive columns of a row one E8M0 scale byte s
+ * meaning 2^(s-127), 0xFF NaN.  Rows to be multiplied are in MX fp8 (engram_mx_quant, engram_gather_mx) or MX fp4, with
+ * their scales in the MX scale layout above.
+ *
+ * Weight layout of this library: uint8 [ceil(Nout/64)][K/128][4352], a record for 64 rows and 128 columns: the element of
+ * row 64 g + 16 j + r and column 128 t + 32 c + e is half e % 2 of byte 1024 j + 256 c + 16 r + e / 2 of record [g][t], its
+ * scale byte 4096 + 64 c + 4 r + j; rows past Nout are zeros.
+ */
+
+/*
+ * engram_mx4_quant -- bf16 rows to MX fp4 by the OCP MX rule: for each row and 32-column block with largest magnitude
+ * amax, e = floor(log2 amax) - 2 (2 being E2M1's largest exponent), kept in [-127, 127] (-127 for an all-zero block);
+ * scale = e + 127; q = x * 2^-e rounded to the nearest E2M1 value, ties to the even code, magnitudes past 6 saturated,
+ * the sign kept.  A block that holds an infinity or a NaN takes the scale 0xFF (every product with it is NaN) and zeros.
+ *
+ * x      uint16 [rows, K] bf16 bits; 16-byte aligned
+ * q      uint8 [rows, K/2], out; 4-byte aligned (16-byte where the product reads it)
+ * scale  uint8, engram_mx_scale_bytes(rows, K) bytes in the MX scale layout, out
+ * Limits: K >= 128 and K % 128 == 0; 0 <= rows, rows * K <= 2^34.
+ */
+int engram_mx4_quant(const uint16_t* x, int64_t rows, int32_t K, uint8_t* q, uint8_t* scale, void* stream);
+
+/* Bytes of the weight layout for Nout rows of K columns, or -1 outside engram_wkv_mx4's limits. */
+int64_t engram_mx4_weight_bytes(int32_t Nout, int32_t K);
+
+/*
+ * engram_mx4_pack_weight -- MX fp4 rows into the weight layout (a one-off conversion, at load or after an update).
+ *
+ * q       uint8 [Nout, K/2] (engram_mx4_quant's); 16-byte aligned
+ * scale   their MX scales
+ * packed  uint8, engram_mx4_weight_bytes(Nout, K) bytes, out; 16-byte aligned
+ * Limits: as engram_wkv_mx4; at most 2^23 records.
+ */
+int engram_mx4_pack_weight(const uint8_t* q, const uint8_t* scale, int32_t Nout, int32_t K, uint8_t* packed, void* stream);
+
+/*
+ * engram_wkv_mx4 -- the projection on MX fp4 weights:
+ *   kv[t,o] = bf16( sum over 32-column blocks b of
+ *                   2^(a_scale[t,b]-127) * 2^(w_scale[o,b]-127) * sum_{k in b} a[t,k] * w[o,k] )
+ * with fp32 accumulation in ascending order of 128-column steps, and one bf16 rounding: an output's bits depend on its
+ * row and weights alone, not on the other rows of the call.
+ *
+ * a        uint8 [T, K] E4M3FN bytes (a_bits 8) or [T, K/2] E2M1 pairs (a_bits 4); 16-byte aligned
+ * a_scale  MX scales of a (T rows); 16-byte aligned
+ * w        the packed weights (engram_mx4_pack_weight's); 16-byte aligned
+ * kv       uint16 [T, Nout] bf16 bits, out: the hc keys then the value, as engram_wkv; 16-byte aligned
+ * Limits: T >= 0; K a multiple of 128 in [128, 2^20]; Nout a multiple of 8 in [8, 2^22]; fewer than 2^31 tiles of
+ * 256 x 256 outputs.
+ */
+int engram_wkv_mx4(const uint8_t* a, const uint8_t* a_scale, int32_t a_bits, const uint8_t* w, uint16_t* kv, int64_t T,
+                   int32_t K, int32_t Nout, void* stream);
+
+/*
+ * engram_wkv_mx4_gate -- engram_wkv_mx4 fused with the gate dot, as engram_wkv_mx_gate fuses engram_wkv_mx: the key
+ * columns of the product are rounded to bf16 and reduced against the stream inside the projection, never written; the
+ * value columns are stored.
+ *
+ *   kv       = engram_wkv_mx4(a, w), Nout = (hc+1)*dim
+ *   value    = kv[:, hc*dim : (hc+1)*dim]                       -> value
+ *   dot[t,c] = as engram_gate_dot, with key = kv[t, c*dim : (c+1)*dim]  -> dot
+ * The value columns equal engram_wkv_mx4's bit for bit; the dot equals engram_gate_dot on engram_wkv_mx4's kv up to the
+ * order of its fp32 sums (per 128 columns in the projection, then added in slice order by a second kernel).
+ *
+ * a, a_scale, a_bits, w  as engram_wkv_mx4, w having (hc+1)*dim rows
+ * x, q_weight, k_weight, eps, value, ld_value, dot  as engram_wkv_gate
+ * workspace  at least engram_wkv_gate_workspace_bytes(T, hc, dim) bytes, 16-byte aligned, caller-owned scratch (no
+ *            initialisation needed); two calls in flight at once must not share it
+ * Limits: as engram_wkv_mx4; 1 <= hc <= 64; dim >= 256 and dim % 256 == 0; (hc+1)*dim <= 2^22; ld_value >= dim,
+ * ld_value % 8 == 0.  Too small a workspace -> ENGRAM_ERANGE.
+ */
+int engram_wkv_mx4_gate(const uint8_t* a, const uint8_t* a_scale, int32_t a_bits, const uint8_t* w, const uint16_t* x,
+                        const uint16_t* q_weight, const uint16_t* k_weight, float eps, uint16_t* value, int64_t ld_value,
+                        float* dot, void* workspace, int64_t workspace_bytes, int64_t T, int32_t K, int32_t hc, int32_t dim,
+                        void* stream);
+
+/*
  * engram_wkv_gate_layers_noalloc -- engram_wkv_gate_layers without a workspace
  * argument, for callers that cannot allocate device memory: code recorded
  * under HIP graph capture, tight serving loops, harnesses that forbid
@@ -645,7 +737,7 @@ int engram_gate_output_backward(const uint16_t* x, const uint16_t* kv, int64_t l
                                 void* workspace, int64_t workspace_bytes, int64_t T, int32_t hc, int32_t dim,
                                 void* stream);
 
-/* Bytes of workspace engram_gate_output_backward needs, or -1 outside its limits. */
+/* Bytes of workspace engram_gate_output_backward and engram_gate_output_backward_ckpt need, or -1 outside their limits. */
 int64_t engram_gate_output_backward_workspace_bytes(int64_t T, int32_t hc, int32_t dim);
 
 /*
@@ -703,6 +795,58 @@ int64_t engram_grad_norm_workspace_bytes(int32_t tensors, const int64_t* n, cons
  */
 int engram_clip_grads(int32_t tensors, const void* const* grads, void* const* out, const int64_t* n,
                       const int32_t* dtype, const float* norm, float max_norm, void* stream);
+
+/*
+ * Checkpoints: rows that a backward pass reads again, kept in 8 bits in the OCP MX int8 format.  32 consecutive columns of
+ * a row (the last block may be shorter) share one E8M0 scale byte s; an element is an integer in [-127, 127] worth
+ * 2^(s-127) / 64.  A row's scales lie together: uint8 [rows, ceil(D/32)].
+ *
+ * engram_ckpt_save -- bf16 rows to checkpoints: s - 127 = floor(log2 amax) of the block, at least -127 (s = 0 for an all-zero
+ * or subnormal block); the integer nearest to 64 x 2^(127-s), ties to even, kept in [-127, 127]: no element is off by more
+ * than half a unit, 2^-7 of the block's amax at most (amax reaches 127.5 units, not 128).  A block that holds an infinity or a NaN takes the scale
+ * 0xFF and zeros, and is read back as NaN.
+ * engram_ckpt_load -- checkpoints to bf16 rows, exactly the values they stand for.
+ *
+ * x      uint16 [rows, D] bf16 bits; 16-byte aligned
+ * q      int8 [rows, D]; 8-byte aligned
+ * scale  uint8 [rows, ceil(D/32)]
+ * Limits: D a multiple of 8 in [8, 2^20]; 0 <= rows, rows * (D up to a multiple of 32) <= 2^34.
+ */
+int engram_ckpt_save(const uint16_t* x, int64_t rows, int32_t D, int8_t* q, uint8_t* scale, void* stream);
+int engram_ckpt_load(const int8_t* q, const uint8_t* scale, int64_t rows, int32_t D, uint16_t* x, void* stream);
+
+/*
+ * engram_gate_output_ckpt -- engram_gate_output that also keeps what its gradient reads, in 8 bits: out as
+ * engram_gate_output's formula from the dot it writes (up to the order of the dot's fp32 sums), computed from x and kv
+ * themselves, and
+ *   x_q, x_scale    = engram_ckpt_save of x's T * hc rows of dim
+ *   kv_q, kv_scale  = engram_ckpt_save of kv's T * (hc+1) rows of dim (the keys, then the value)
+ * bit for bit.
+ *
+ * x, kv, ld_kv, q_weight, k_weight, eps, token_mask, out  as engram_gate_output
+ * dot       float32 [T, hc], out (kept for the gradient); 4-byte aligned
+ * x_q       int8 [T, hc, dim], out; 8-byte aligned;     x_scale   uint8 [T, hc, ceil(dim/32)], out
+ * kv_q      int8 [T, hc+1, dim], out; 8-byte aligned;   kv_scale  uint8 [T, hc+1, ceil(dim/32)], out
+ * Limits: T * hc <= 2^23; 1 <= hc <= 64; 8 <= dim <= 8192 and dim % 8 == 0.
+ */
+int engram_gate_output_ckpt(const uint16_t* x, const uint16_t* kv, int64_t ld_kv, const uint16_t* q_weight,
+                            const uint16_t* k_weight, float eps, const uint8_t* token_mask, uint16_t* out, float* dot,
+                            int8_t* x_q, uint8_t* x_scale, int8_t* kv_q, uint8_t* kv_scale, int64_t T, int32_t hc,
+                            int32_t dim, void* stream);
+
+/*
+ * engram_gate_output_backward_ckpt -- engram_gate_output_backward from checkpoints: its results for the x and kv that
+ * engram_ckpt_load gives, bit for bit.
+ *
+ * x_q, x_scale, kv_q, kv_scale  as engram_gate_output_ckpt wrote them
+ * Other arguments, limits and errors: as engram_gate_output_backward (workspace:
+ * engram_gate_output_backward_workspace_bytes).
+ */
+int engram_gate_output_backward_ckpt(const int8_t* x_q, const uint8_t* x_scale, const int8_t* kv_q, const uint8_t* kv_scale,
+                                     const uint16_t* q_weight, const uint16_t* k_weight, float eps, const float* dot,
+                                     const uint16_t* dout, const uint8_t* token_mask, uint16_t* dx, uint16_t* dkv, float* dq,
+                                     float* dk, void* workspace, int64_t workspace_bytes, int64_t T, int32_t hc, int32_t dim,
+                                     void* stream);
 
 #ifdef __cplusplus
 }

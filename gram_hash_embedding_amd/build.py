@@ -39,6 +39,7 @@ FILE_FLAGS = {
     "wkv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "wkv16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "wkv_grad.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "wkv_mx4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

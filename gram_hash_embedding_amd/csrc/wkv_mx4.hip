@@ -191,6 +191,277 @@ __global__ __launch_bounds__(kGate ? 512 : 256) void mx4_direct_kernel(Mx4Args p
     }
 }
 
+// ---- tiles: a workgroup of four waves has 32 MI tokens x 128 columns, two workgroups a CU, so that one's stores, sums and first
+// loads run under the other's matrix instructions.  Wave (wm, wn) has 16 MI tokens x 64 columns, MI x 4 blocks of 16 x 16.  The
+// token rows come through LDS, steps of 128 columns in kStages stages by direct-to-LDS loads (rows past M are outside their
+// resource and read as zero); the weights go from memory to the registers, a step ahead, and leave LDS its bandwidth: every
+// wave reads MI KB (8-bit rows: 2 MI) of a stage for 4 MI matrix instructions of 16 (32) cycles, where with the weights in LDS
+// it would read half as much again.
+//
+// LDS rows: 64 bytes of a 4-bit row, its 16-byte piece c at slot c ^ (row / 4) % 4; 128 bytes of an 8-bit one, piece c at slot
+// c ^ (row / 2) % 8: eight neighbouring lanes' pieces lie in different banks.
+constexpr int kBufferWord3 = 0x00020000;
+constexpr int kWaitLgkmcnt0 = 0xC07F;
+constexpr int wait_vmcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | 0x0F70; }
+constexpr int kXcds = 8;
+constexpr int kGroupM = 8;  // tile rows that an XCD walks together
+
+// the halves of the four lanes of a token, {16 j + 4 g .. +3 of blocks j = 0, 1} for lane group g, as 8 neighbouring columns a
+// lane: group g has columns 8 g .. 8 g + 7 of the two blocks' 32
+__device__ inline u32x4 swap_groups(u32x2 a, u32x2 b) {
+    u32x4 o;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t x = a[e], y = b[e];
+        const auto s = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+        const uint32_t s0 = s[0], s1 = s[1];
+        const auto t = __builtin_amdgcn_permlane16_swap(s0, s1, false, false);
+        o[e] = t[0];
+        o[2 + e] = t[1];
+    }
+    return o;
+}
+
+__device__ inline i32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+    return i32x4{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+}
+__device__ inline int load4(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    return static_cast<int>(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+}
+
+template <bool kA8, int MI, bool kGate>
+__device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int tiles_n) {
+    constexpr int BM = 32 * MI, BN = 128;
+    constexpr int kRow = kA8 ? 128 : 64;             // bytes of a row and step
+    constexpr int kStageBytes = BM * kRow + BM * 4;  // the rows, then their scales
+    constexpr int kStages = kA8 ? 2 : 3;
+    constexpr int kRowLoads = BM * kRow / 4096;      // per wave and step
+    constexpr int kLoads = kRowLoads + 1;            // and their scales
+    constexpr int kWLoads = 5;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * kStageBytes];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave & 1, wn = wave >> 1;
+    const int g = lane >> 4, r = lane & 15;
+    const int S = p.steps;
+    // the workgroup's tile: an XCD (workgroups blockIdx % 8) takes a contiguous run of the order, kGroupM tile rows deep
+    int64_t m0;
+    int n0;
+    {
+        const int64_t n = static_cast<int64_t>(tiles_m) * tiles_n;
+        const int64_t pid = blockIdx.x, xcd = pid % kXcds, per = n / kXcds, rem = n % kXcds;
+        const int64_t at = xcd * per + min(xcd, rem) + pid / kXcds;
+        const int64_t in_group = static_cast<int64_t>(kGroupM) * tiles_n;
+        const int64_t group = at / in_group;
+        const int first = static_cast<int>(group) * kGroupM;
+        const int deep = min(tiles_m - first, kGroupM);
+        const int left = static_cast<int>(at - group * in_group);
+        m0 = static_cast<int64_t>(first + left % deep) * BM;
+        n0 = left / deep * BN;
+    }
+    const int row_bytes = S * kRow;
+    const int valid = static_cast<int>(min<int64_t>(BM, p.M - m0));
+    // row loads: instruction q of the wave fills 1 KB, rows (kRowLoads wave + q) 1024 / kRow on, lane l a 16-byte slot
+    constexpr int kRowsPerLoad = 1024 / kRow;
+    const int lrow = lane / (kRow / 16), lslot = lane % (kRow / 16);
+    uint32_t voff[kA8 ? 2 : 1];  // (8-bit rows: the key of an odd instruction's rows is that of an even one's, plus 4)
+#pragma unroll
+    for (int o = 0; o < (kA8 ? 2 : 1); ++o) {
+        const int key = kA8 ? (((lrow >> 1) + 4 * o) & 7) : ((lrow >> 2) & 3);
+        voff[o] = static_cast<uint32_t>((wave * kRowLoads * kRowsPerLoad + lrow) * row_bytes + ((lslot ^ key) << 4));
+    }
+    const uint32_t soff = static_cast<uint32_t>(((wave * 64) % BM + lane) * 4);
+    const uint8_t* as0 = p.as + m0 * 4;
+    const int scale_bytes = static_cast<int>(min<int64_t>(BM, p.M4 - m0)) * 4;
+    auto issue = [&](int s) {  // step s's rows and scales; past the last step nothing is fetched (zeros are written)
+        uint8_t* st = lds + (s % kStages) * kStageBytes;
+        const bool on = s < S;
+        const __amdgpu_buffer_rsrc_t ra =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.a + m0 * row_bytes), 0, on ? valid * row_bytes : 0, kBufferWord3);
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(as0 + static_cast<int64_t>(s) * p.M4 * 4), 0, on ? scale_bytes : 0, kBufferWord3);
+#pragma unroll
+        for (int q = 0; q < kRowLoads; ++q)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, st + (wave * kRowLoads + q) * 1024, 16,
+                                                     voff[kA8 ? q & 1 : 0] + static_cast<uint32_t>(q * kRowsPerLoad * row_bytes),
+                                                     s * kRow, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, st + BM * kRow + (wave * 64) % BM * 4, 4, soff, 0, 0, 0);
+    };
+    const int group = min(n0 / kGroupRows + wn, (p.N + kGroupRows - 1) / kGroupRows - 1);  // (columns past N are not stored)
+    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(p.w + static_cast<int64_t>(group) * S * kRecord), 0, S * kRecord, kBufferWord3);
+    struct WRegs {
+        i32x4 f[4];
+        int s;
+    };
+    uint32_t woff = 16 * lane, wsoff = 4096 + 4 * lane;
+    auto load_w = [&](WRegs& d) {  // the next record (past the last: nothing is fetched)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            d.f[j] = load16(rw, woff + 1024 * j);
+        d.s = load4(rw, wsoff);
+        woff += kRecord;
+        wsoff += kRecord;
+    };
+    AFrag<kA8> fa[MI];
+    int sa[MI];
+    const uint32_t foff = static_cast<uint32_t>((wm * 16 * MI + r) * kRow);
+    const uint32_t fkey = kA8 ? (r >> 1) & 7 : (r >> 2) & 3;
+    const uint32_t fo0 = foff + ((g ^ fkey) << 4), fo1 = foff + (((4 + g) ^ fkey) << 4);
+    const uint32_t sco = static_cast<uint32_t>(BM * kRow + (wm * 16 * MI + r) * 4 + g);
+    auto read_a = [&](int stage, int i) {
+        const uint8_t* st = lds + stage * kStageBytes;
+        fa[i].lo = *reinterpret_cast<const i32x4*>(st + fo0 + i * 16 * kRow);
+        if constexpr (kA8) fa[i].hi = *reinterpret_cast<const i32x4*>(st + fo1 + i * 16 * kRow);
+        sa[i] = st[sco + 64 * i];
+    };
+    auto fence = [&]() {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto barrier = [&]() {  // this wave's LDS reads are done; then all waves'
+        __builtin_amdgcn_s_waitcnt(kWaitLgkmcnt0);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        fence();
+    };
+    f32x4 acc[MI][4];
+    // One step: the operands of step s are in registers.  The next weights are asked for; one block row into the step the next
+    // stage is waited for (the loads issued after its own are left in flight) and published, the stage read out is refilled,
+    // and each token operand is replaced by the next step's behind its last use.  The last step does so too: zeros.
+    WRegs cur, nxt;
+    auto step = [&](auto first_tag, int s) {
+        constexpr bool kFirst = decltype(first_tag)::value;
+        load_w(nxt);
+        fence();
+        const int nst = (s + 1) % kStages;
+        const f32x4 z = {};
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            acc[i][0] = mfma<kA8, 0>(cur.f[0], cur.s, fa[i], sa[i], kFirst ? z : acc[i][0]);
+            acc[i][1] = mfma<kA8, 1>(cur.f[1], cur.s, fa[i], sa[i], kFirst ? z : acc[i][1]);
+            acc[i][2] = mfma<kA8, 2>(cur.f[2], cur.s, fa[i], sa[i], kFirst ? z : acc[i][2]);
+            acc[i][3] = mfma<kA8, 3>(cur.f[3], cur.s, fa[i], sa[i], kFirst ? z : acc[i][3]);
+            if (i == 0) {
+                fence();
+                __builtin_amdgcn_s_waitcnt(wait_vmcnt(kStages == 2 ? kWLoads : 2 * kWLoads + kLoads));
+                barrier();
+                issue(s + kStages);
+            }
+            read_a(nst, i);
+            fence();
+        }
+        cur = nxt;
+    };
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) issue(s);
+    fence();
+    load_w(cur);
+    fence();
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(kWLoads + (kStages - 1) * kLoads));
+    barrier();
+#pragma unroll
+    for (int i = 0; i < MI; ++i) read_a(0, i);
+    fence();
+    step(std::true_type{}, 0);
+    for (int s = 1; s < S; ++s) step(std::false_type{}, s);
+    // lane group g has, of token 16 i + r and block pair h, the eight columns 32 h + 8 g .. +7
+    const int nw = n0 + 64 * wn;
+    auto columns = [&](int i, int h) {
+        const f32x4 &u = acc[i][2 * h], &v = acc[i][2 * h + 1];
+        return swap_groups(u32x2{pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3])},
+                           u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])});
+    };
+    const int64_t mw = m0 + 16 * MI * wm + r;
+    if (!kGate || n0 >= p.n_key) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int64_t m = mw + 16 * i;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 v = columns(i, h);
+                const int n = nw + 32 * h + 8 * g;
+                if (m < p.M && n < p.N)
+                    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p.kv + m * p.ld_out + (n - p.n_key)));
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));  // (loads past the last step still write LDS: let them land)
+        return;
+    }
+    if constexpr (kGate) {
+        // the lane's 16 columns of q * k (exact in fp32), and the stream rows a block row ahead
+        float wq[2][8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int n = nw + 32 * h + 8 * g;
+            const u32x4 q = *reinterpret_cast<const u32x4*>(p.q + n), k = *reinterpret_cast<const u32x4*>(p.k + n);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                wq[h][2 * e] = lo_bf16(q[e]) * lo_bf16(k[e]);
+                wq[h][2 * e + 1] = hi_bf16(q[e]) * hi_bf16(k[e]);
+            }
+        }
+        auto load_x = [&](u32x4 (&d)[2], int i) {
+            const int64_t m = min(mw + 16 * i, p.M - 1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                d[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.x + m * p.n_key + nw + 32 * h + 8 * g));
+        };
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
+        barrier();  // the stages are free, and nothing in flight writes them
+        float* sums = reinterpret_cast<float*>(lds);  // [wm][3][16 MI]: the right half's
+        float res[MI][3];
+        u32x4 xr[2][2];
+        load_x(xr[0], 0);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            if (i + 1 < MI) load_x(xr[(i + 1) & 1], i + 1);
+            float hwk = 0.f, kk = 0.f, hh = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 key = columns(i, h), x = xr[i & 1][h];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float k0 = lo_bf16(key[e]), k1 = hi_bf16(key[e]), h0 = lo_bf16(x[e]), h1 = hi_bf16(x[e]);
+                    hwk += h0 * wq[h][2 * e] * k0 + h1 * wq[h][2 * e + 1] * k1;
+                    kk += k0 * k0 + k1 * k1;
+                    hh += h0 * h0 + h1 * h1;
+                }
+            }
+            hwk += __shfl_xor(hwk, 16, 64);
+            kk += __shfl_xor(kk, 16, 64);
+            hh += __shfl_xor(hh, 16, 64);
+            res[i][0] = hwk + __shfl_xor(hwk, 32, 64);
+            res[i][1] = kk + __shfl_xor(kk, 32, 64);
+            res[i][2] = hh + __shfl_xor(hh, 32, 64);
+        }
+        if (wn == 1 && g == 0) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int e = 0; e < 3; ++e) sums[(wm * 3 + e) * 16 * MI + 16 * i + r] = res[i][e];
+        }
+        __syncthreads();
+        if (wn == 0 && g == 0) {  // the two halves' 64 columns, left first
+            float* out = p.part + static_cast<int64_t>(n0 / BN) * 3 * p.M;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const int64_t m = mw + 16 * i;
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (m < p.M) out[e * p.M + m] = res[i][e] + sums[(wm * 3 + e) * 16 * MI + 16 * i + r];
+            }
+        }
+    }
+}
+
+template <bool kA8, int MI, bool kGate>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void mx4_tile_kernel(Mx4Args p, int tiles_m,
+                                                                                                 int tiles_n) {
+    mx4_tile_body<kA8, MI, kGate>(p, tiles_m, tiles_n);
+}
+
 // ---- quantisation of bf16 rows: a thread has 8 consecutive columns, the 4 threads of a block find its largest magnitude (as
 // bit patterns, whose order is the magnitudes').  floor(log2 amax) is the pattern's exponent field less the bias; E2M1's
 // largest exponent is 2, so the shared scale's code is the field less 2, or 0 where that is below E8M0's range (fields 0, of
@@ -252,6 +523,25 @@ int launch_direct(const Mx4Args& p, hipStream_t stream, const char* what) {
     else if (mi == 2) hipLaunchKernelGGL((mx4_direct_kernel<kA8, 2, kGate>), grid, block, 0, stream, p, groups_n);
     else hipLaunchKernelGGL((mx4_direct_kernel<kA8, 4, kGate>), grid, block, 0, stream, p, groups_n);
     return check_launch(what);
+}
+
+template <bool kA8, bool kGate>
+int launch_tiles(const Mx4Args& p, hipStream_t stream, const char* what) {
+    const int mi = p.M <= 512 ? 4 : 8;
+    const int64_t tiles_m = (p.M + 32 * mi - 1) / (32 * mi);
+    const int tiles_n = (p.N + 127) / 128;
+    if (tiles_m > kMostGroups / tiles_n) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
+    const dim3 grid(static_cast<unsigned>(tiles_m * tiles_n)), block(256);
+    const int tm = static_cast<int>(tiles_m);
+    if (mi == 4) hipLaunchKernelGGL((mx4_tile_kernel<kA8, 4, kGate>), grid, block, 0, stream, p, tm, tiles_n);
+    else hipLaunchKernelGGL((mx4_tile_kernel<kA8, 8, kGate>), grid, block, 0, stream, p, tm, tiles_n);
+    return check_launch(what);
+}
+
+template <bool kA8, bool kGate>
+int launch(const Mx4Args& p, hipStream_t stream, const char* what) {
+    if (p.M <= 64) return launch_direct<kA8, kGate>(p, stream, what);
+    return launch_tiles<kA8, kGate>(p, stream, what);
 }
 
 constexpr int kMaxK = 1 << 20, kMaxN = 1 << 22;
@@ -321,8 +611,7 @@ extern "C" int engram_wkv_mx4(const uint8_t* a, const uint8_t* a_scale, int32_t 
     p.ld_out = Nout;
     p.N = Nout;
     p.steps = K / kStepCols;
-    return a_bits == 8 ? launch_direct<true, false>(p, as_stream(stream), what)
-                       : launch_direct<false, false>(p, as_stream(stream), what);
+    return a_bits == 8 ? launch<true, false>(p, as_stream(stream), what) : launch<false, false>(p, as_stream(stream), what);
 }
 
 extern "C" int engram_wkv_mx4_gate(const uint8_t* a, const uint8_t* a_scale, int32_t a_bits, const uint8_t* w,
@@ -365,8 +654,7 @@ extern "C" int engram_wkv_mx4_gate(const uint8_t* a, const uint8_t* a_scale, int
     p.part = static_cast<float*>(workspace);
     p.dim = dim;
     p.n_key = hc * dim;
-    const int rc = a_bits == 8 ? launch_direct<true, true>(p, as_stream(stream), what)
-                               : launch_direct<false, true>(p, as_stream(stream), what);
+    const int rc = a_bits == 8 ? launch<true, true>(p, as_stream(stream), what) : launch<false, true>(p, as_stream(stream), what);
     if (rc != ENGRAM_OK) return rc;
     float* dots[1] = {dot};
     return launch_gate_finalize(static_cast<const float*>(workspace), 0, dots, 1, T, hc, dim, eps, as_stream(stream), what);

@@ -191,15 +191,14 @@ __global__ __launch_bounds__(kGate ? 512 : 256) void mx4_direct_kernel(Mx4Args p
     }
 }
 
-// ---- tiles: a workgroup of four waves has 32 MI tokens x 128 columns, two workgroups a CU, so that one's stores, sums and first
-// loads run under the other's matrix instructions.  Wave (wm, wn) has 16 MI tokens x 64 columns, MI x 4 blocks of 16 x 16.  The
-// token rows come through LDS, steps of 128 columns in kStages stages by direct-to-LDS loads (rows past M are outside their
-// resource and read as zero); the weights go from memory to the registers, a step ahead, and leave LDS its bandwidth: every
-// wave reads MI KB (8-bit rows: 2 MI) of a stage for 4 MI matrix instructions of 16 (32) cycles, where with the weights in LDS
-// it would read half as much again.
+// ---- tiles: a workgroup of four waves has 16 MI tokens x 256 columns, two workgroups a CU, so that one's stores, sums and first
+// loads run under the other's matrix instructions.  A wave has all tokens and 64 columns, MI x 4 blocks of 16 x 16.  The token
+// rows come through LDS, 128 bytes of each (128 columns in 8 bits, 256 in 4) a stage, in two stages, by direct-to-LDS loads (rows
+// past M are outside their resource and read as zero); the weights go from memory to the registers, a step ahead, each read by
+// one wave only.  What bounds it is the path of the loads through the CU's address unit (busy 84 % of the clocks where two waves
+// of a 256 x 128 tile read the same weights, at 64 bytes of a row a load), so as few and as long runs as the registers allow.
 //
-// LDS rows: 64 bytes of a 4-bit row, its 16-byte piece c at slot c ^ (row / 4) % 4; 128 bytes of an 8-bit one, piece c at slot
-// c ^ (row / 2) % 8: eight neighbouring lanes' pieces lie in different banks.
+// LDS rows: the 16-byte piece c of a row at slot c ^ (row / 2) % 8: neighbouring lanes' pieces lie in different banks.
 constexpr int kBufferWord3 = 0x00020000;
 constexpr int kWaitLgkmcnt0 = 0xC07F;
 constexpr int wait_vmcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | 0x0F70; }
@@ -232,17 +231,17 @@ __device__ inline int load4(__amdgpu_buffer_rsrc_t r, uint32_t at) {
 
 template <bool kA8, int MI, bool kGate>
 __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int tiles_n) {
-    constexpr int BM = 32 * MI, BN = 128;
-    constexpr int kRow = kA8 ? 128 : 64;             // bytes of a row and step
-    constexpr int kStageBytes = BM * kRow + BM * 4;  // the rows, then their scales
-    constexpr int kStages = kA8 ? 2 : 3;
-    constexpr int kRowLoads = BM * kRow / 4096;      // per wave and step
-    constexpr int kLoads = kRowLoads + 1;            // and their scales
+    constexpr int BM = 16 * MI, BN = 256;
+    constexpr int kSub = kA8 ? 1 : 2;                       // steps of a stage
+    constexpr int kScales = BM * 128;                       // a stage: its rows, then a word per row and step
+    constexpr int kStageBytes = kScales + kSub * BM * 4;
+    constexpr int kRowLoads = (BM + 31) / 32;               // per wave and stage: 8 rows each
+    constexpr int kScaleLoads = (kSub * BM + 255) / 256;    // 64 rows of a step each
+    constexpr int kLoads = kRowLoads + kScaleLoads;
     constexpr int kWLoads = 5;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * kStageBytes];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStageBytes];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave & 1, wn = wave >> 1;
     const int g = lane >> 4, r = lane & 15;
     const int S = p.steps;
     // the workgroup's tile: an XCD (workgroups blockIdx % 8) takes a contiguous run of the order, kGroupM tile rows deep
@@ -260,61 +259,49 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         m0 = static_cast<int64_t>(first + left % deep) * BM;
         n0 = left / deep * BN;
     }
-    const int row_bytes = S * kRow;
-    const int valid = static_cast<int>(min<int64_t>(BM, p.M - m0));
-    // row loads: instruction q of the wave fills 1 KB, rows (kRowLoads wave + q) 1024 / kRow on, lane l a 16-byte slot
-    constexpr int kRowsPerLoad = 1024 / kRow;
-    const int lrow = lane / (kRow / 16), lslot = lane % (kRow / 16);
-    uint32_t voff[kA8 ? 2 : 1];  // (8-bit rows: the key of an odd instruction's rows is that of an even one's, plus 4)
-#pragma unroll
-    for (int o = 0; o < (kA8 ? 2 : 1); ++o) {
-        const int key = kA8 ? (((lrow >> 1) + 4 * o) & 7) : ((lrow >> 2) & 3);
-        voff[o] = static_cast<uint32_t>((wave * kRowLoads * kRowsPerLoad + lrow) * row_bytes + ((lslot ^ key) << 4));
-    }
-    const uint32_t soff = static_cast<uint32_t>(((wave * 64) % BM + lane) * 4);
-    const uint8_t* as0 = p.as + m0 * 4;
+    const int row_bytes = S * (kA8 ? 128 : 64);
+    const int valid_bytes = static_cast<int>(min<int64_t>(BM, p.M - m0)) * row_bytes;
+    // row loads: load q of the wave fills 1 KB, rows 8 (kRowLoads wave + q) on, lane l slot l % 8 of row l / 8; the key of an odd
+    // group of 8 rows is that of an even one plus 4
+    const int at_row = wave * kRowLoads * 8 + (lane >> 3);
+    const uint32_t piece = static_cast<uint32_t>(((lane & 7) ^ ((at_row >> 1) & 7)) << 4);
+    const uint32_t voff[2] = {at_row * row_bytes + piece, at_row * row_bytes + (piece ^ 64u)};
     const int scale_bytes = static_cast<int>(min<int64_t>(BM, p.M4 - m0)) * 4;
-    auto issue = [&](int s) {  // step s's rows and scales; past the last step nothing is fetched (zeros are written)
-        uint8_t* st = lds + (s % kStages) * kStageBytes;
-        const bool on = s < S;
-        const __amdgpu_buffer_rsrc_t ra =
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.a + m0 * row_bytes), 0, on ? valid * row_bytes : 0, kBufferWord3);
-        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t*>(as0 + static_cast<int64_t>(s) * p.M4 * 4), 0, on ? scale_bytes : 0, kBufferWord3);
-#pragma unroll
-        for (int q = 0; q < kRowLoads; ++q)
+    // load q (0 .. kLoads - 1) of a stage: the rows', then their scales; past the last step nothing is fetched (zeros are
+    // written)
+    auto issue = [&](int stage, int q) {
+        uint8_t* st = lds + (stage & 1) * kStageBytes;
+        if (q < kRowLoads) {
+            const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<uint8_t*>(p.a + m0 * row_bytes), 0, stage * kSub < S ? valid_bytes : 0, kBufferWord3);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, st + (wave * kRowLoads + q) * 1024, 16,
-                                                     voff[kA8 ? q & 1 : 0] + static_cast<uint32_t>(q * kRowsPerLoad * row_bytes),
-                                                     s * kRow, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, st + BM * kRow + (wave * 64) % BM * 4, 4, soff, 0, 0, 0);
+                                                     voff[q & 1] + static_cast<uint32_t>(q * 8 * row_bytes),
+                                                     stage * 128, 0, 0);
+        } else {
+            const int u = (wave + 4 * (q - kRowLoads)) * 64 % (kSub * BM);  // (with fewer rows than lanes, waves load the same)
+            const int s = stage * kSub + u / BM;
+            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<uint8_t*>(p.as + (static_cast<int64_t>(s) * p.M4 + m0) * 4), 0, s < S ? scale_bytes : 0, kBufferWord3);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, st + kScales + u * 4, 4, static_cast<uint32_t>((u % BM + lane) * 4), 0, 0,
+                                                     0);
+        }
     };
-    const int group = min(n0 / kGroupRows + wn, (p.N + kGroupRows - 1) / kGroupRows - 1);  // (columns past N are not stored)
+    const int group = min(n0 / kGroupRows + wave, (p.N + kGroupRows - 1) / kGroupRows - 1);  // (columns past N are not stored)
     const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint8_t*>(p.w + static_cast<int64_t>(group) * S * kRecord), 0, S * kRecord, kBufferWord3);
-    struct WRegs {
-        i32x4 f[4];
-        int s;
-    };
-    uint32_t woff = 16 * lane, wsoff = 4096 + 4 * lane;
-    auto load_w = [&](WRegs& d) {  // the next record (past the last: nothing is fetched)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            d.f[j] = load16(rw, woff + 1024 * j);
-        d.s = load4(rw, wsoff);
-        woff += kRecord;
-        wsoff += kRecord;
-    };
+    uint32_t woff = 16 * lane, wsoff = 4096 + 4 * lane;  // (past the last record: nothing is fetched)
+    i32x4 w[4];
+    int sw;
     AFrag<kA8> fa[MI];
     int sa[MI];
-    const uint32_t foff = static_cast<uint32_t>((wm * 16 * MI + r) * kRow);
-    const uint32_t fkey = kA8 ? (r >> 1) & 7 : (r >> 2) & 3;
-    const uint32_t fo0 = foff + ((g ^ fkey) << 4), fo1 = foff + (((4 + g) ^ fkey) << 4);
-    const uint32_t sco = static_cast<uint32_t>(BM * kRow + (wm * 16 * MI + r) * 4 + g);
-    auto read_a = [&](int stage, int i) {
-        const uint8_t* st = lds + stage * kStageBytes;
-        fa[i].lo = *reinterpret_cast<const i32x4*>(st + fo0 + i * 16 * kRow);
-        if constexpr (kA8) fa[i].hi = *reinterpret_cast<const i32x4*>(st + fo1 + i * 16 * kRow);
-        sa[i] = st[sco + 64 * i];
+    const uint32_t key = (r >> 1) & 7;
+    const uint32_t fo = static_cast<uint32_t>(r * 128) + ((g ^ key) << 4);  // (piece 4 + g: bit 6 the other way)
+    const uint32_t sco = static_cast<uint32_t>(kScales + r * 4 + g);
+    auto read_a = [&](int stage, int sub, int i) {
+        const uint8_t* st = lds + (stage & 1) * kStageBytes;
+        fa[i].lo = *reinterpret_cast<const i32x4*>(st + (fo ^ (sub << 6)) + i * 2048);
+        if constexpr (kA8) fa[i].hi = *reinterpret_cast<const i32x4*>(st + (fo ^ 64u) + i * 2048);
+        sa[i] = st[sco + (sub * BM + 16 * i) * 4];
     };
     auto fence = [&]() {
         asm volatile("" ::: "memory");
@@ -327,53 +314,88 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         fence();
     };
     f32x4 acc[MI][4];
-    // One step: the operands of step s are in registers.  The next weights are asked for; one block row into the step the next
-    // stage is waited for (the loads issued after its own are left in flight) and published, the stage read out is refilled,
-    // and each token operand is replaced by the next step's behind its last use.  The last step does so too: zeros.
-    WRegs cur, nxt;
-    auto step = [&](auto first_tag, int s) {
-        constexpr bool kFirst = decltype(first_tag)::value;
-        load_w(nxt);
-        fence();
-        const int nst = (s + 1) % kStages;
+    // One step: its operands are in registers.  A weight operand is replaced by the next record's behind the MI instructions that
+    // use it, a token operand by the next step's behind its last, so each load is 3 MI or MI instructions ahead of its use and
+    // no second set is held.  In a step that ends its stage (t), the next stage is waited for before the first of the latter
+    // (the loads issued after its own are left in flight: kBehind) and published, and the stage read out is refilled.  The last
+    // step loads too: zeros, or the columns of another row, which nothing uses.
+    constexpr int kBehind = kSub * kWLoads;
+    auto step = [&](auto first_tag, auto ends_tag, int t) {
+        constexpr bool kFirst = decltype(first_tag)::value, kEnds = decltype(ends_tag)::value;
         const f32x4 z = {};
+        woff += kRecord;
+        wsoff += kRecord;
+        int next_sw = 0;
+        auto phase = [&](auto j_tag) {
+            constexpr int j = decltype(j_tag)::value;
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            acc[i][0] = mfma<kA8, 0>(cur.f[0], cur.s, fa[i], sa[i], kFirst ? z : acc[i][0]);
-            acc[i][1] = mfma<kA8, 1>(cur.f[1], cur.s, fa[i], sa[i], kFirst ? z : acc[i][1]);
-            acc[i][2] = mfma<kA8, 2>(cur.f[2], cur.s, fa[i], sa[i], kFirst ? z : acc[i][2]);
-            acc[i][3] = mfma<kA8, 3>(cur.f[3], cur.s, fa[i], sa[i], kFirst ? z : acc[i][3]);
-            if (i == 0) {
-                fence();
-                __builtin_amdgcn_s_waitcnt(wait_vmcnt(kStages == 2 ? kWLoads : 2 * kWLoads + kLoads));
-                barrier();
-                issue(s + kStages);
+            for (int i = 0; i < MI; ++i) {
+                acc[i][j] = mfma<kA8, j>(w[j], sw, fa[i], sa[i], kFirst ? z : acc[i][j]);
+                if constexpr (j == 3) {
+                    if (kEnds && i == 0) {
+                        fence();
+                        __builtin_amdgcn_s_waitcnt(wait_vmcnt(kBehind));
+                        barrier();
+                    }
+                    read_a(kEnds ? t + 1 : t, kEnds ? 0 : 1, i);
+                    if (kEnds) {
+                        if (i < kLoads) issue(t + 2, i);
+                        if (i == MI - 1) {
+#pragma unroll
+                            for (int q = MI; q < kLoads; ++q) issue(t + 2, q);
+                        }
+                    }
+                    fence();
+                }
             }
-            read_a(nst, i);
+            w[j] = load16(rw, woff + 1024 * j);
+            if constexpr (j == 2) next_sw = load4(rw, wsoff);
             fence();
-        }
-        cur = nxt;
+        };
+        phase(std::integral_constant<int, 0>{});
+        phase(std::integral_constant<int, 1>{});
+        phase(std::integral_constant<int, 2>{});
+        phase(std::integral_constant<int, 3>{});
+        sw = next_sw;
     };
 #pragma unroll
-    for (int s = 0; s < kStages; ++s) issue(s);
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) issue(t, q);
     fence();
-    load_w(cur);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = load16(rw, woff + 1024 * j);
+    sw = load4(rw, wsoff);
     fence();
-    __builtin_amdgcn_s_waitcnt(wait_vmcnt(kWLoads + (kStages - 1) * kLoads));
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(kWLoads + kLoads));
     barrier();
 #pragma unroll
-    for (int i = 0; i < MI; ++i) read_a(0, i);
+    for (int i = 0; i < MI; ++i) read_a(0, 0, i);
     fence();
-    step(std::true_type{}, 0);
-    for (int s = 1; s < S; ++s) step(std::false_type{}, s);
+    using T_ = std::true_type;
+    using F_ = std::false_type;
+    if constexpr (kSub == 1) {
+        step(T_{}, T_{}, 0);
+        for (int s = 1; s < S; ++s) step(F_{}, T_{}, s);
+    } else {
+        step(T_{}, F_{}, 0);
+        int s = 1;
+        for (; s + 1 < S; s += 2) {
+            step(F_{}, T_{}, s >> 1);
+            step(F_{}, F_{}, (s >> 1) + 1);
+        }
+        if (s < S) step(F_{}, T_{}, s >> 1);
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));  // loads past the last step still write LDS; no store is waited for
+    fence();
     // lane group g has, of token 16 i + r and block pair h, the eight columns 32 h + 8 g .. +7
-    const int nw = n0 + 64 * wn;
+    const int nw = n0 + 64 * wave;
     auto columns = [&](int i, int h) {
         const f32x4 &u = acc[i][2 * h], &v = acc[i][2 * h + 1];
         return swap_groups(u32x2{pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3])},
                            u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])});
     };
-    const int64_t mw = m0 + 16 * MI * wm + r;
+    const int64_t mw = m0 + r;
     if (!kGate || n0 >= p.n_key) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
@@ -386,7 +408,6 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
                     __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p.kv + m * p.ld_out + (n - p.n_key)));
             }
         }
-        __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));  // (loads past the last step still write LDS: let them land)
         return;
     }
     if constexpr (kGate) {
@@ -408,9 +429,8 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
             for (int h = 0; h < 2; ++h)
                 d[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.x + m * p.n_key + nw + 32 * h + 8 * g));
         };
-        __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
         barrier();  // the stages are free, and nothing in flight writes them
-        float* sums = reinterpret_cast<float*>(lds);  // [wm][3][16 MI]: the right half's
+        float* sums = reinterpret_cast<float*>(lds) + (wave >> 1) * 3 * BM;  // the right half's of 128 columns
         float res[MI][3];
         u32x4 xr[2][2];
         load_x(xr[0], 0);
@@ -420,10 +440,10 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
             float hwk = 0.f, kk = 0.f, hh = 0.f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const u32x4 key = columns(i, h), x = xr[i & 1][h];
+                const u32x4 kr = columns(i, h), x = xr[i & 1][h];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float k0 = lo_bf16(key[e]), k1 = hi_bf16(key[e]), h0 = lo_bf16(x[e]), h1 = hi_bf16(x[e]);
+                    const float k0 = lo_bf16(kr[e]), k1 = hi_bf16(kr[e]), h0 = lo_bf16(x[e]), h1 = hi_bf16(x[e]);
                     hwk += h0 * wq[h][2 * e] * k0 + h1 * wq[h][2 * e + 1] * k1;
                     kk += k0 * k0 + k1 * k1;
                     hh += h0 * h0 + h1 * h1;
@@ -436,21 +456,21 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
             res[i][1] = kk + __shfl_xor(kk, 32, 64);
             res[i][2] = hh + __shfl_xor(hh, 32, 64);
         }
-        if (wn == 1 && g == 0) {
+        if ((wave & 1) && g == 0) {
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
-                for (int e = 0; e < 3; ++e) sums[(wm * 3 + e) * 16 * MI + 16 * i + r] = res[i][e];
+                for (int e = 0; e < 3; ++e) sums[e * BM + 16 * i + r] = res[i][e];
         }
         __syncthreads();
-        if (wn == 0 && g == 0) {  // the two halves' 64 columns, left first
-            float* out = p.part + static_cast<int64_t>(n0 / BN) * 3 * p.M;
+        if (!(wave & 1) && g == 0) {  // the two halves of 128 columns, left first
+            float* out = p.part + static_cast<int64_t>(n0 / 128 + (wave >> 1)) * 3 * p.M;
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 const int64_t m = mw + 16 * i;
 #pragma unroll
                 for (int e = 0; e < 3; ++e)
-                    if (m < p.M) out[e * p.M + m] = res[i][e] + sums[(wm * 3 + e) * 16 * MI + 16 * i + r];
+                    if (m < p.M) out[e * p.M + m] = res[i][e] + sums[e * BM + 16 * i + r];
             }
         }
     }
@@ -527,9 +547,9 @@ int launch_direct(const Mx4Args& p, hipStream_t stream, const char* what) {
 
 template <bool kA8, bool kGate>
 int launch_tiles(const Mx4Args& p, hipStream_t stream, const char* what) {
-    const int mi = p.M <= 512 ? 4 : 8;
-    const int64_t tiles_m = (p.M + 32 * mi - 1) / (32 * mi);
-    const int tiles_n = (p.N + 127) / 128;
+    const int mi = p.M <= 256 ? 4 : 8;
+    const int64_t tiles_m = (p.M + 16 * mi - 1) / (16 * mi);
+    const int tiles_n = (p.N + 255) / 256;
     if (tiles_m > kMostGroups / tiles_n) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
     const dim3 grid(static_cast<unsigned>(tiles_m * tiles_n)), block(256);
     const int tm = static_cast<int>(tiles_m);

@@ -58,6 +58,11 @@ __device__ inline bf16x2 as_pair(uint32_t w) { return __builtin_bit_cast(bf16x2,
 __device__ inline float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ inline float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// c + a.lo * b.lo + a.hi * b.hi over packed bf16 pairs, fp32 accumulation
+__device__ inline float dot2_bf16(uint32_t a, uint32_t b, float c) {
+    return __builtin_amdgcn_fdot2_f32_bf16(as_pair(a), as_pair(b), c, false);
+}
+
 // a token operand of the matrix instruction
 template <bool kA8>
 struct AFrag;
@@ -202,24 +207,9 @@ __global__ __launch_bounds__(kGate ? 512 : 256) void mx4_direct_kernel(Mx4Args p
 constexpr int kBufferWord3 = 0x00020000;
 constexpr int kWaitLgkmcnt0 = 0xC07F;
 constexpr int wait_vmcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | 0x0F70; }
+constexpr int kNonTemporal = 2;  // cache-policy operand of a load: streamed past L2
 constexpr int kXcds = 8;
 constexpr int kGroupM = 8;  // tile rows that an XCD walks together
-
-// the halves of the four lanes of a token, {16 j + 4 g .. +3 of blocks j = 0, 1} for lane group g, as 8 neighbouring columns a
-// lane: group g has columns 8 g .. 8 g + 7 of the two blocks' 32
-__device__ inline u32x4 swap_groups(u32x2 a, u32x2 b) {
-    u32x4 o;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const uint32_t x = a[e], y = b[e];
-        const auto s = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-        const uint32_t s0 = s[0], s1 = s[1];
-        const auto t = __builtin_amdgcn_permlane16_swap(s0, s1, false, false);
-        o[e] = t[0];
-        o[2 + e] = t[1];
-    }
-    return o;
-}
 
 __device__ inline i32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t at) {
     const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
@@ -239,7 +229,9 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
     constexpr int kScaleLoads = (kSub * BM + 255) / 256;    // 64 rows of a step each
     constexpr int kLoads = kRowLoads + kScaleLoads;
     constexpr int kWLoads = 5;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStageBytes];
+    constexpr int kWaveBytes = BM * 128;                    // a wave's part of the tile as bf16, behind the last step
+    constexpr int kLds = 2 * kStageBytes > 4 * kWaveBytes ? 2 * kStageBytes : 4 * kWaveBytes;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r = lane & 15;
@@ -386,68 +378,77 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         }
         if (s < S) step(F_{}, T_{}, s >> 1);
     }
-    __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));  // loads past the last step still write LDS; no store is waited for
-    fence();
-    // lane group g has, of token 16 i + r and block pair h, the eight columns 32 h + 8 g .. +7
+    // Loads past the last step still write LDS: they land, and every wave has read its last operands, before the stages hold
+    // anything else.  From here a wave keeps to its own part of LDS: BM rows of its 64 columns, 16-byte piece c of row t at slot
+    // c ^ (t / 2) % 8, so that memory is written and read in whole lines of 128 bytes, two to 16 lanes.
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
+    barrier();
+    uint8_t* const mine = lds + wave * kWaveBytes;
     const int nw = n0 + 64 * wave;
-    auto columns = [&](int i, int h) {
-        const f32x4 &u = acc[i][2 * h], &v = acc[i][2 * h + 1];
-        return swap_groups(u32x2{pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3])},
-                           u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])});
-    };
-    const int64_t mw = m0 + r;
+    const int line_row = lane >> 3;  // a load or store of 16 bytes a lane has 8 rows: of these the lane's, and its piece
+    // a lane's four columns 16 j + 4 g .. +3 of token 16 i + r
+    const uint32_t quad[2] = {static_cast<uint32_t>(r * 128 + (((g >> 1) ^ key) << 4) + (g & 1) * 8),
+                              static_cast<uint32_t>(r * 128 + (((4 + (g >> 1)) ^ key) << 4) + (g & 1) * 8)};
+    auto quad_at = [&](int i, int j) { return mine + i * 2048 + (quad[j >> 1] ^ ((j & 1) << 5)); };
     if (!kGate || n0 >= p.n_key) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const int64_t m = mw + 16 * i;
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const u32x4 v = columns(i, h);
-                const int n = nw + 32 * h + 8 * g;
-                if (m < p.M && n < p.N)
-                    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p.kv + m * p.ld_out + (n - p.n_key)));
-            }
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<u32x2*>(quad_at(i, j)) =
+                    u32x2{pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3])};
+        const int n = nw + 8 * (lane & 7);
+        uint16_t* out = p.kv + (m0 + line_row) * p.ld_out + (n - p.n_key);
+#pragma unroll
+        for (int q = 0; q < 2 * MI; ++q) {
+            const int t = 8 * q + line_row;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(mine + t * 128 + (((lane & 7) ^ ((t >> 1) & 7)) << 4));
+            if (m0 + t < p.M && n < p.N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out + 8 * q * p.ld_out));
         }
         return;
     }
     if constexpr (kGate) {
-        // the lane's 16 columns of q * k (exact in fp32), and the stream rows a block row ahead
-        float wq[2][8];
+        // the stream's rows of the wave's tokens and columns (rows past M: zeros)
+        const int64_t x_bytes = static_cast<int64_t>(p.n_key) * 2;
+        const int x_rows = static_cast<int>(min<int64_t>(BM, p.M - m0));
+        const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint16_t*>(p.x + m0 * p.n_key + nw), 0, static_cast<int>(x_rows * x_bytes - 2 * nw), kBufferWord3);
+        const uint32_t xo = static_cast<uint32_t>(line_row * x_bytes), xp = ((lane & 7) ^ ((line_row >> 1) & 7)) << 4;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int n = nw + 32 * h + 8 * g;
-            const u32x4 q = *reinterpret_cast<const u32x4*>(p.q + n), k = *reinterpret_cast<const u32x4*>(p.k + n);
+        for (int q = 0; q < 2 * MI; ++q)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, mine + q * 1024, 16,
+                                                     xo + static_cast<uint32_t>(8 * q * x_bytes) + (q & 1 ? xp ^ 64u : xp), 0, 0,
+                                                     kNonTemporal);
+        float wq[4][4];  // q * k of the lane's columns (exact in fp32)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                wq[h][2 * e] = lo_bf16(q[e]) * lo_bf16(k[e]);
-                wq[h][2 * e + 1] = hi_bf16(q[e]) * hi_bf16(k[e]);
+        for (int j = 0; j < 4; ++j) {
+            const int n = nw + 16 * j + 4 * g;
+            const u32x2 q = *reinterpret_cast<const u32x2*>(p.q + n), k = *reinterpret_cast<const u32x2*>(p.k + n);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                wq[j][2 * e] = lo_bf16(q[e]) * lo_bf16(k[e]);
+                wq[j][2 * e + 1] = hi_bf16(q[e]) * hi_bf16(k[e]);
             }
         }
-        auto load_x = [&](u32x4 (&d)[2], int i) {
-            const int64_t m = min(mw + 16 * i, p.M - 1);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                d[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.x + m * p.n_key + nw + 32 * h + 8 * g));
-        };
-        barrier();  // the stages are free, and nothing in flight writes them
-        float* sums = reinterpret_cast<float*>(lds) + (wave >> 1) * 3 * BM;  // the right half's of 128 columns
         float res[MI][3];
-        u32x4 xr[2][2];
-        load_x(xr[0], 0);
+        fence();
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));  // the wave's own rows
+        fence();
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            if (i + 1 < MI) load_x(xr[(i + 1) & 1], i + 1);
             float hwk = 0.f, kk = 0.f, hh = 0.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const u32x4 kr = columns(i, h), x = xr[i & 1][h];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float k0 = lo_bf16(kr[e]), k1 = hi_bf16(kr[e]), h0 = lo_bf16(x[e]), h1 = hi_bf16(x[e]);
-                    hwk += h0 * wq[h][2 * e] * k0 + h1 * wq[h][2 * e + 1] * k1;
-                    kk += k0 * k0 + k1 * k1;
-                    hh += h0 * h0 + h1 * h1;
-                }
+            for (int j = 0; j < 4; ++j) {
+                // the product is a bf16 tensor before it is used, as the other forms of the projection round it
+                const uint32_t k01 = pack_bf16(acc[i][j][0], acc[i][j][1]), k23 = pack_bf16(acc[i][j][2], acc[i][j][3]);
+                const u32x2 x = *reinterpret_cast<const u32x2*>(quad_at(i, j));
+                const uint32_t x01 = x[0], x23 = x[1];
+                hwk += lo_bf16(x01) * wq[j][0] * lo_bf16(k01);
+                hwk += hi_bf16(x01) * wq[j][1] * hi_bf16(k01);
+                hwk += lo_bf16(x23) * wq[j][2] * lo_bf16(k23);
+                hwk += hi_bf16(x23) * wq[j][3] * hi_bf16(k23);
+                kk = dot2_bf16(k23, k23, dot2_bf16(k01, k01, kk));
+                hh = dot2_bf16(x23, x23, dot2_bf16(x01, x01, hh));
             }
             hwk += __shfl_xor(hwk, 16, 64);
             kk += __shfl_xor(kk, 16, 64);
@@ -456,6 +457,11 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
             res[i][1] = kk + __shfl_xor(kk, 32, 64);
             res[i][2] = hh + __shfl_xor(hh, 32, 64);
         }
+        // two waves' 64 columns make a slice of 128: the right one leaves its sums in its part of LDS
+        float* sums = reinterpret_cast<float*>(lds + (wave | 1) * kWaveBytes);
+        fence();
+        __builtin_amdgcn_s_waitcnt(kWaitLgkmcnt0);
+        fence();
         if ((wave & 1) && g == 0) {
 #pragma unroll
             for (int i = 0; i < MI; ++i)
@@ -463,11 +469,11 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
                 for (int e = 0; e < 3; ++e) sums[e * BM + 16 * i + r] = res[i][e];
         }
         __syncthreads();
-        if (!(wave & 1) && g == 0) {  // the two halves of 128 columns, left first
+        if (!(wave & 1) && g == 0) {
             float* out = p.part + static_cast<int64_t>(n0 / 128 + (wave >> 1)) * 3 * p.M;
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
-                const int64_t m = mw + 16 * i;
+                const int64_t m = m0 + 16 * i + r;
 #pragma unroll
                 for (int e = 0; e < 3; ++e)
                     if (m < p.M) out[e * p.M + m] = res[i][e] + sums[e * BM + 16 * i + r];

@@ -74,10 +74,15 @@ __device__ inline mx_u32x2 mxint8_encode8(const u32x4& v, uint32_t code) {
 __device__ inline float mxint8_unit(uint32_t code) {
     return code == 255 ? __uint_as_float(0x7FC00000u) : __builtin_ldexpf(1.0f, static_cast<int>(code) - 133);
 }
+// element e of eight, in units (cut out of its word: as shifted bytes the eight of a row are made 64-bit shifts that hold a
+// register pair each, and the gradient that reads eight rows spilled 86 registers)
+__device__ inline float mxint8_at(const mx_u32x2& q, int e) {
+    return static_cast<float>(static_cast<int>(__builtin_amdgcn_sbfe(q[e / 4], 8 * (e % 4), 8)));
+}
 // eight elements as floats (exact)
 __device__ inline void mxint8_decode8(const mx_u32x2& q, float unit, float (&f)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = static_cast<float>(static_cast<int8_t>(q[e / 4] >> (8 * (e % 4)))) * unit;
+    for (int e = 0; e < 8; ++e) f[e] = mxint8_at(q, e) * unit;
 }
 
 }  // namespace engram

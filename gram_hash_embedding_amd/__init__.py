@@ -116,8 +116,9 @@ def _check(status: int) -> None:
 def _stream(stream):
     import torch
 
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # the current stream's handle, without a Stream object for it
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _dev(t, name, dtype, ndim=None):

@@ -84,118 +84,6 @@ __device__ inline f32x4 mfma(const i32x4& w, int sw, const AFrag<kA8>& a, int sa
                                                             kA8 ? kFp8 : kFp4, kSel, sw, 0, sa);
 }
 
-// ---- the sums of a (token, 4 columns) piece of a key row against the stream
-struct GateSums {
-    float hwk, kk, hh;
-};
-__device__ inline void gate_add(GateSums& s, const f32x4& acc, u32x2 h, u32x2 q, u32x2 k) {
-    // the product is a bf16 tensor before it is used, as the other forms of the projection round it
-    const uint32_t k01 = pack_bf16(acc[0], acc[1]), k23 = pack_bf16(acc[2], acc[3]);
-    const float key[4] = {lo_bf16(k01), hi_bf16(k01), lo_bf16(k23), hi_bf16(k23)};
-    const float hv[4] = {lo_bf16(h[0]), hi_bf16(h[0]), lo_bf16(h[1]), hi_bf16(h[1])};
-    const float w[4] = {lo_bf16(q[0]) * lo_bf16(k[0]), hi_bf16(q[0]) * hi_bf16(k[0]), lo_bf16(q[1]) * lo_bf16(k[1]),
-                        hi_bf16(q[1]) * hi_bf16(k[1])};  // exact: bf16 * bf16 fits fp32
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        s.hwk += hv[e] * w[e] * key[e];
-        s.kk += key[e] * key[e];
-        s.hh += hv[e] * hv[e];
-    }
-}
-
-// ---- few tokens: a wave per 16 weight rows and 16 MI tokens, every operand straight from memory to registers, kDepth steps
-// of 128 columns in flight.  A workgroup has 64 rows (a gate launch: 128, whose sums meet in LDS).
-template <bool kA8, int MI, bool kGate>
-__global__ __launch_bounds__(kGate ? 512 : 256) void mx4_direct_kernel(Mx4Args p, int groups_n) {
-    constexpr int kDepth = 4;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int g = lane >> 4, r = lane & 15, j = wave & 3;
-    const int bn = static_cast<int>(blockIdx.x % groups_n);
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x / groups_n) * (16 * MI);
-    const int group = (kGate ? 2 : 1) * bn + (wave >> 2);
-    const uint8_t* w = p.w + static_cast<int64_t>(group) * p.steps * kRecord;
-    const uint8_t* a[MI];
-    const uint8_t* as[MI];
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int64_t m = min(m0 + 16 * i + r, p.M - 1);  // rows past the last repeat it; they are not stored
-        a[i] = p.a + m * p.steps * (kA8 ? 128 : 64) + 16 * g;
-        as[i] = p.as + m * 4 + g;
-    }
-    i32x4 wf[kDepth];
-    AFrag<kA8> af[kDepth][MI];
-    int sw[kDepth], sa[kDepth][MI];
-    auto load = [&](int d, int s) {
-        const uint8_t* rec = w + static_cast<int64_t>(s) * kRecord;
-        wf[d] = *reinterpret_cast<const i32x4*>(rec + 1024 * j + 16 * lane);
-        sw[d] = rec[4096 + 4 * lane + j];
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const uint8_t* row = a[i] + static_cast<int64_t>(s) * (kA8 ? 128 : 64);
-            af[d][i].lo = *reinterpret_cast<const i32x4*>(row);
-            if constexpr (kA8) af[d][i].hi = *reinterpret_cast<const i32x4*>(row + 64);
-            sa[d][i] = as[i][static_cast<int64_t>(s) * p.M4 * 4];
-        }
-    };
-    f32x4 acc[MI];
-#pragma unroll
-    for (int i = 0; i < MI; ++i) acc[i] = f32x4{};
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(d, min(d, p.steps - 1));
-    for (int s0 = 0; s0 < p.steps; s0 += kDepth) {
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-            if (s0 + d < p.steps) {
-#pragma unroll
-                for (int i = 0; i < MI; ++i) acc[i] = mfma<kA8, 0>(wf[d], sw[d], af[d][i], sa[d][i], acc[i]);
-            }
-            load(d, min(s0 + d + kDepth, p.steps - 1));
-        }
-    }
-    const int n = kGroupRows * group + 16 * j + 4 * g;  // the lane's four columns
-    if (!kGate || n >= p.n_key) {  // (a workgroup's columns are all keys or none)
-        if (n >= p.N) return;
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const int64_t m = m0 + 16 * i + r;
-            if (m < p.M)
-                *reinterpret_cast<u32x2*>(p.kv + m * p.ld_out + (n - p.n_key)) =
-                    u32x2{pack_bf16(acc[i][0], acc[i][1]), pack_bf16(acc[i][2], acc[i][3])};
-        }
-        return;
-    }
-    if constexpr (kGate) {
-        __shared__ float sums[3][8][16 * MI];
-        const u32x2 q = *reinterpret_cast<const u32x2*>(p.q + n), k = *reinterpret_cast<const u32x2*>(p.k + n);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const int64_t m = min(m0 + 16 * i + r, p.M - 1);
-            GateSums s = {0.f, 0.f, 0.f};
-            gate_add(s, acc[i], *reinterpret_cast<const u32x2*>(p.x + m * p.n_key + n), q, k);
-            s.hwk += __shfl_xor(s.hwk, 16, 64);
-            s.kk += __shfl_xor(s.kk, 16, 64);
-            s.hh += __shfl_xor(s.hh, 16, 64);
-            s.hwk += __shfl_xor(s.hwk, 32, 64);
-            s.kk += __shfl_xor(s.kk, 32, 64);
-            s.hh += __shfl_xor(s.hh, 32, 64);
-            if (g == 0) {
-                sums[0][wave][16 * i + r] = s.hwk;
-                sums[1][wave][16 * i + r] = s.kk;
-                sums[2][wave][16 * i + r] = s.hh;
-            }
-        }
-        __syncthreads();
-        const int tid = threadIdx.x;
-        if (tid < 3 * 16 * MI) {
-            const int which = tid / (16 * MI), t = tid % (16 * MI);
-            float v = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v += sums[which][e][t];
-            if (m0 + t < p.M) p.part[(static_cast<int64_t>(bn) * 3 + which) * p.M + m0 + t] = v;
-        }
-    }
-}
-
 // ---- tiles: a workgroup of four waves has 16 MI tokens x 256 columns, two workgroups a CU, so that one's stores, sums and first
 // loads run under the other's matrix instructions.  A wave has all tokens and 64 columns, MI x 4 blocks of 16 x 16.  The token
 // rows come through LDS, 128 bytes of each (128 columns in 8 bits, 256 in 4) a stage, in two stages, by direct-to-LDS loads (rows
@@ -219,18 +107,21 @@ __device__ inline int load4(__amdgpu_buffer_rsrc_t r, uint32_t at) {
     return static_cast<int>(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
 }
 
-template <bool kA8, int MI, bool kGate>
+template <bool kA8, int MI, int kSets, bool kGate>
 __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int tiles_n) {
     constexpr int BM = 16 * MI, BN = 256;
     constexpr int kSub = kA8 ? 1 : 2;                       // steps of a stage
     constexpr int kScales = BM * 128;                       // a stage: its rows, then a word per row and step
-    constexpr int kStageBytes = kScales + kSub * BM * 4;
+    constexpr int kScaleRows = BM > 64 ? BM : 64;           // (a load of them writes 64 words)
+    constexpr int kStageBytes = kScales + kSub * kScaleRows * 4;
     constexpr int kRowLoads = (BM + 31) / 32;               // per wave and stage: 8 rows each
-    constexpr int kScaleLoads = (kSub * BM + 255) / 256;    // 64 rows of a step each
+    constexpr int kScaleLoads = (kSub * kScaleRows + 255) / 256;  // 64 rows of a step each
     constexpr int kLoads = kRowLoads + kScaleLoads;
     constexpr int kWLoads = 5;
+    constexpr int kStages = kSets > 1 ? kSets / kSub + 1 : 2;
+    constexpr int kRing = kStages * kStageBytes;
     constexpr int kWaveBytes = BM * 128;                    // a wave's part of the tile as bf16, behind the last step
-    constexpr int kLds = 2 * kStageBytes > 4 * kWaveBytes ? 2 * kStageBytes : 4 * kWaveBytes;
+    constexpr int kLds = kRing > 4 * kWaveBytes ? kRing : 4 * kWaveBytes;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -255,45 +146,46 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
     const int valid_bytes = static_cast<int>(min<int64_t>(BM, p.M - m0)) * row_bytes;
     // row loads: load q of the wave fills 1 KB, rows 8 (kRowLoads wave + q) on, lane l slot l % 8 of row l / 8; the key of an odd
     // group of 8 rows is that of an even one plus 4
-    const int at_row = wave * kRowLoads * 8 + (lane >> 3);
+    const int row0 = wave * kRowLoads * 8 % BM;  // (with fewer rows than the waves load, some load the same)
+    const int at_row = row0 + (lane >> 3);
     const uint32_t piece = static_cast<uint32_t>(((lane & 7) ^ ((at_row >> 1) & 7)) << 4);
     const uint32_t voff[2] = {at_row * row_bytes + piece, at_row * row_bytes + (piece ^ 64u)};
     const int scale_bytes = static_cast<int>(min<int64_t>(BM, p.M4 - m0)) * 4;
-    // load q (0 .. kLoads - 1) of a stage: the rows', then their scales; past the last step nothing is fetched (zeros are
-    // written)
-    auto issue = [&](int stage, int q) {
-        uint8_t* st = lds + (stage & 1) * kStageBytes;
+    // load q (0 .. kLoads - 1) of a stage into the one at `slot`: the rows', then their scales; past the last step nothing is
+    // fetched (zeros are written)
+    auto issue = [&](int stage, int slot, int q) {
+        uint8_t* st = lds + slot;
         if (q < kRowLoads) {
             const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
                 const_cast<uint8_t*>(p.a + m0 * row_bytes), 0, stage * kSub < S ? valid_bytes : 0, kBufferWord3);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, st + (wave * kRowLoads + q) * 1024, 16,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, st + (row0 + 8 * q) * 128, 16,
                                                      voff[q & 1] + static_cast<uint32_t>(q * 8 * row_bytes),
                                                      stage * 128, 0, 0);
         } else {
-            const int u = (wave + 4 * (q - kRowLoads)) * 64 % (kSub * BM);  // (with fewer rows than lanes, waves load the same)
-            const int s = stage * kSub + u / BM;
+            const int u = (wave + 4 * (q - kRowLoads)) * 64 % (kSub * kScaleRows);  // (some waves load the same here too)
+            const int s = stage * kSub + u / kScaleRows;
             const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
                 const_cast<uint8_t*>(p.as + (static_cast<int64_t>(s) * p.M4 + m0) * 4), 0, s < S ? scale_bytes : 0, kBufferWord3);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, st + kScales + u * 4, 4, static_cast<uint32_t>((u % BM + lane) * 4), 0, 0,
-                                                     0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, st + kScales + u * 4, 4, static_cast<uint32_t>((u % kScaleRows + lane) * 4), 0,
+                                                     0, 0);
         }
     };
     const int group = min(n0 / kGroupRows + wave, (p.N + kGroupRows - 1) / kGroupRows - 1);  // (columns past N are not stored)
     const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint8_t*>(p.w + static_cast<int64_t>(group) * S * kRecord), 0, S * kRecord, kBufferWord3);
     uint32_t woff = 16 * lane, wsoff = 4096 + 4 * lane;  // (past the last record: nothing is fetched)
-    i32x4 w[4];
-    int sw;
+    i32x4 w[kSets][4];
+    int sw[kSets];
     AFrag<kA8> fa[MI];
     int sa[MI];
     const uint32_t key = (r >> 1) & 7;
     const uint32_t fo = static_cast<uint32_t>(r * 128) + ((g ^ key) << 4);  // (piece 4 + g: bit 6 the other way)
     const uint32_t sco = static_cast<uint32_t>(kScales + r * 4 + g);
-    auto read_a = [&](int stage, int sub, int i) {
-        const uint8_t* st = lds + (stage & 1) * kStageBytes;
+    auto read_a = [&](int slot, int sub, int i) {
+        const uint8_t* st = lds + slot;
         fa[i].lo = *reinterpret_cast<const i32x4*>(st + (fo ^ (sub << 6)) + i * 2048);
         if constexpr (kA8) fa[i].hi = *reinterpret_cast<const i32x4*>(st + (fo ^ 64u) + i * 2048);
-        sa[i] = st[sco + (sub * BM + 16 * i) * 4];
+        sa[i] = st[sco + (sub * kScaleRows + 16 * i) * 4];
     };
     auto fence = [&]() {
         asm volatile("" ::: "memory");
@@ -306,41 +198,48 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         fence();
     };
     f32x4 acc[MI][4];
-    // One step: its operands are in registers.  A weight operand is replaced by the next record's behind the MI instructions that
-    // use it, a token operand by the next step's behind its last, so each load is 3 MI or MI instructions ahead of its use and
-    // no second set is held.  In a step that ends its stage (t), the next stage is waited for before the first of the latter
-    // (the loads issued after its own are left in flight: kBehind) and published, and the stage read out is refilled.  The last
-    // step loads too: zeros, or the columns of another row, which nothing uses.
-    constexpr int kBehind = kSub * kWLoads;
-    auto step = [&](auto first_tag, auto ends_tag, int t) {
+    // One step: its operands are in registers, the weights' in set kSet.  A weight operand is replaced by that of kSets steps on
+    // behind the MI instructions that use it, a token operand by the next step's behind its last.  In a step that ends its
+    // stage (t), the next stage is waited for before the first of the latter (the loads issued after its own are left in
+    // flight: kBehind) and published, and the stage read out is refilled.  The last step loads too: zeros, or the columns of
+    // another row, which nothing uses.
+    //
+    // kBehind: behind the loads of stage t + 1, which a wave issued in the step that ended stage t + 1 - kStages, stand that
+    // step's last weight load, the kStages - 2 whole stages between, and stage t's weight loads but the last.  The first
+    // kStages stages are issued together, before kSets records of weights: behind any of them stand more than kBehind.
+    constexpr int kBehind = (kStages - 2) * (kSub * kWLoads + kLoads) + kSub * kWLoads;
+    static_assert(kSets > (kStages - 2) * kSub, "the first barriers count on this");
+    static_assert(kBehind < 64 && (kSets == 1 || kSets % kSub == 0), "");
+    int slot = 0;
+    auto step = [&](auto first_tag, auto ends_tag, auto set_tag, int t) {
         constexpr bool kFirst = decltype(first_tag)::value, kEnds = decltype(ends_tag)::value;
+        constexpr int kSet = decltype(set_tag)::value % kSets;
         const f32x4 z = {};
-        woff += kRecord;
-        wsoff += kRecord;
+        const int next = !kEnds ? slot : slot == (kStages - 1) * kStageBytes ? 0 : slot + kStageBytes;
         int next_sw = 0;
         auto phase = [&](auto j_tag) {
             constexpr int j = decltype(j_tag)::value;
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
-                acc[i][j] = mfma<kA8, j>(w[j], sw, fa[i], sa[i], kFirst ? z : acc[i][j]);
+                acc[i][j] = mfma<kA8, j>(w[kSet][j], sw[kSet], fa[i], sa[i], kFirst ? z : acc[i][j]);
                 if constexpr (j == 3) {
                     if (kEnds && i == 0) {
                         fence();
                         __builtin_amdgcn_s_waitcnt(wait_vmcnt(kBehind));
                         barrier();
                     }
-                    read_a(kEnds ? t + 1 : t, kEnds ? 0 : 1, i);
+                    read_a(next, kEnds ? 0 : 1, i);
                     if (kEnds) {
-                        if (i < kLoads) issue(t + 2, i);
+                        if (i < kLoads) issue(t + kStages, slot, i);
                         if (i == MI - 1) {
 #pragma unroll
-                            for (int q = MI; q < kLoads; ++q) issue(t + 2, q);
+                            for (int q = MI; q < kLoads; ++q) issue(t + kStages, slot, q);
                         }
                     }
                     fence();
                 }
             }
-            w[j] = load16(rw, woff + 1024 * j);
+            w[kSet][j] = load16(rw, woff + 1024 * j);
             if constexpr (j == 2) next_sw = load4(rw, wsoff);
             fence();
         };
@@ -348,35 +247,52 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         phase(std::integral_constant<int, 1>{});
         phase(std::integral_constant<int, 2>{});
         phase(std::integral_constant<int, 3>{});
-        sw = next_sw;
+        sw[kSet] = next_sw;
+        woff += kRecord;
+        wsoff += kRecord;
+        slot = next;
     };
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < kStages; ++t)
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q) issue(t, q);
+        for (int q = 0; q < kLoads; ++q) issue(t, t * kStageBytes, q);
     fence();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = load16(rw, woff + 1024 * j);
-    sw = load4(rw, wsoff);
-    fence();
-    __builtin_amdgcn_s_waitcnt(wait_vmcnt(kWLoads + kLoads));
+    for (int e = 0; e < kSets; ++e) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[e][j] = load16(rw, woff + 1024 * j);
+        sw[e] = load4(rw, wsoff);
+        woff += kRecord;
+        wsoff += kRecord;
+        fence();
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(kSets * kWLoads + (kStages - 1) * kLoads));
     barrier();
 #pragma unroll
     for (int i = 0; i < MI; ++i) read_a(0, 0, i);
     fence();
-    using T_ = std::true_type;
-    using F_ = std::false_type;
-    if constexpr (kSub == 1) {
-        step(T_{}, T_{}, 0);
-        for (int s = 1; s < S; ++s) step(F_{}, T_{}, s);
-    } else {
-        step(T_{}, F_{}, 0);
+    {
+        // sets and the steps of a stage in turn: step s has set s % kSets and ends its stage if s % kSub is kSub - 1
+        constexpr int kTurn = kSets > kSub ? kSets : kSub;
+        auto turn = [&](auto u_tag, int s) {
+            constexpr int u = decltype(u_tag)::value;
+            step(std::false_type{}, std::integral_constant<bool, u % kSub == kSub - 1>{}, u_tag, s / kSub);
+        };
+        step(std::true_type{}, std::integral_constant<bool, kSub == 1>{}, std::integral_constant<int, 0>{}, 0);
         int s = 1;
-        for (; s + 1 < S; s += 2) {
-            step(F_{}, T_{}, s >> 1);
-            step(F_{}, F_{}, (s >> 1) + 1);
+        for (; s + kTurn <= S; s += kTurn) {
+            turn(std::integral_constant<int, 1>{}, s);
+            if constexpr (kTurn > 1) turn(std::integral_constant<int, 2>{}, s + 1);
+            if constexpr (kTurn > 2) turn(std::integral_constant<int, 3>{}, s + 2);
+            if constexpr (kTurn > 3) turn(std::integral_constant<int, 4>{}, s + 3);
         }
-        if (s < S) step(F_{}, T_{}, s >> 1);
+        if constexpr (kTurn > 1) {
+            if (s < S) turn(std::integral_constant<int, 1>{}, s);
+        }
+        if constexpr (kTurn > 2) {
+            if (s + 1 < S) turn(std::integral_constant<int, 2>{}, s + 1);
+            if (s + 2 < S) turn(std::integral_constant<int, 3>{}, s + 2);
+        }
     }
     // Loads past the last step still write LDS: they land, and every wave has read its last operands, before the stages hold
     // anything else.  From here a wave keeps to its own part of LDS: BM rows of its 64 columns, 16-byte piece c of row t at slot
@@ -482,10 +398,10 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
     }
 }
 
-template <bool kA8, int MI, bool kGate>
+template <bool kA8, int MI, int kSets, bool kGate>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void mx4_tile_kernel(Mx4Args p, int tiles_m,
                                                                                                  int tiles_n) {
-    mx4_tile_body<kA8, MI, kGate>(p, tiles_m, tiles_n);
+    mx4_tile_body<kA8, MI, kSets, kGate>(p, tiles_m, tiles_n);
 }
 
 // ---- quantisation of bf16 rows: a thread has 8 consecutive columns, the 4 threads of a block find its largest magnitude (as
@@ -539,35 +455,18 @@ __global__ __launch_bounds__(256) void mx4_pack_kernel(const uint8_t* q, const u
 constexpr int64_t kMostGroups = (1 << 23) - 1;  // workgroups of a launch: its threads have to stay under 2^32
 
 template <bool kA8, bool kGate>
-int launch_direct(const Mx4Args& p, hipStream_t stream, const char* what) {
-    const int groups_n = (p.N + (kGate ? 128 : 64) - 1) / (kGate ? 128 : 64);
-    const int mi = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
-    const int64_t groups = (p.M + 16 * mi - 1) / (16 * mi) * groups_n;
-    if (groups > kMostGroups) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
-    const dim3 grid(static_cast<unsigned>(groups)), block(kGate ? 512 : 256);
-    if (mi == 1) hipLaunchKernelGGL((mx4_direct_kernel<kA8, 1, kGate>), grid, block, 0, stream, p, groups_n);
-    else if (mi == 2) hipLaunchKernelGGL((mx4_direct_kernel<kA8, 2, kGate>), grid, block, 0, stream, p, groups_n);
-    else hipLaunchKernelGGL((mx4_direct_kernel<kA8, 4, kGate>), grid, block, 0, stream, p, groups_n);
-    return check_launch(what);
-}
-
-template <bool kA8, bool kGate>
-int launch_tiles(const Mx4Args& p, hipStream_t stream, const char* what) {
-    const int mi = p.M <= 256 ? 4 : 8;
+int launch(const Mx4Args& p, hipStream_t stream, const char* what) {
+    const int mi = p.M <= 32 ? 1 : p.M <= 128 ? 2 : p.M <= 256 ? 4 : 8;
     const int64_t tiles_m = (p.M + 16 * mi - 1) / (16 * mi);
     const int tiles_n = (p.N + 255) / 256;
     if (tiles_m > kMostGroups / tiles_n) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
     const dim3 grid(static_cast<unsigned>(tiles_m * tiles_n)), block(256);
     const int tm = static_cast<int>(tiles_m);
-    if (mi == 4) hipLaunchKernelGGL((mx4_tile_kernel<kA8, 4, kGate>), grid, block, 0, stream, p, tm, tiles_n);
-    else hipLaunchKernelGGL((mx4_tile_kernel<kA8, 8, kGate>), grid, block, 0, stream, p, tm, tiles_n);
+    if (mi == 1) hipLaunchKernelGGL((mx4_tile_kernel<kA8, 1, 4, kGate>), grid, block, 0, stream, p, tm, tiles_n);
+    else if (mi == 2) hipLaunchKernelGGL((mx4_tile_kernel<kA8, 2, 4, kGate>), grid, block, 0, stream, p, tm, tiles_n);
+    else if (mi == 4) hipLaunchKernelGGL((mx4_tile_kernel<kA8, 4, 2, kGate>), grid, block, 0, stream, p, tm, tiles_n);
+    else hipLaunchKernelGGL((mx4_tile_kernel<kA8, 8, 1, kGate>), grid, block, 0, stream, p, tm, tiles_n);
     return check_launch(what);
-}
-
-template <bool kA8, bool kGate>
-int launch(const Mx4Args& p, hipStream_t stream, const char* what) {
-    if (p.M <= 64) return launch_direct<kA8, kGate>(p, stream, what);
-    return launch_tiles<kA8, kGate>(p, stream, what);
 }
 
 constexpr int kMaxK = 1 << 20, kMaxN = 1 << 22;

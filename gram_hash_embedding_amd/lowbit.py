@@ -13,9 +13,10 @@ no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import NamedTuple
 
-from . import _check, engram_mx_scale_bytes, engram_wkv_gate_workspace_bytes, lib
+from . import _check, lib
 from . import training as _t
 
 RECORD_BYTES = 4352  # of the weight layout: 64 rows x 128 columns
@@ -49,6 +50,11 @@ def _scale_shape(rows: int, K: int):
     return (K // 128, (rows + 3) // 4 * 4, 4)
 
 
+def _scale_bytes(rows: int, K: int) -> int:
+    """engram_mx_scale_bytes; a K that is no multiple of 128 is left to the entry point's own check."""
+    return K // 128 * ((rows + 3) // 4 * 16)
+
+
 def engram_mx4_quant(x, q=None, scale=None, stream=None):
     """(q uint8 [rows, K/2], scale uint8 [K/128, ceil4(rows), 4]): bf16 rows x [rows, K] in OCP MX fp4 (E2M1, two elements
     a byte, the even column in the low half; an E8M0 scale per 32 columns in the layout of engram_mx_quant's)."""
@@ -56,17 +62,27 @@ def engram_mx4_quant(x, q=None, scale=None, stream=None):
     torch = _t.torch
     xp = on.ptr(x, "x", torch.bfloat16, 2)
     rows, K = x.shape
-    need = engram_mx_scale_bytes(rows, K)
-    if q is None:
-        q = on.empty((rows, K // 2), torch.uint8)
-    elif q.shape != (rows, K // 2):
-        raise ValueError("q must be [rows, K/2]")
+    if K < 128 or K % 128:
+        raise ValueError(f"K={K} must be a positive multiple of 128")
+    q, qp = _out(on, q, "q", (rows, K // 2), torch.uint8)
     if scale is None:
-        scale = on.empty(_scale_shape(rows, K), torch.uint8)
-    elif scale.numel() != need:
-        raise ValueError(f"scale must hold {need} bytes")
-    _check(lib().engram_mx4_quant(xp, rows, K, on.ptr(q, "q", torch.uint8), on.ptr(scale, "scale", torch.uint8), on.handle))
+        scale, sp = _out(on, None, "scale", _scale_shape(rows, K), torch.uint8)
+    elif scale.numel() != _scale_bytes(rows, K):
+        raise ValueError(f"scale must hold {_scale_bytes(rows, K)} bytes")
+    else:
+        sp = on.ptr(scale, "scale", torch.uint8)
+    _check(lib().engram_mx4_quant(xp, rows, K, qp, sp, on.handle))
     return q, scale
+
+
+def _out(on, t, name, shape, dtype):
+    """(tensor, address) of an output: the given one, checked, or a new one."""
+    if t is None:
+        t = on.empty(shape, dtype)
+        return t, t.data_ptr()
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t, on.ptr(t, name, dtype)
 
 
 def engram_mx4_weight_bytes(nout: int, K: int) -> int:
@@ -84,31 +100,28 @@ def engram_mx4_pack_weight(q, scale, out=None, stream=None):
     qp = on.ptr(q, "q", u8, 2)
     N, K = q.shape[0], 2 * q.shape[1]
     engram_mx4_weight_bytes(N, K)
-    if scale.numel() != engram_mx_scale_bytes(N, K):
+    if scale.numel() != _scale_bytes(N, K):
         raise ValueError("scale must be the MX scale array of q")
-    shape = ((N + 63) // 64, K // 128, RECORD_BYTES)
-    if out is None:
-        out = on.empty(shape, u8)
-    elif tuple(out.shape) != shape:
-        raise ValueError(f"out must be {shape}")
-    _check(lib().engram_mx4_pack_weight(qp, on.ptr(scale, "scale", u8), N, K, on.ptr(out, "out", u8), on.handle))
+    out, op = _out(on, out, "out", ((N + 63) // 64, K // 128, RECORD_BYTES), u8)
+    _check(lib().engram_mx4_pack_weight(qp, on.ptr(scale, "scale", u8), N, K, op, on.handle))
     return out
 
 
 def _operands(on, a, a_scale, w):
     """(a address, scale address, bits, weight address, T, K, rows of the weight's records)."""
     u8 = _t.torch.uint8
-    if a.dtype == _t.torch.float8_e4m3fn:
-        a = a.view(u8)
-    ap, wp = on.ptr(a, "a", u8, 2), on.ptr(w, "w", u8, 3)
-    if w.shape[2] != RECORD_BYTES:
+    ap = on.ptr(a, "a", _t.torch.float8_e4m3fn if a.dtype is _t.torch.float8_e4m3fn else u8, 2)
+    wp = on.ptr(w, "w", u8, 3)
+    groups, steps, record = w.shape
+    if record != RECORD_BYTES:
         raise ValueError("w must be packed weights (engram_mx4_pack_weight)")
-    T, K = a.shape[0], 128 * w.shape[1]
-    if a.shape[1] not in (K, K // 2):
+    T, row = a.shape
+    K = 128 * steps
+    if row != K and (row != K // 2 or a.dtype is not u8):
         raise ValueError(f"a must be [T, K={K}] (MX fp8) or [T, K/2] (MX fp4), got {tuple(a.shape)}")
-    if a_scale.numel() != engram_mx_scale_bytes(T, K):
+    if a_scale.numel() != _scale_bytes(T, K):
         raise ValueError("a_scale must be the MX scale array of a")
-    return ap, on.ptr(a_scale, "a_scale", u8), 8 if a.shape[1] == K else 4, wp, T, K, 64 * w.shape[0]
+    return ap, on.ptr(a_scale, "a_scale", u8), 8 if row == K else 4, wp, T, K, 64 * groups
 
 
 def engram_wkv_mx4(a, a_scale, w, nout=None, out=None, stream=None):
@@ -121,11 +134,8 @@ def engram_wkv_mx4(a, a_scale, w, nout=None, out=None, stream=None):
         nout = rows if out is None else out.shape[-1]
     if not rows - 64 < nout <= rows:
         raise ValueError(f"nout={nout} is not the row count of weights of {rows // 64} records")
-    if out is None:
-        out = on.empty((T, nout), _t.torch.bfloat16)
-    elif tuple(out.shape) != (T, nout):
-        raise ValueError("out must be [T, nout]")
-    _check(lib().engram_wkv_mx4(ap, sp, bits, wp, on.ptr(out, "out", _t.torch.bfloat16, 2), T, K, nout, on.handle))
+    out, op = _out(on, out, "out", (T, nout), _t.torch.bfloat16)
+    _check(lib().engram_wkv_mx4(ap, sp, bits, wp, op, T, K, nout, on.handle))
     return out
 
 
@@ -150,14 +160,11 @@ def engram_wkv_mx4_gate(a, a_scale, w, x, q_weight, k_weight, eps, value=None, d
         raise ValueError("value must be [T, >= dim] with unit column stride")
     if value.dtype != bf or value.get_device() != on.index:
         raise TypeError("value must be a bf16 tensor of the call's GPU")
-    if dot is None:
-        dot = on.empty((T, hc), f32)
-    elif dot.shape != (T, hc):
-        raise ValueError("dot must be [T, hc]")
-    _ws, sw, sn = on.workspace(workspace, engram_wkv_gate_workspace_bytes(T, hc, dim))
+    dot, dp = _out(on, dot, "dot", (T, hc), f32)
+    _ws, sw, sn = on.workspace(workspace, hc * (dim // 128) * 3 * T * 4)  # engram_wkv_gate_workspace_bytes
     _check(lib().engram_wkv_mx4_gate(ap, sp, bits, wp, on.ptr(x, "x", bf), on.ptr(q_weight, "q_weight", bf),
-                                     on.ptr(k_weight, "k_weight", bf), float(eps), value.data_ptr(), value.stride(0),
-                                     on.ptr(dot, "dot", f32), sw, sn, T, K, hc, dim, on.handle))
+                                     on.ptr(k_weight, "k_weight", bf), float(eps), value.data_ptr(), value.stride(0), dp, sw,
+                                     sn, T, K, hc, dim, on.handle))
     return value, dot
 
 
@@ -168,17 +175,11 @@ def engram_ckpt_save(x, q=None, scale=None, stream=None):
     xp = on.ptr(x, "x", torch.bfloat16)
     if x.dim() < 1:
         raise ValueError("x must have a dimension")
-    D = x.shape[-1]
-    rows, shape = _rows(x.shape), (*x.shape[:-1], (D + 31) // 32)
-    if q is None:
-        q = on.empty(x.shape, torch.int8)
-    elif q.shape != x.shape:
-        raise ValueError("q must have x's shape")
-    if scale is None:
-        scale = on.empty(shape, torch.uint8)
-    elif scale.shape != shape:
-        raise ValueError(f"scale must be {tuple(shape)}")
-    _check(lib().engram_ckpt_save(xp, rows, D, on.ptr(q, "q", torch.int8), on.ptr(scale, "scale", torch.uint8), on.handle))
+    shape = x.shape
+    D = shape[-1]
+    q, qp = _out(on, q, "q", shape, torch.int8)
+    scale, sp = _out(on, scale, "scale", (*shape[:-1], (D + 31) // 32), torch.uint8)
+    _check(lib().engram_ckpt_save(xp, math.prod(shape[:-1]), D, qp, sp, on.handle))
     return q, scale
 
 
@@ -187,22 +188,15 @@ def engram_ckpt_load(q, scale, out=None, stream=None):
     on = _t._On(stream, q, "q")
     torch = _t.torch
     qp = on.ptr(q, "q", torch.int8)
-    if q.dim() < 1 or scale.shape != (*q.shape[:-1], (q.shape[-1] + 31) // 32):
+    if q.dim() < 1:
+        raise ValueError("q must have a dimension")
+    shape = q.shape
+    *lead, D = shape
+    if scale.shape != (*lead, (D + 31) // 32):
         raise ValueError("scale must hold a byte per 32 columns of each row of q")
-    if out is None:
-        out = on.empty(q.shape, torch.bfloat16)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    _check(lib().engram_ckpt_load(qp, on.ptr(scale, "scale", torch.uint8), _rows(q.shape), q.shape[-1],
-                                  on.ptr(out, "out", torch.bfloat16), on.handle))
+    out, op = _out(on, out, "out", shape, torch.bfloat16)
+    _check(lib().engram_ckpt_load(qp, on.ptr(scale, "scale", torch.uint8), math.prod(lead), D, op, on.handle))
     return out
-
-
-def _rows(shape) -> int:
-    n = 1
-    for d in shape[:-1]:
-        n *= d
-    return n
 
 
 def _mask(on, token_mask, T):
@@ -213,11 +207,6 @@ def _mask(on, token_mask, T):
     if token_mask.dtype == _t.torch.bool:
         token_mask = token_mask.view(_t.torch.uint8)
     return on.ptr(token_mask, "token_mask", _t.torch.uint8)
-
-
-def _ckpt_shapes(T, hc, dim):
-    nb = (dim + 31) // 32
-    return (T, hc, dim), (T, hc, nb), (T, hc + 1, dim), (T, hc + 1, nb)
 
 
 def engram_gate_output_ckpt(x, kv, q_weight, k_weight, eps, token_mask=None, out=None, dot=None, checkpoint=None,
@@ -237,33 +226,24 @@ def engram_gate_output_ckpt(x, kv, q_weight, k_weight, eps, token_mask=None, out
     if q_weight.shape != (hc, dim) or k_weight.shape != (hc, dim):
         raise ValueError("q_weight and k_weight must be [hc, dim]")
     mp = _mask(on, token_mask, T)
-    if out is None:
-        out = on.empty(x.shape, bf)
-    elif out.shape != x.shape:
-        raise ValueError("out must have x's shape")
-    if dot is None:
-        dot = on.empty((T, hc), f32)
-    elif dot.shape != (T, hc):
-        raise ValueError("dot must be [T, hc]")
-    shapes = _ckpt_shapes(T, hc, dim)
-    if checkpoint is None:
-        checkpoint = GateCheckpoint(*(on.empty(s, torch.uint8 if i % 2 else torch.int8) for i, s in enumerate(shapes)))
-    c = _checkpoint(on, checkpoint, shapes)
+    out, op = _out(on, out, "out", x.shape, bf)
+    dot, dp = _out(on, dot, "dot", (T, hc), f32)
+    checkpoint, c = _checkpoint(on, checkpoint, T, hc, dim)
     _check(lib().engram_gate_output_ckpt(
         on.ptr(x, "x", bf), on.ptr(kv, "kv", bf, 2), kv.shape[1], on.ptr(q_weight, "q_weight", bf),
-        on.ptr(k_weight, "k_weight", bf), float(eps), mp, on.ptr(out, "out", bf), on.ptr(dot, "dot", f32), *c, T, hc, dim,
-        on.handle))
+        on.ptr(k_weight, "k_weight", bf), float(eps), mp, op, dp, *c, T, hc, dim, on.handle))
     return out, dot, checkpoint
 
 
-def _checkpoint(on, checkpoint, shapes):
-    """The addresses of a checkpoint's four tensors."""
-    names = GateCheckpoint._fields
-    for t, s, name in zip(checkpoint, shapes, names):
-        if tuple(t.shape) != s:
-            raise ValueError(f"checkpoint.{name} must be {s}, got {tuple(t.shape)}")
-    return [on.ptr(t, f"checkpoint.{name}", _t.torch.uint8 if i % 2 else _t.torch.int8)
-            for i, (t, name) in enumerate(zip(checkpoint, names))]
+def _checkpoint(on, given, T, hc, dim):
+    """(GateCheckpoint, its addresses): the given one, checked, or a new one."""
+    i8, u8, nb = _t.torch.int8, _t.torch.uint8, (dim + 31) // 32
+    x, xs, kv, kvs = given if given is not None else (None, None, None, None)
+    x, p0 = _out(on, x, "checkpoint.x", (T, hc, dim), i8)
+    xs, p1 = _out(on, xs, "checkpoint.x_scale", (T, hc, nb), u8)
+    kv, p2 = _out(on, kv, "checkpoint.kv", (T, hc + 1, dim), i8)
+    kvs, p3 = _out(on, kvs, "checkpoint.kv_scale", (T, hc + 1, nb), u8)
+    return (given if given is not None else GateCheckpoint(x, xs, kv, kvs)), (p0, p1, p2, p3)
 
 
 def engram_gate_output_backward_ckpt(checkpoint, q_weight, k_weight, eps, dot, dout, token_mask=None, dx=None, dkv=None,
@@ -277,31 +257,22 @@ def engram_gate_output_backward_ckpt(checkpoint, q_weight, k_weight, eps, dot, d
         raise ValueError("dout must be [T, hc, dim] (or [B, L, hc, dim])")
     hc, dim = dout.shape[-2:]
     T = dout.numel() // (hc * dim) if hc * dim else 0
-    c = _checkpoint(on, checkpoint, _ckpt_shapes(T, hc, dim))
+    if checkpoint is None or any(t is None for t in checkpoint):
+        raise ValueError("the gradient needs the checkpoint of engram_gate_output_ckpt")
+    _, c = _checkpoint(on, checkpoint, T, hc, dim)
     if q_weight.shape != (hc, dim) or k_weight.shape != (hc, dim):
         raise ValueError("q_weight and k_weight must be [hc, dim]")
     if dot.shape != (T, hc):
         raise ValueError("dot must be [T, hc]")
     mp = _mask(on, token_mask, T)
-    if dx is None:
-        dx = on.empty(dout.shape, bf)
-    elif dx.shape != dout.shape:
-        raise ValueError("dx must have dout's shape")
-    if dkv is None:
-        dkv = on.empty((T, (hc + 1) * dim), bf)
-    elif dkv.shape != (T, (hc + 1) * dim):
-        raise ValueError("dkv must be [T, (hc+1)*dim]")
-    if dq is None:
-        dq = on.empty((hc, dim), f32)
-    if dk is None:
-        dk = on.empty((hc, dim), f32)
-    if dq.shape != (hc, dim) or dk.shape != (hc, dim):
-        raise ValueError("dq and dk must be [hc, dim]")
+    dx, xp = _out(on, dx, "dx", dout.shape, bf)
+    dkv, kvp = _out(on, dkv, "dkv", (T, (hc + 1) * dim), bf)
+    dq, qp = _out(on, dq, "dq", (hc, dim), f32)
+    dk, kp = _out(on, dk, "dk", (hc, dim), f32)
     _ws, wp, wn = on.workspace(workspace, _t.engram_gate_output_backward_workspace_bytes(T, hc, dim))
     _check(lib().engram_gate_output_backward_ckpt(
         *c, on.ptr(q_weight, "q_weight", bf), on.ptr(k_weight, "k_weight", bf), float(eps), on.ptr(dot, "dot", f32),
-        on.ptr(dout, "dout", bf), mp, on.ptr(dx, "dx", bf), on.ptr(dkv, "dkv", bf), on.ptr(dq, "dq", f32),
-        on.ptr(dk, "dk", f32), wp, wn, T, hc, dim, on.handle))
+        on.ptr(dout, "dout", bf), mp, xp, kvp, qp, kp, wp, wn, T, hc, dim, on.handle))
     return dx, dkv, dq, dk
 
 

@@ -68,7 +68,7 @@ class _On:
             if not like.is_cuda:
                 raise ValueError(f"{name} must be a GPU tensor")
             self.index = like.get_device()
-            if self.index != torch.cuda.current_device():
+            if self.index != torch._C._cuda_getDevice():
                 raise ValueError(f"{name} is on GPU {self.index}, the current device is {torch.cuda.current_device()}")
         current = torch._C._cuda_getCurrentRawStream(self.index)
         self.handle, self.side = current, None

@@ -46,8 +46,8 @@ struct Mx4Args {
     const uint16_t* x;   // [M, hc, dim] bf16
     const uint16_t* q;   // [hc, dim] bf16
     const uint16_t* k;
-    float* part;         // [hc][dim/128][3][M]: per 128 columns sum(h w key), sum(key^2), sum(h^2)
-    int dim, n_key;
+    float* part;         // [hc * dim / 128][3][M]: per 128 columns sum(h w key), sum(key^2), sum(h^2)
+    int n_key;
 };
 
 __device__ inline uint32_t pack_bf16(float lo, float hi) {
@@ -84,12 +84,13 @@ __device__ inline f32x4 mfma(const i32x4& w, int sw, const AFrag<kA8>& a, int sa
                                                             kA8 ? kFp8 : kFp4, kSel, sw, 0, sa);
 }
 
-// ---- tiles: a workgroup of four waves has 16 MI tokens x 256 columns, two workgroups a CU, so that one's stores, sums and first
-// loads run under the other's matrix instructions.  A wave has all tokens and 64 columns, MI x 4 blocks of 16 x 16.  The token
-// rows come through LDS, 128 bytes of each (128 columns in 8 bits, 256 in 4) a stage, in two stages, by direct-to-LDS loads (rows
-// past M are outside their resource and read as zero); the weights go from memory to the registers, a step ahead, each read by
-// one wave only.  What bounds it is the path of the loads through the CU's address unit (busy 84 % of the clocks where two waves
-// of a 256 x 128 tile read the same weights, at 64 bytes of a row a load), so as few and as long runs as the registers allow.
+// ---- tiles: a workgroup of NW waves has 16 MI tokens x 64 NW columns, two waves a SIMD, so that one workgroup's stores, sums
+// and first loads run under another's matrix instructions.  A wave has all tokens and 64 columns, MI x 4 blocks of 16 x 16.  The
+// token rows come through LDS, 128 bytes of each (128 columns in 8 bits, 256 in 4) a stage, by direct-to-LDS loads (rows past M
+// are outside their resource and read as zero); the weights go from memory to the registers, kSets steps ahead, each read by one
+// wave only.  What bounds large products is the path of the loads through the CU's address unit (busy 84 % of the clocks where
+// two waves of a 256 x 128 tile read the same weights, at 64 bytes of a row a load), so as few and as long runs as the registers
+// allow; a few tokens are bound by the weights' latency, so as many steps in flight as they allow.
 //
 // LDS rows: the 16-byte piece c of a row at slot c ^ (row / 2) % 8: neighbouring lanes' pieces lie in different banks.
 constexpr int kBufferWord3 = 0x00020000;
@@ -107,21 +108,21 @@ __device__ inline int load4(__amdgpu_buffer_rsrc_t r, uint32_t at) {
     return static_cast<int>(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
 }
 
-template <bool kA8, int MI, int kSets, bool kGate>
+template <bool kA8, int MI, int NW, int kSets, bool kGate>
 __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int tiles_n) {
-    constexpr int BM = 16 * MI, BN = 256;
+    constexpr int BM = 16 * MI, BN = 64 * NW;
     constexpr int kSub = kA8 ? 1 : 2;                       // steps of a stage
     constexpr int kScales = BM * 128;                       // a stage: its rows, then a word per row and step
     constexpr int kScaleRows = BM > 64 ? BM : 64;           // (a load of them writes 64 words)
     constexpr int kStageBytes = kScales + kSub * kScaleRows * 4;
-    constexpr int kRowLoads = (BM + 31) / 32;               // per wave and stage: 8 rows each
-    constexpr int kScaleLoads = (kSub * kScaleRows + 255) / 256;  // 64 rows of a step each
+    constexpr int kRowLoads = (BM + 8 * NW - 1) / (8 * NW);  // per wave and stage: 8 rows each
+    constexpr int kScaleLoads = (kSub * kScaleRows + BN - 1) / BN;  // 64 rows of a step each
     constexpr int kLoads = kRowLoads + kScaleLoads;
     constexpr int kWLoads = 5;
     constexpr int kStages = kSets > 1 ? kSets / kSub + 1 : 2;
     constexpr int kRing = kStages * kStageBytes;
     constexpr int kWaveBytes = BM * 128;                    // a wave's part of the tile as bf16, behind the last step
-    constexpr int kLds = kRing > 4 * kWaveBytes ? kRing : 4 * kWaveBytes;
+    constexpr int kLds = kRing > NW * kWaveBytes ? kRing : NW * kWaveBytes;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -162,7 +163,7 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
                                                      voff[q & 1] + static_cast<uint32_t>(q * 8 * row_bytes),
                                                      stage * 128, 0, 0);
         } else {
-            const int u = (wave + 4 * (q - kRowLoads)) * 64 % (kSub * kScaleRows);  // (some waves load the same here too)
+            const int u = (wave + NW * (q - kRowLoads)) * 64 % (kSub * kScaleRows);  // (some waves load the same here too)
             const int s = stage * kSub + u / kScaleRows;
             const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
                 const_cast<uint8_t*>(p.as + (static_cast<int64_t>(s) * p.M4 + m0) * 4), 0, s < S ? scale_bytes : 0, kBufferWord3);
@@ -398,10 +399,10 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
     }
 }
 
-template <bool kA8, int MI, int kSets, bool kGate>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void mx4_tile_kernel(Mx4Args p, int tiles_m,
-                                                                                                 int tiles_n) {
-    mx4_tile_body<kA8, MI, kSets, kGate>(p, tiles_m, tiles_n);
+template <bool kA8, int MI, int NW, int kSets, bool kGate>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void mx4_tile_kernel(Mx4Args p, int tiles_m,
+                                                                                                     int tiles_n) {
+    mx4_tile_body<kA8, MI, NW, kSets, kGate>(p, tiles_m, tiles_n);
 }
 
 // ---- quantisation of bf16 rows: a thread has 8 consecutive columns, the 4 threads of a block find its largest magnitude (as
@@ -454,19 +455,30 @@ __global__ __launch_bounds__(256) void mx4_pack_kernel(const uint8_t* q, const u
 
 constexpr int64_t kMostGroups = (1 << 23) - 1;  // workgroups of a launch: its threads have to stay under 2^32
 
+template <bool kA8, int MI, int NW, int kSets, bool kGate>
+int launch_tiles(const Mx4Args& p, hipStream_t stream, const char* what) {
+    const int64_t tiles_m = (p.M + 16 * MI - 1) / (16 * MI);
+    const int tiles_n = (p.N + 64 * NW - 1) / (64 * NW);
+    if (tiles_m > kMostGroups / tiles_n) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
+    hipLaunchKernelGGL((mx4_tile_kernel<kA8, MI, NW, kSets, kGate>), dim3(static_cast<unsigned>(tiles_m * tiles_n)),
+                       dim3(64 * NW), 0, stream, p, static_cast<int>(tiles_m), tiles_n);
+    return check_launch(what);
+}
+
+// The tile: 128 tokens where that makes one and a half tiles or more for every CU; 64, then 32, where it makes one for half of
+// them and is more than half filled; else 16, by two waves.  A small tile has more steps of weights in flight, and few tiles
+// take the latency of their chain of steps; many are bound by what they read.  8-bit rows of 1,536 columns, us at 16 / 32 / 64
+// / 128 tokens a tile: 1 x 25,600 5.8 / 6.1 / 7.7 / 11.4; 64 x 25,600 8.3 / 7.0 / 8.3 / 11.8; 128 13.0 / 9.4 / 8.4 / 12.2; and
+// at 16 / 64 / 128: 256 20.6 / 12.1 / 12.5; 384 28.6 / 18.3 / 19.4; 512 36 / 22.7 / 19.8; 1,024 x 2,560 10.4 / 8.1 / 12.0.
 template <bool kA8, bool kGate>
 int launch(const Mx4Args& p, hipStream_t stream, const char* what) {
-    const int mi = p.M <= 32 ? 1 : p.M <= 128 ? 2 : p.M <= 256 ? 4 : 8;
-    const int64_t tiles_m = (p.M + 16 * mi - 1) / (16 * mi);
-    const int tiles_n = (p.N + 255) / 256;
-    if (tiles_m > kMostGroups / tiles_n) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
-    const dim3 grid(static_cast<unsigned>(tiles_m * tiles_n)), block(256);
-    const int tm = static_cast<int>(tiles_m);
-    if (mi == 1) hipLaunchKernelGGL((mx4_tile_kernel<kA8, 1, 4, kGate>), grid, block, 0, stream, p, tm, tiles_n);
-    else if (mi == 2) hipLaunchKernelGGL((mx4_tile_kernel<kA8, 2, 4, kGate>), grid, block, 0, stream, p, tm, tiles_n);
-    else if (mi == 4) hipLaunchKernelGGL((mx4_tile_kernel<kA8, 4, 2, kGate>), grid, block, 0, stream, p, tm, tiles_n);
-    else hipLaunchKernelGGL((mx4_tile_kernel<kA8, 8, 1, kGate>), grid, block, 0, stream, p, tm, tiles_n);
-    return check_launch(what);
+    constexpr int kCUs = 256;
+    const int64_t tiles_n = (p.N + 255) / 256;
+    auto tiles = [&](int tokens) { return (p.M + tokens - 1) / tokens * tiles_n; };
+    if (p.M > 64 && 2 * tiles(128) >= 3 * kCUs) return launch_tiles<kA8, 8, 4, 1, kGate>(p, stream, what);
+    if (p.M > 32 && 2 * tiles(64) >= kCUs) return launch_tiles<kA8, 4, 4, 2, kGate>(p, stream, what);
+    if (p.M > 16 && 2 * tiles(32) >= kCUs) return launch_tiles<kA8, 2, 4, 4, kGate>(p, stream, what);
+    return launch_tiles<kA8, 1, 2, 4, kGate>(p, stream, what);
 }
 
 constexpr int kMaxK = 1 << 20, kMaxN = 1 << 22;
@@ -577,7 +589,6 @@ extern "C" int engram_wkv_mx4_gate(const uint8_t* a, const uint8_t* a_scale, int
     p.q = q_weight;
     p.k = k_weight;
     p.part = static_cast<float*>(workspace);
-    p.dim = dim;
     p.n_key = hc * dim;
     const int rc = a_bits == 8 ? launch<true, true>(p, as_stream(stream), what) : launch<false, true>(p, as_stream(stream), what);
     if (rc != ENGRAM_OK) return rc;

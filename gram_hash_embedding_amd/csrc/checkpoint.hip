@@ -1,6 +1,6 @@
 // 8-bit checkpoints of the rows that a backward pass reads again, in OCP MXINT8: 32 consecutive columns of a row share an
-// E8M0 scale, elements are integers in [-127, 127], in 64ths of the scale (mx.h).  A row's scales lie together, [rows][ceil(D / 32)], the last
-// block of a row may be shorter.
+// E8M0 scale, elements are integers in [-127, 127], in 64ths of the scale (mx.h).  A row's scales lie together, [rows][ceil(D
+// / 32)], the last block of a row may be shorter.
 //
 //   engram_ckpt_save        -- bf16 rows -> MXINT8
 //   engram_ckpt_load        -- MXINT8 -> bf16 rows (exact: an element has 7 bits, bf16 holds 8)
@@ -16,7 +16,6 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int64_t kMostGroups = (1 << 23) - 1;  // workgroups of a launch: its threads have to stay under 2^32
 
 // Four lanes hold a block of 32 (piece j: columns 8 j .. 8 j + 7); lanes without a piece pass zeros and `ok` false.  Every lane
 // of the wave takes part.
@@ -32,7 +31,7 @@ __device__ inline void save_piece(const u32x4& v, bool ok, int8_t* q, uint8_t* s
 __global__ __launch_bounds__(kThreads) void ckpt_save_kernel(const uint16_t* x, int64_t rows, int chunks, int8_t* q,
                                                              uint8_t* scale) {
     const int blocks = (chunks + 3) / 4;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t i = group_index() * kThreads + threadIdx.x;
     const int64_t r = i / (4 * blocks);
     const int j = static_cast<int>(i - r * (4 * blocks));
     const bool ok = r < rows && j < chunks;
@@ -43,7 +42,7 @@ __global__ __launch_bounds__(kThreads) void ckpt_save_kernel(const uint16_t* x, 
 
 __global__ __launch_bounds__(kThreads) void ckpt_load_kernel(const int8_t* q, const uint8_t* scale, int64_t rows, int chunks,
                                                              uint16_t* x) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t i = group_index() * kThreads + threadIdx.x;
     const int64_t r = i / chunks;
     const int j = static_cast<int>(i - r * chunks);
     if (r >= rows) return;
@@ -80,8 +79,9 @@ template <int P>
 __global__ __launch_bounds__(kThreads) void gate_output_ckpt_kernel(CkptArgs a) {
     __shared__ float part[kWaves][3];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t tc = blockIdx.x;  // token * hc + copy
+    const int64_t tc = group_index();  // token * hc + copy
     const int64_t t = tc / a.hc;
+    if (t >= a.T) return;
     const int c = static_cast<int>(tc - t * a.hc);
     const int chunks = a.dim / 8, blocks = (chunks + 3) / 4;
     const u32x4* q = reinterpret_cast<const u32x4*>(a.q + static_cast<int64_t>(c) * a.dim);
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(kThreads) void gate_output_ckpt_kernel(CkptArgs a) 
 const char* bad_rows(int64_t rows, int32_t D) {
     if (rows < 0) return "rows < 0";
     if (D < 8 || D % 8 != 0 || D > (1 << 20)) return "D must be a multiple of 8 in [8, 2^20]";
-    if (rows > kMostGroups * kThreads / (4 * ((D + 31) / 32))) return "too many rows";
+    if (rows > (1ll << 48) / ((D + 31) / 32 * 32)) return "too many rows";
     return nullptr;
 }
 
@@ -172,7 +172,7 @@ extern "C" int engram_ckpt_save(const uint16_t* x, int64_t rows, int32_t D, int8
     if (!x || !q || !scale) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
     if (!aligned(x, 16) || !aligned(q, 8)) return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
     const int64_t blocks = (rows * 4 * ((D + 31) / 32) + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL(ckpt_save_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, as_stream(stream), x, rows,
+    hipLaunchKernelGGL(ckpt_save_kernel, group_grid(blocks), dim3(kThreads), 0, as_stream(stream), x, rows,
                        D / 8, q, scale);
     return check_launch(what);
 }
@@ -184,7 +184,7 @@ extern "C" int engram_ckpt_load(const int8_t* q, const uint8_t* scale, int64_t r
     if (!x || !q || !scale) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
     if (!aligned(x, 16) || !aligned(q, 8)) return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
     const int64_t blocks = (rows * (D / 8) + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL(ckpt_load_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, as_stream(stream), q, scale,
+    hipLaunchKernelGGL(ckpt_load_kernel, group_grid(blocks), dim3(kThreads), 0, as_stream(stream), q, scale,
                        rows, D / 8, x);
     return check_launch(what);
 }
@@ -200,7 +200,7 @@ extern "C" int engram_gate_output_ckpt(const uint16_t* x, const uint16_t* kv, in
         return fail(ENGRAM_EINVAL, "%s: dim=%d must be a multiple of 8 in [8, 8192]", what, dim);
     if (ld_kv < static_cast<int64_t>(hc + 1) * dim || ld_kv % 8 != 0)
         return fail(ENGRAM_EINVAL, "%s: ld_kv=%lld must be >= (hc+1)*dim and a multiple of 8", what, (long long)ld_kv);
-    if (T > kMostGroups / hc) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
+    if (T > (1ll << 38) / hc) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
     if (T == 0) return ENGRAM_OK;
     if (!x || !kv || !q_weight || !k_weight || !out || !dot || !x_q || !x_scale || !kv_q || !kv_scale)
         return fail(ENGRAM_EINVAL, "%s: null pointer", what);
@@ -226,7 +226,7 @@ extern "C" int engram_gate_output_ckpt(const uint16_t* x, const uint16_t* kv, in
     a.T = T;
     a.hc = hc;
     a.dim = dim;
-    const dim3 grid(static_cast<unsigned>(T * hc)), block(kThreads);
+    const dim3 grid = group_grid(T * hc), block(kThreads);
     const int pieces = (dim / 8 + kThreads - 1) / kThreads;
     if (pieces == 1) hipLaunchKernelGGL(gate_output_ckpt_kernel<1>, grid, block, 0, as_stream(stream), a);
     else if (pieces == 2) hipLaunchKernelGGL(gate_output_ckpt_kernel<2>, grid, block, 0, as_stream(stream), a);

@@ -18,6 +18,15 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
+// A grid of `groups` workgroups (at most kMostGroups) of up to 256 threads, along x as far as its threads stay below 2^32
+// and then along y, and a workgroup's index in it, which can be groups or more.
+constexpr int64_t kMaxGroupsX = 1ll << 23, kMostGroups = kMaxGroupsX * 65535;
+inline dim3 group_grid(int64_t groups) {
+    const int64_t x = groups < kMaxGroupsX ? groups : kMaxGroupsX;
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>((groups + x - 1) / x));
+}
+__device__ inline int64_t group_index() { return blockIdx.y * kMaxGroupsX + blockIdx.x; }
+
 // 16-byte vector of 32-bit words: the unit of every wide global access.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 

@@ -128,12 +128,13 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r = lane & 15;
     const int S = p.steps;
-    // the workgroup's tile: an XCD (workgroups blockIdx % 8) takes a contiguous run of the order, kGroupM tile rows deep
+    // the workgroup's tile: an XCD (workgroups % 8) takes a contiguous run of the order, kGroupM tile rows deep
     int64_t m0;
     int n0;
     {
         const int64_t n = static_cast<int64_t>(tiles_m) * tiles_n;
-        const int64_t pid = blockIdx.x, xcd = pid % kXcds, per = n / kXcds, rem = n % kXcds;
+        const int64_t pid = group_index(), xcd = pid % kXcds, per = n / kXcds, rem = n % kXcds;
+        if (pid >= n) return;
         const int64_t at = xcd * per + min(xcd, rem) + pid / kXcds;
         const int64_t in_group = static_cast<int64_t>(kGroupM) * tiles_n;
         const int64_t group = at / in_group;
@@ -412,7 +413,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // checked on every bf16 pattern.  A block with an infinity or a NaN, which E2M1 has not, takes the NaN scale 0xFF and zeros.
 __global__ __launch_bounds__(256) void mx4_quant_kernel(const uint16_t* x, int64_t rows, int K, int64_t rows4, uint8_t* q,
                                                         uint8_t* scale) {
-    const int64_t gid = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t gid = group_index() * 256 + threadIdx.x;
     const int per_row = K / 8;
     const int64_t r = gid / per_row;
     const int c8 = static_cast<int>(gid - r * per_row);
@@ -436,32 +437,31 @@ __global__ __launch_bounds__(256) void mx4_quant_kernel(const uint16_t* x, int64
 // a workgroup per record
 __global__ __launch_bounds__(256) void mx4_pack_kernel(const uint8_t* q, const uint8_t* scale, int N, int steps, int64_t rows4,
                                                        uint8_t* packed) {
-    const int s = static_cast<int>(blockIdx.x % steps), group = static_cast<int>(blockIdx.x / steps);
-    uint8_t* rec = packed + static_cast<int64_t>(blockIdx.x) * kRecord;
+    const int64_t at = group_index(), group = at / steps;
+    if (group * kGroupRows >= N) return;
+    const int s = static_cast<int>(at - group * steps);
+    uint8_t* rec = packed + at * kRecord;
     const int t = threadIdx.x;
     {
         const int j = t >> 6, c = (t >> 4) & 3, r = t & 15;
-        const int64_t n = static_cast<int64_t>(group) * kGroupRows + 16 * j + r;
+        const int64_t n = group * kGroupRows + 16 * j + r;
         u32x4 v = {0, 0, 0, 0};
         if (n < N) v = *reinterpret_cast<const u32x4*>(q + (n * steps + s) * 64 + 16 * c);
         *reinterpret_cast<u32x4*>(rec + 16 * t) = v;
     }
     {
         const int c = t >> 6, r = (t >> 2) & 15, j = t & 3;
-        const int64_t n = static_cast<int64_t>(group) * kGroupRows + 16 * j + r;
+        const int64_t n = group * kGroupRows + 16 * j + r;
         rec[4096 + t] = n < N ? scale[(static_cast<int64_t>(s) * rows4 + n) * 4 + c] : 0;
     }
 }
-
-constexpr int64_t kMostGroups = (1 << 23) - 1;  // workgroups of a launch: its threads have to stay under 2^32
 
 template <bool kA8, int MI, int NW, int kSets, bool kGate>
 int launch_tiles(const Mx4Args& p, hipStream_t stream, const char* what) {
     const int64_t tiles_m = (p.M + 16 * MI - 1) / (16 * MI);
     const int tiles_n = (p.N + 64 * NW - 1) / (64 * NW);
-    if (tiles_m > kMostGroups / tiles_n) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
-    hipLaunchKernelGGL((mx4_tile_kernel<kA8, MI, NW, kSets, kGate>), dim3(static_cast<unsigned>(tiles_m * tiles_n)),
-                       dim3(64 * NW), 0, stream, p, static_cast<int>(tiles_m), tiles_n);
+    hipLaunchKernelGGL((mx4_tile_kernel<kA8, MI, NW, kSets, kGate>), group_grid(tiles_m * tiles_n), dim3(64 * NW), 0,
+                       stream, p, static_cast<int>(tiles_m), tiles_n);
     return check_launch(what);
 }
 
@@ -489,6 +489,7 @@ const char* bad_shape(int64_t T, int32_t a_bits, int32_t K, int32_t N) {
     if (a_bits != 4 && a_bits != 8) return "a_bits must be 4 or 8";
     if (K < kStepCols || K % kStepCols != 0 || K > kMaxK) return "K must be a multiple of 128 in [128, 2^20]";
     if (N < 8 || N % 8 != 0 || N > kMaxN) return "the columns must be a multiple of 8 in [8, 2^22]";
+    if (T > 1ll << 34 || T > (1ll << 48) / N) return "too many tokens";
     return nullptr;
 }
 
@@ -500,14 +501,14 @@ using namespace engram;
 extern "C" int engram_mx4_quant(const uint16_t* x, int64_t rows, int32_t K, uint8_t* q, uint8_t* scale, void* stream) {
     const char* what = "engram_mx4_quant";
     if (rows < 0) return fail(ENGRAM_EINVAL, "%s: rows < 0", what);
-    if (K < kStepCols || K % kStepCols != 0)
-        return fail(ENGRAM_EINVAL, "%s: K=%d must be a positive multiple of %d", what, K, kStepCols);
+    if (K < kStepCols || K % kStepCols != 0 || K > kMaxK)
+        return fail(ENGRAM_EINVAL, "%s: K=%d must be a multiple of 128 in [128, 2^20]", what, K);
+    if (rows > (1ll << 48) / K) return fail(ENGRAM_EINVAL, "%s: too many rows", what);
     if (rows == 0) return ENGRAM_OK;
     if (!x || !q || !scale) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
     if (!aligned(x, 16) || !aligned(q, 4)) return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
-    if (rows > kMostGroups * 256 / (K / 8)) return fail(ENGRAM_EINVAL, "%s: too many rows", what);
     const int64_t blocks = (rows * (K / 8) + 255) / 256;
-    hipLaunchKernelGGL(mx4_quant_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, as_stream(stream), x, rows, K,
+    hipLaunchKernelGGL(mx4_quant_kernel, group_grid(blocks), dim3(256), 0, as_stream(stream), x, rows, K,
                        (rows + 3) / 4 * 4, q, scale);
     return check_launch(what);
 }
@@ -524,8 +525,7 @@ extern "C" int engram_mx4_pack_weight(const uint8_t* q, const uint8_t* scale, in
     if (!q || !scale || !packed) return fail(ENGRAM_EINVAL, "%s: null pointer", what);
     if (!aligned(q, 16) || !aligned(packed, 16)) return fail(ENGRAM_EINVAL, "%s: misaligned pointer", what);
     const int64_t records = engram_mx4_weight_bytes(Nout, K) / kRecord;
-    if (records > kMostGroups) return fail(ENGRAM_EINVAL, "%s: weights too large", what);
-    hipLaunchKernelGGL(mx4_pack_kernel, dim3(static_cast<unsigned>(records)), dim3(256), 0, as_stream(stream), q, scale, Nout,
+    hipLaunchKernelGGL(mx4_pack_kernel, group_grid(records), dim3(256), 0, as_stream(stream), q, scale, Nout,
                        K / kStepCols, (static_cast<int64_t>(Nout) + 3) / 4 * 4, packed);
     return check_launch(what);
 }
@@ -563,6 +563,7 @@ extern "C" int engram_wkv_mx4_gate(const uint8_t* a, const uint8_t* a_scale, int
         return fail(ENGRAM_EINVAL, "%s: (hc + 1) * dim = %lld exceeds 2^22", what, static_cast<long long>(hc + 1) * dim);
     const int N = (hc + 1) * dim;
     if (const char* bad = bad_shape(T, a_bits, K, N)) return fail(ENGRAM_EINVAL, "%s: %s", what, bad);
+    if (T > (1ll << 31) / hc) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
     if (ld_value < dim || ld_value % 8 != 0)
         return fail(ENGRAM_EINVAL, "%s: ld_value=%lld must be >= dim and a multiple of 8", what, (long long)ld_value);
     const int64_t need = engram_wkv_gate_workspace_bytes(T, hc, dim);

@@ -552,7 +552,7 @@ int engram_wkv_mx_gate(const uint8_t* a, const uint8_t* a_scale, const uint8_t* 
  * x      uint16 [rows, K] bf16 bits; 16-byte aligned
  * q      uint8 [rows, K/2], out; 4-byte aligned (16-byte where the product reads it)
  * scale  uint8, engram_mx_scale_bytes(rows, K) bytes in the MX scale layout, out
- * Limits: K >= 128 and K % 128 == 0; 0 <= rows, rows * K <= 2^34.
+ * Limits: K a multiple of 128 in [128, 2^20]; 0 <= rows, rows * K <= 2^48.
  */
 int engram_mx4_quant(const uint16_t* x, int64_t rows, int32_t K, uint8_t* q, uint8_t* scale, void* stream);
 
@@ -565,7 +565,7 @@ int64_t engram_mx4_weight_bytes(int32_t Nout, int32_t K);
  * q       uint8 [Nout, K/2] (engram_mx4_quant's); 16-byte aligned
  * scale   their MX scales
  * packed  uint8, engram_mx4_weight_bytes(Nout, K) bytes, out; 16-byte aligned
- * Limits: as engram_wkv_mx4; at most 2^23 records.
+ * Limits: as engram_wkv_mx4.
  */
 int engram_mx4_pack_weight(const uint8_t* q, const uint8_t* scale, int32_t Nout, int32_t K, uint8_t* packed, void* stream);
 
@@ -580,8 +580,7 @@ int engram_mx4_pack_weight(const uint8_t* q, const uint8_t* scale, int32_t Nout,
  * a_scale  MX scales of a (T rows); 16-byte aligned
  * w        the packed weights (engram_mx4_pack_weight's); 16-byte aligned
  * kv       uint16 [T, Nout] bf16 bits, out: the hc keys then the value, as engram_wkv; 16-byte aligned
- * Limits: T >= 0; K a multiple of 128 in [128, 2^20]; Nout a multiple of 8 in [8, 2^22]; fewer than 2^31 tiles of
- * 256 x 256 outputs.
+ * Limits: 0 <= T <= 2^34, T * Nout <= 2^48; K a multiple of 128 in [128, 2^20]; Nout a multiple of 8 in [8, 2^22].
  */
 int engram_wkv_mx4(const uint8_t* a, const uint8_t* a_scale, int32_t a_bits, const uint8_t* w, uint16_t* kv, int64_t T,
                    int32_t K, int32_t Nout, void* stream);
@@ -601,8 +600,8 @@ int engram_wkv_mx4(const uint8_t* a, const uint8_t* a_scale, int32_t a_bits, con
  * x, q_weight, k_weight, eps, value, ld_value, dot  as engram_wkv_gate
  * workspace  at least engram_wkv_gate_workspace_bytes(T, hc, dim) bytes, 16-byte aligned, caller-owned scratch (no
  *            initialisation needed); two calls in flight at once must not share it
- * Limits: as engram_wkv_mx4; 1 <= hc <= 64; dim >= 256 and dim % 256 == 0; (hc+1)*dim <= 2^22; ld_value >= dim,
- * ld_value % 8 == 0.  Too small a workspace -> ENGRAM_ERANGE.
+ * Limits: as engram_wkv_mx4; 1 <= hc <= 64; T * hc <= 2^31; dim >= 256 and dim % 256 == 0; (hc+1)*dim <= 2^22;
+ * ld_value >= dim, ld_value % 8 == 0.  Too small a workspace -> ENGRAM_ERANGE.
  */
 int engram_wkv_mx4_gate(const uint8_t* a, const uint8_t* a_scale, int32_t a_bits, const uint8_t* w, const uint16_t* x,
                         const uint16_t* q_weight, const uint16_t* k_weight, float eps, uint16_t* value, int64_t ld_value,
@@ -803,14 +802,14 @@ int engram_clip_grads(int32_t tensors, const void* const* grads, void* const* ou
  *
  * engram_ckpt_save -- bf16 rows to checkpoints: s - 127 = floor(log2 amax) of the block, at least -127 (s = 0 for an all-zero
  * or subnormal block); the integer nearest to 64 x 2^(127-s), ties to even, kept in [-127, 127]: no element is off by more
- * than half a unit, 2^-7 of the block's amax at most (amax reaches 127.5 units, not 128).  A block that holds an infinity or a NaN takes the scale
- * 0xFF and zeros, and is read back as NaN.
+ * than half a unit, 2^-7 of the block's amax at most (amax reaches 127.5 units, not 128).  A
+ * block that holds an infinity or a NaN takes the scale 0xFF and zeros, and is read back as NaN.
  * engram_ckpt_load -- checkpoints to bf16 rows, exactly the values they stand for.
  *
  * x      uint16 [rows, D] bf16 bits; 16-byte aligned
  * q      int8 [rows, D]; 8-byte aligned
  * scale  uint8 [rows, ceil(D/32)]
- * Limits: D a multiple of 8 in [8, 2^20]; 0 <= rows, rows * (D up to a multiple of 32) <= 2^34.
+ * Limits: D a multiple of 8 in [8, 2^20]; 0 <= rows, rows * (D up to a multiple of 32) <= 2^48.
  */
 int engram_ckpt_save(const uint16_t* x, int64_t rows, int32_t D, int8_t* q, uint8_t* scale, void* stream);
 int engram_ckpt_load(const int8_t* q, const uint8_t* scale, int64_t rows, int32_t D, uint16_t* x, void* stream);
@@ -827,7 +826,7 @@ int engram_ckpt_load(const int8_t* q, const uint8_t* scale, int64_t rows, int32_
  * dot       float32 [T, hc], out (kept for the gradient); 4-byte aligned
  * x_q       int8 [T, hc, dim], out; 8-byte aligned;     x_scale   uint8 [T, hc, ceil(dim/32)], out
  * kv_q      int8 [T, hc+1, dim], out; 8-byte aligned;   kv_scale  uint8 [T, hc+1, ceil(dim/32)], out
- * Limits: T * hc <= 2^23; 1 <= hc <= 64; 8 <= dim <= 8192 and dim % 8 == 0.
+ * Limits: T * hc <= 2^38; 1 <= hc <= 64; 8 <= dim <= 8192 and dim % 8 == 0.
  */
 int engram_gate_output_ckpt(const uint16_t* x, const uint16_t* kv, int64_t ld_kv, const uint16_t* q_weight,
                             const uint16_t* k_weight, float eps, const uint8_t* token_mask, uint16_t* out, float* dot,

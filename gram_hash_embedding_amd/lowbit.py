@@ -77,12 +77,20 @@ def engram_mx4_quant(x, q=None, scale=None, stream=None):
 
 def _out(on, t, name, shape, dtype):
     """(tensor, address) of an output: the given one, checked, or a new one."""
-    if t is None:
-        t = on.empty(shape, dtype)
+    if t is None:  # (sizes as arguments are parsed faster than as a tuple)
+        t = _t.torch.empty(*shape, dtype=dtype, device=on.index) if on.side is None else on.empty(shape, dtype)
         return t, t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     return t, on.ptr(t, name, dtype)
+
+
+def _out_like(on, t, name, like, dtype):
+    """_out of the shape of `like`, a contiguous tensor of the call's device."""
+    if t is None and on.side is None:
+        t = _t.torch.empty_like(like, dtype=dtype)
+        return t, t.data_ptr()
+    return _out(on, t, name, like.shape, dtype)
 
 
 def engram_mx4_weight_bytes(nout: int, K: int) -> int:
@@ -177,7 +185,7 @@ def engram_ckpt_save(x, q=None, scale=None, stream=None):
         raise ValueError("x must have a dimension")
     shape = x.shape
     D = shape[-1]
-    q, qp = _out(on, q, "q", shape, torch.int8)
+    q, qp = _out_like(on, q, "q", x, torch.int8)
     scale, sp = _out(on, scale, "scale", (*shape[:-1], (D + 31) // 32), torch.uint8)
     _check(lib().engram_ckpt_save(xp, math.prod(shape[:-1]), D, qp, sp, on.handle))
     return q, scale
@@ -194,7 +202,7 @@ def engram_ckpt_load(q, scale, out=None, stream=None):
     *lead, D = shape
     if scale.shape != (*lead, (D + 31) // 32):
         raise ValueError("scale must hold a byte per 32 columns of each row of q")
-    out, op = _out(on, out, "out", shape, torch.bfloat16)
+    out, op = _out_like(on, out, "out", q, torch.bfloat16)
     _check(lib().engram_ckpt_load(qp, on.ptr(scale, "scale", torch.uint8), math.prod(lead), D, op, on.handle))
     return out
 
@@ -225,12 +233,13 @@ def engram_gate_output_ckpt(x, kv, q_weight, k_weight, eps, token_mask=None, out
         raise ValueError("kv must be [T, >= (hc+1)*dim]")
     if q_weight.shape != (hc, dim) or k_weight.shape != (hc, dim):
         raise ValueError("q_weight and k_weight must be [hc, dim]")
+    xp = on.ptr(x, "x", bf)
     mp = _mask(on, token_mask, T)
-    out, op = _out(on, out, "out", x.shape, bf)
+    out, op = _out_like(on, out, "out", x, bf)
     dot, dp = _out(on, dot, "dot", (T, hc), f32)
     checkpoint, c = _checkpoint(on, checkpoint, T, hc, dim)
     _check(lib().engram_gate_output_ckpt(
-        on.ptr(x, "x", bf), on.ptr(kv, "kv", bf, 2), kv.shape[1], on.ptr(q_weight, "q_weight", bf),
+        xp, on.ptr(kv, "kv", bf, 2), kv.shape[1], on.ptr(q_weight, "q_weight", bf),
         on.ptr(k_weight, "k_weight", bf), float(eps), mp, op, dp, *c, T, hc, dim, on.handle))
     return out, dot, checkpoint
 
@@ -264,15 +273,16 @@ def engram_gate_output_backward_ckpt(checkpoint, q_weight, k_weight, eps, dot, d
         raise ValueError("q_weight and k_weight must be [hc, dim]")
     if dot.shape != (T, hc):
         raise ValueError("dot must be [T, hc]")
+    gp = on.ptr(dout, "dout", bf)
     mp = _mask(on, token_mask, T)
-    dx, xp = _out(on, dx, "dx", dout.shape, bf)
+    dx, xp = _out_like(on, dx, "dx", dout, bf)
     dkv, kvp = _out(on, dkv, "dkv", (T, (hc + 1) * dim), bf)
     dq, qp = _out(on, dq, "dq", (hc, dim), f32)
     dk, kp = _out(on, dk, "dk", (hc, dim), f32)
     _ws, wp, wn = on.workspace(workspace, _t.engram_gate_output_backward_workspace_bytes(T, hc, dim))
     _check(lib().engram_gate_output_backward_ckpt(
         *c, on.ptr(q_weight, "q_weight", bf), on.ptr(k_weight, "k_weight", bf), float(eps), on.ptr(dot, "dot", f32),
-        on.ptr(dout, "dout", bf), mp, xp, kvp, qp, kp, wp, wn, T, hc, dim, on.handle))
+        gp, mp, xp, kvp, qp, kp, wp, wn, T, hc, dim, on.handle))
     return dx, dkv, dq, dk
 
 

@@ -137,6 +137,14 @@ def _dev(t, name, dtype, ndim=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _addr(torch, t, name, dtype, ndim=None):
+    """_dev as a plain integer, for the calls whose time is the host's."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and
+            (ndim is None or t.dim() == ndim)):
+        return t.data_ptr()
+    return _dev(t, name, dtype, ndim)
+
+
 def engram_hash(input_ids, start_pos, token_mask, token_map, cache, multipliers, primes, offsets, pad_id,
                 dead=-1, out=None, stream=None, int32_ids=False):
     """Hash ids int64 [B, L, E, (N-1)*H] (int32 with `int32_ids`: engram_hash_i32, ids outside [0, 2^31) as -1);
@@ -700,13 +708,13 @@ def engram_gate_residual(x, value, dot, token_mask=None, out=None, stream=None):
     (False shuts the gate).  `out` may be x itself."""
     import torch
 
-    x3 = x.reshape(-1, x.shape[-2], x.shape[-1])
+    x3 = x if x.dim() == 3 else x.reshape(-1, x.shape[-2], x.shape[-1])
     T, hc, dim = x3.shape
     if value.dim() != 2 or value.shape[0] != T or value.shape[1] < dim or value.stride(1) != 1:
         raise ValueError("value must be [T, >= dim] with unit column stride")
     if value.dtype != torch.bfloat16 or not value.is_cuda:
         raise TypeError("value must be a bf16 GPU tensor")
-    if tuple(dot.shape) != (T, hc):
+    if dot.shape != (T, hc):
         raise ValueError("dot must be [T, hc]")
     if out is None:
         out = torch.empty_like(x)
@@ -718,10 +726,11 @@ def engram_gate_residual(x, value, dot, token_mask=None, out=None, stream=None):
             raise ValueError("token_mask must hold one entry per token")
         if token_mask.dtype == torch.bool:
             token_mask = token_mask.view(torch.uint8)
-        mask_p = _dev(token_mask.reshape(T), "token_mask", torch.uint8, 1)
+        mask_p = _addr(torch, token_mask if token_mask.dim() == 1 else token_mask.reshape(T), "token_mask", torch.uint8, 1)
     _check(lib().engram_gate_residual(
-        _dev(x3, "x", torch.bfloat16, 3), ctypes.c_void_p(value.data_ptr()), value.stride(0),
-        _dev(dot, "dot", torch.float32), mask_p, _dev(out, "out", torch.bfloat16), T, hc, dim, _stream(stream)))
+        _addr(torch, x3, "x", torch.bfloat16, 3), value.data_ptr(), value.stride(0),
+        _addr(torch, dot, "dot", torch.float32), mask_p, _addr(torch, out, "out", torch.bfloat16), T, hc, dim,
+        _stream(stream)))
     return out
 
 

@@ -374,24 +374,47 @@ struct ResArgs {
     int hc, chunks;       // chunks = dim / 8
 };
 
-constexpr int kResPieces = 4;  // 16-byte pieces per thread
-
-// Streaming: thread-block b covers kResPieces * 256 consecutive 16-byte pieces of out (= of x);
+// Streaming: thread-block b covers P * 256 consecutive 16-byte pieces of out (= of x), P a thread;
 // the gate of a piece's (token, copy) is recomputed from its dot (one fp32 sqrt, exp and divide per
-// 8 outputs), the value piece of its token is re-read from L2 by the hc copies.
+// 8 outputs), the value piece of its token is re-read from L2 by the hc copies.  A thread loads all
+// its pieces before it stores any (`out` may be x: no other thread reads them), and divides in 64
+// bits for the first alone, if at all: 8,192 tokens x 4 x 5,120 128 us so, 133 piece by piece.
+template <int P>
 __global__ __launch_bounds__(kThreads) void gate_residual_kernel(ResArgs a) {
-    const int64_t base = static_cast<int64_t>(blockIdx.x) * (kResPieces * kThreads) + threadIdx.x;
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * (P * kThreads) + threadIdx.x;
+    const bool narrow = a.pieces <= 0xFFFFFFFFll;
+    int64_t tc = narrow ? static_cast<uint32_t>(base) / static_cast<uint32_t>(a.chunks) : base / a.chunks;
+    uint32_t j = static_cast<uint32_t>(base - tc * a.chunks);
+    int64_t t = narrow ? static_cast<uint32_t>(tc) / static_cast<uint32_t>(a.hc) : tc / a.hc;
+    uint32_t c = static_cast<uint32_t>(tc - t * a.hc);
+    u32x4 h[P], v[P];
+    float d[P];
+    bool live[P];
 #pragma unroll
-    for (int u = 0; u < kResPieces; ++u) {
+    for (int u = 0; u < P; ++u) {
+        const int64_t i = base + u * kThreads;
+        if (i < a.pieces) {
+            h[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.x) + i);  // read once
+            v[u] = *reinterpret_cast<const u32x4*>(a.value + t * a.ld_value + 8ll * j);    // shared by the copies
+            d[u] = a.dot[t * a.hc + c];
+            live[u] = !a.mask || a.mask[t] != 0;
+        }
+        j += kThreads;
+        if (j >= static_cast<uint32_t>(a.chunks)) {
+            const uint32_t over = j / static_cast<uint32_t>(a.chunks);
+            j -= over * a.chunks;
+            c += over;
+            if (c >= static_cast<uint32_t>(a.hc)) {
+                t += c / static_cast<uint32_t>(a.hc);
+                c %= static_cast<uint32_t>(a.hc);
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
         const int64_t i = base + u * kThreads;
         if (i >= a.pieces) return;
-        const int64_t tc = i / a.chunks;
-        const int j = static_cast<int>(i - tc * a.chunks);
-        const int64_t t = tc / a.hc;
-        const float g = (a.mask && a.mask[t] == 0) ? 0.f : gate_of(a.dot[tc]);
-        const u32x4 h = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.x) + i);  // read once
-        const u32x4 v = *reinterpret_cast<const u32x4*>(a.value + t * a.ld_value + 8 * j);    // shared by the copies
-        __builtin_nontemporal_store(residual(h, v, g), reinterpret_cast<u32x4*>(a.out) + i);
+        __builtin_nontemporal_store(residual(h[u], v[u], live[u] ? gate_of(d[u]) : 0.f), reinterpret_cast<u32x4*>(a.out) + i);
     }
 }
 
@@ -505,9 +528,13 @@ extern "C" int engram_gate_residual(const uint16_t* x, const uint16_t* value, in
     a.chunks = dim / 8;
     a.hc = hc;
     a.pieces = T * hc * a.chunks;
-    const int64_t blocks = (a.pieces + kResPieces * kThreads - 1) / (kResPieces * kThreads);
+    // Four pieces a thread where the launch is long; one where it is a few latencies.  us at 1 / 4 pieces, 4 x 5,120: 1 token
+    // 2.3 / 3.7, 256 7.0 / 8.1, 1,024 19.9 / 20.8, 8,192 134 / 128, 65,536 1,041 / 1,012.
+    const int per = a.pieces <= 1 << 22 ? 1 : 4;
+    const int64_t blocks = (a.pieces + per * kThreads - 1) / (per * kThreads);
     if (blocks > 0x7FFFFFFF) return fail(ENGRAM_EINVAL, "engram_gate_residual: too many tokens");
-    hipLaunchKernelGGL(gate_residual_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,
-                       as_stream(stream), a);
+    const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
+    if (per == 1) hipLaunchKernelGGL(gate_residual_kernel<1>, grid, block, 0, as_stream(stream), a);
+    else hipLaunchKernelGGL(gate_residual_kernel<4>, grid, block, 0, as_stream(stream), a);
     return check_launch("engram_gate_residual");
 }

@@ -163,15 +163,17 @@ def engram_wkv_mx4_gate(a, a_scale, w, x, q_weight, k_weight, eps, value=None, d
     if q_weight.shape != (hc, dim) or k_weight.shape != (hc, dim):
         raise ValueError("q_weight and k_weight must be [hc, dim]")
     if value is None:
-        value = on.empty((T, dim), bf)
-    if value.dim() != 2 or value.shape[0] != T or value.shape[1] < dim or value.stride(1) != 1:
+        value, vp = _out(on, None, "value", (T, dim), bf)
+    elif value.dim() != 2 or value.shape[0] != T or value.shape[1] < dim or value.stride(1) != 1:
         raise ValueError("value must be [T, >= dim] with unit column stride")
-    if value.dtype != bf or value.get_device() != on.index:
+    elif value.dtype != bf or value.get_device() != on.index:
         raise TypeError("value must be a bf16 tensor of the call's GPU")
+    else:
+        vp = value.data_ptr()
     dot, dp = _out(on, dot, "dot", (T, hc), f32)
     _ws, sw, sn = on.workspace(workspace, hc * (dim // 128) * 3 * T * 4)  # engram_wkv_gate_workspace_bytes
     _check(lib().engram_wkv_mx4_gate(ap, sp, bits, wp, on.ptr(x, "x", bf), on.ptr(q_weight, "q_weight", bf),
-                                     on.ptr(k_weight, "k_weight", bf), float(eps), value.data_ptr(), value.stride(0), dp, sw,
+                                     on.ptr(k_weight, "k_weight", bf), float(eps), vp, value.stride(0), dp, sw,
                                      sn, T, K, hc, dim, on.handle))
     return value, dot
 

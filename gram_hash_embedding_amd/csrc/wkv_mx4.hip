@@ -122,7 +122,10 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
     constexpr int kStages = kSets > 1 ? kSets / kSub + 1 : 2;
     constexpr int kRing = kStages * kStageBytes;
     constexpr int kWaveBytes = BM * 128;                    // a wave's part of the tile as bf16, behind the last step
-    constexpr int kLds = kRing > NW * kWaveBytes ? kRing : NW * kWaveBytes;
+    // the gate's stream rows have room beside the stages (two workgroups a CU): they are loaded ahead of the steps
+    constexpr bool kEarly = kGate && kRing + NW * kWaveBytes <= 80 * 1024;
+    constexpr int kParts = kEarly ? kRing : 0;
+    constexpr int kLds = kParts + NW * kWaveBytes > kRing ? kParts + NW * kWaveBytes : kRing;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -254,6 +257,30 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         wsoff += kRecord;
         slot = next;
     };
+    uint8_t* const mine = lds + kParts + wave * kWaveBytes;  // the wave's part, behind the last step
+    const int nw = n0 + 64 * wave;
+    const int line_row = lane >> 3;  // a load or store of 16 bytes a lane has 8 rows: of these the lane's, and its piece
+    const bool keys = kGate && n0 < p.n_key;
+    u32x2 qw[4], kw[4];  // q and k of the lane's columns
+    // the stream's rows of the wave's tokens and columns (rows past M: zeros), and the weights
+    auto load_stream = [&]() {
+        const int64_t x_bytes = static_cast<int64_t>(p.n_key) * 2;
+        const int x_rows = static_cast<int>(min<int64_t>(BM, p.M - m0));
+        const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint16_t*>(p.x + m0 * p.n_key + nw), 0, static_cast<int>(x_rows * x_bytes - 2 * nw), kBufferWord3);
+        const uint32_t xo = static_cast<uint32_t>(line_row * x_bytes), xp = ((lane & 7) ^ ((line_row >> 1) & 7)) << 4;
+#pragma unroll
+        for (int q = 0; q < 2 * MI; ++q)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, mine + q * 1024, 16,
+                                                     xo + static_cast<uint32_t>(8 * q * x_bytes) + (q & 1 ? xp ^ 64u : xp), 0, 0,
+                                                     kNonTemporal);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = nw + 16 * j + 4 * g;
+            qw[j] = *reinterpret_cast<const u32x2*>(p.q + n);
+            kw[j] = *reinterpret_cast<const u32x2*>(p.k + n);
+        }
+    };
 #pragma unroll
     for (int t = 0; t < kStages; ++t)
 #pragma unroll
@@ -268,6 +295,7 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         wsoff += kRecord;
         fence();
     }
+    if (kEarly && keys) load_stream();
     __builtin_amdgcn_s_waitcnt(wait_vmcnt(kSets * kWLoads + (kStages - 1) * kLoads));
     barrier();
 #pragma unroll
@@ -301,14 +329,11 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
     // c ^ (t / 2) % 8, so that memory is written and read in whole lines of 128 bytes, two to 16 lanes.
     __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
     barrier();
-    uint8_t* const mine = lds + wave * kWaveBytes;
-    const int nw = n0 + 64 * wave;
-    const int line_row = lane >> 3;  // a load or store of 16 bytes a lane has 8 rows: of these the lane's, and its piece
     // a lane's four columns 16 j + 4 g .. +3 of token 16 i + r
     const uint32_t quad[2] = {static_cast<uint32_t>(r * 128 + (((g >> 1) ^ key) << 4) + (g & 1) * 8),
                               static_cast<uint32_t>(r * 128 + (((4 + (g >> 1)) ^ key) << 4) + (g & 1) * 8)};
     auto quad_at = [&](int i, int j) { return mine + i * 2048 + (quad[j >> 1] ^ ((j & 1) << 5)); };
-    if (!kGate || n0 >= p.n_key) {
+    if (!keys) {
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -326,28 +351,15 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         return;
     }
     if constexpr (kGate) {
-        // the stream's rows of the wave's tokens and columns (rows past M: zeros)
-        const int64_t x_bytes = static_cast<int64_t>(p.n_key) * 2;
-        const int x_rows = static_cast<int>(min<int64_t>(BM, p.M - m0));
-        const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint16_t*>(p.x + m0 * p.n_key + nw), 0, static_cast<int>(x_rows * x_bytes - 2 * nw), kBufferWord3);
-        const uint32_t xo = static_cast<uint32_t>(line_row * x_bytes), xp = ((lane & 7) ^ ((line_row >> 1) & 7)) << 4;
+        if (!kEarly) load_stream();
+        float wq[4][4];  // q * k (exact in fp32)
 #pragma unroll
-        for (int q = 0; q < 2 * MI; ++q)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, mine + q * 1024, 16,
-                                                     xo + static_cast<uint32_t>(8 * q * x_bytes) + (q & 1 ? xp ^ 64u : xp), 0, 0,
-                                                     kNonTemporal);
-        float wq[4][4];  // q * k of the lane's columns (exact in fp32)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = nw + 16 * j + 4 * g;
-            const u32x2 q = *reinterpret_cast<const u32x2*>(p.q + n), k = *reinterpret_cast<const u32x2*>(p.k + n);
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                wq[j][2 * e] = lo_bf16(q[e]) * lo_bf16(k[e]);
-                wq[j][2 * e + 1] = hi_bf16(q[e]) * hi_bf16(k[e]);
+                wq[j][2 * e] = lo_bf16(qw[j][e]) * lo_bf16(kw[j][e]);
+                wq[j][2 * e + 1] = hi_bf16(qw[j][e]) * hi_bf16(kw[j][e]);
             }
-        }
         float res[MI][3];
         fence();
         __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));  // the wave's own rows
@@ -376,7 +388,7 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
             res[i][2] = hh + __shfl_xor(hh, 32, 64);
         }
         // two waves' 64 columns make a slice of 128: the right one leaves its sums in its part of LDS
-        float* sums = reinterpret_cast<float*>(lds + (wave | 1) * kWaveBytes);
+        float* sums = reinterpret_cast<float*>(lds + kParts + (wave | 1) * kWaveBytes);
         fence();
         __builtin_amdgcn_s_waitcnt(kWaitLgkmcnt0);
         fence();

@@ -27,6 +27,16 @@ inline dim3 group_grid(int64_t groups) {
 }
 __device__ inline int64_t group_index() { return blockIdx.y * kMaxGroupsX + blockIdx.x; }
 
+// The part of the work, of `parts`, that workgroup `group` of as many does where `run` parts in a row share data: workgroups go
+// to the 8 XCDs in turn, so those that are 8 apart take a run's parts, and its data is read into one L2.
+__device__ inline int64_t part_of_group(int64_t group, int64_t parts, uint32_t run) {
+    const uint32_t turn = 8 * run;
+    const int64_t first = group / turn * turn;
+    if (first + turn > parts) return group;
+    const uint32_t left = static_cast<uint32_t>(group - first);
+    return first + left % 8 * run + left / 8;
+}
+
 // 16-byte vector of 32-bit words: the unit of every wide global access.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 

@@ -26,6 +26,8 @@
 // is written from the registers: x, key and value each cross HBM once, out is
 // written once (the value row is re-read by the hc waves of a token from L2).
 // Small launches split each row over a workgroup, as the dot does.
+#include <numeric>
+
 #include "gate.h"
 
 namespace engram {
@@ -372,16 +374,18 @@ struct ResArgs {
     int64_t T;
     int64_t pieces;       // T * hc * dim / 8
     int hc, chunks;       // chunks = dim / 8
+    uint32_t run;         // workgroups in a row that an XCD takes
 };
 
 // Streaming: thread-block b covers P * 256 consecutive 16-byte pieces of out (= of x), P a thread;
 // the gate of a piece's (token, copy) is recomputed from its dot (one fp32 sqrt, exp and divide per
 // 8 outputs), the value piece of its token is re-read from L2 by the hc copies.  A thread loads all
 // its pieces before it stores any (`out` may be x: no other thread reads them), and divides in 64
-// bits for the first alone, if at all: 8,192 tokens x 4 x 5,120 128 us so, 133 piece by piece.
+// bits for the first alone, if at all: 8,192 tokens x 4 x 5,120 128 us so, 133 piece by piece (and
+// 117 with a token's copies on one XCD).
 template <int P>
 __global__ __launch_bounds__(kThreads) void gate_residual_kernel(ResArgs a) {
-    const int64_t base = static_cast<int64_t>(blockIdx.x) * (P * kThreads) + threadIdx.x;
+    const int64_t base = part_of_group(blockIdx.x, gridDim.x, a.run) * (P * kThreads) + threadIdx.x;
     const bool narrow = a.pieces <= 0xFFFFFFFFll;
     int64_t tc = narrow ? static_cast<uint32_t>(base) / static_cast<uint32_t>(a.chunks) : base / a.chunks;
     uint32_t j = static_cast<uint32_t>(base - tc * a.chunks);
@@ -533,6 +537,11 @@ extern "C" int engram_gate_residual(const uint16_t* x, const uint16_t* value, in
     const int per = a.pieces <= 1 << 22 ? 1 : 4;
     const int64_t blocks = (a.pieces + per * kThreads - 1) / (per * kThreads);
     if (blocks > 0x7FFFFFFF) return fail(ENGRAM_EINVAL, "engram_gate_residual: too many tokens");
+    // An XCD takes whole tokens, whose value rows it then reads once: as many workgroups in a row as end with one, or 8 where
+    // that takes more than 16.  8,192 x 4 x 5,120 117 us at runs of five (two tokens), 120 at 4, 128 one by one.
+    const int64_t token = static_cast<int64_t>(hc) * a.chunks;
+    const int64_t whole = token / std::gcd(token, static_cast<int64_t>(per * kThreads));
+    a.run = static_cast<uint32_t>(whole <= 16 ? whole : 8);
     const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
     if (per == 1) hipLaunchKernelGGL(gate_residual_kernel<1>, grid, block, 0, as_stream(stream), a);
     else hipLaunchKernelGGL(gate_residual_kernel<4>, grid, block, 0, as_stream(stream), a);

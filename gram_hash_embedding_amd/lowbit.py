@@ -223,7 +223,8 @@ def engram_gate_output_ckpt(x, kv, q_weight, k_weight, eps, token_mask=None, out
                             stream=None):
     """(out, dot, GateCheckpoint): engram_gate_output of x bf16 [T, hc, dim] (or [B, L, hc, dim]) and kv [T, >= (hc+1)*dim],
     with x, the keys and the value kept in 8 bits (engram_ckpt_save's, of their rows of dim) for
-    engram_gate_output_backward_ckpt.  out (x's shape), dot (float32 [T, hc]) and `checkpoint` are allocated if not given."""
+    engram_gate_output_backward_ckpt.  out (x's shape; x itself is allowed), dot (float32 [T, hc]) and `checkpoint` are
+    allocated if not given."""
     on = _t._On(stream, x, "x")
     torch = _t.torch
     bf, f32 = torch.bfloat16, torch.float32

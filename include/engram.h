@@ -822,7 +822,9 @@ int engram_ckpt_load(const int8_t* q, const uint8_t* scale, int64_t rows, int32_
  *   kv_q, kv_scale  = engram_ckpt_save of kv's T * (hc+1) rows of dim (the keys, then the value)
  * bit for bit.
  *
- * x, kv, ld_kv, q_weight, k_weight, eps, token_mask, out  as engram_gate_output
+ * x, kv, ld_kv, q_weight, k_weight, eps, token_mask  as engram_gate_output
+ * out       uint16 [T, hc, dim] bf16 bits, out; 16-byte aligned; may be x itself (a row is read before it is written, by
+ *           the same workgroup)
  * dot       float32 [T, hc], out (kept for the gradient); 4-byte aligned
  * x_q       int8 [T, hc, dim], out; 8-byte aligned;     x_scale   uint8 [T, hc, ceil(dim/32)], out
  * kv_q      int8 [T, hc+1, dim], out; 8-byte aligned;   kv_scale  uint8 [T, hc+1, ceil(dim/32)], out

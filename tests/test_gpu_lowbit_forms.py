@@ -197,3 +197,19 @@ def test_two_graphs_one_workspace(gpu_device):
             got = [t.clone() for t in held[i]]
             for p, r in zip(got, step(i)):
                 assert torch.equal(p, r), (turn, i)
+
+
+@pytest.mark.parametrize("T,hc,dim", [(50, 4, 512), (33, 3, 264), (9, 1, 8192), (700, 4, 5120)])
+def test_output_with_checkpoints_in_place(gpu_device, T, hc, dim):
+    """out may be x: the stream kept is the one that came in; given tensors are filled and nothing beside them."""
+    x, kv, q, k, mask, _ = _gate_case(T, hc, dim, gpu_device, extra=8)
+    out, dot, c = g.engram_gate_output_ckpt(x, kv, q, k, EPS, mask)
+    nb = (dim + 31) // 32
+    held = [torch.full((T + 1, n, w), 9, dtype=t, device=gpu_device) for n, w, t in (
+        (hc, dim, torch.int8), (hc, nb, torch.uint8), (hc + 1, dim, torch.int8), (hc + 1, nb, torch.uint8))]
+    stream = x.clone()
+    o2, d2, c2 = g.engram_gate_output_ckpt(stream, kv, q, k, EPS, mask, out=stream, dot=torch.empty_like(dot),
+                                           checkpoint=g.GateCheckpoint(*[t[:T] for t in held]))
+    assert o2 is stream and torch.equal(o2, out) and torch.equal(d2, dot)
+    for t, a, b in zip(held, c, c2):
+        assert torch.equal(a, b) and (t[T] == 9).all()

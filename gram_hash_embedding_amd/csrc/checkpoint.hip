@@ -14,8 +14,7 @@
 namespace engram {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
+constexpr int kThreads = 256;
 
 // Four lanes hold a block of 32 (piece j: columns 8 j .. 8 j + 7); lanes without a piece pass zeros and `ok` false.  Every lane
 // of the wave takes part.
@@ -73,16 +72,42 @@ struct CkptArgs {
     int hc, dim;
 };
 
-// A workgroup per (token, copy), a token's copies on one XCD, which reads its value row from HBM once (8,192 x 4 x 5,120 269 us,
-// 5.5 TB/s; 279 with every copy on another); thread i has the 16-byte pieces i + 256 u (P of them) of the copy's stream and key
-// rows and of the value row.  The sums of the four waves meet in LDS and every thread adds them in wave order.
-template <int P>
-__global__ __launch_bounds__(kThreads) void gate_output_ckpt_kernel(CkptArgs a) {
-    __shared__ float part[kWaves][3];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t tc = part_of_group(group_index(), a.T * a.hc, a.hc);  // token * hc + copy
+// The sum of v over the lanes of a row: L neighbours in a wave, or a workgroup, whose waves' sums meet in `part` (every thread
+// adds them in wave order).
+template <int L>
+__device__ inline void row_sums(float (&v)[3], float (*part)[3]) {
+#pragma unroll
+    for (int off = (L < 64 ? L : 64) / 2; off >= 1; off >>= 1)
+#pragma unroll
+        for (int e = 0; e < 3; ++e) v[e] += __shfl_xor(v[e], off, 64);
+    if constexpr (L > 64) {
+        if ((threadIdx.x & 63) == 0)
+            for (int e = 0; e < 3; ++e) part[threadIdx.x >> 6][e] = v[e];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            v[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < L / 64; ++w) v[e] += part[w][e];
+        }
+    }
+}
+
+// L threads per (token, copy), a token's copies in one workgroup or on one XCD, which reads its value row from HBM once (8,192 x
+// 4 x 5,120 269 us, 5.5 TB/s; 279 with every copy on another); thread i has the 16-byte pieces i + L u (P of them) of the copy's
+// stream and key rows and of the value row.
+template <int L, int P>
+__global__ __launch_bounds__(L < kThreads ? kThreads : L) void gate_output_ckpt_kernel(CkptArgs a) {
+    __shared__ float part[(L + 63) / 64][3];
+    constexpr int kRows = L < kThreads ? kThreads / L : 1;  // of a workgroup
+    const int64_t n = a.T * a.hc, groups = (n + kRows - 1) / kRows;
+    const int64_t group = part_of_group(group_index(), groups, (a.hc + kRows - 1) / kRows);
+    if (group >= groups) return;
+    const int lane = kRows == 1 ? threadIdx.x : threadIdx.x % L;
+    const int64_t at = kRows == 1 ? group : group * kRows + threadIdx.x / L;  // token * hc + copy
+    const bool live = kRows == 1 || at < n;
+    const int64_t tc = live ? at : n - 1;
     const int64_t t = tc / a.hc;
-    if (t >= a.T) return;
     const int c = static_cast<int>(tc - t * a.hc);
     const int chunks = a.dim / 8, blocks = (chunks + 3) / 4;
     const u32x4* q = reinterpret_cast<const u32x4*>(a.q + static_cast<int64_t>(c) * a.dim);
@@ -96,19 +121,19 @@ __global__ __launch_bounds__(kThreads) void gate_output_ckpt_kernel(CkptArgs a) 
     u32x4 hr[P], kr[P], vr[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const int j = threadIdx.x + kThreads * i;
+        const int j = lane + L * i;
         hr[i] = kr[i] = vr[i] = u32x4{0, 0, 0, 0};
-        if (j < chunks) {
+        if (live && j < chunks) {
             hr[i] = __builtin_nontemporal_load(h + j);
             kr[i] = __builtin_nontemporal_load(key + j);
             vr[i] = val[j];
         }
     }
-    float hh = 0.f, kk = 0.f, hwk = 0.f;
+    float sum[3] = {0.f, 0.f, 0.f};  // of h^2, key^2 and h w key
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const int j = threadIdx.x + kThreads * i;
-        const bool ok = j < chunks;
+        const int j = lane + L * i;
+        const bool ok = live && j < chunks;
         if (ok) {
             const u32x4 qv = q[j], kw = k[j];
 #pragma unroll
@@ -117,40 +142,33 @@ __global__ __launch_bounds__(kThreads) void gate_output_ckpt_kernel(CkptArgs a) 
                 const float w1 = hi_bf16(qv[e]) * hi_bf16(kw[e]);
                 const float h0 = lo_bf16(hr[i][e]), h1 = hi_bf16(hr[i][e]);
                 const float k0 = lo_bf16(kr[i][e]), k1 = hi_bf16(kr[i][e]);
-                hh += h0 * h0 + h1 * h1;
-                kk += k0 * k0 + k1 * k1;
-                hwk += h0 * w0 * k0 + h1 * w1 * k1;
+                sum[0] += h0 * h0 + h1 * h1;
+                sum[1] += k0 * k0 + k1 * k1;
+                sum[2] += h0 * w0 * k0 + h1 * w1 * k1;
             }
         }
         save_piece(hr[i], ok, a.xq + tc * a.dim, a.xs + tc * blocks, j);
         save_piece(kr[i], ok, a.kvq + krow * a.dim, a.kvs + krow * blocks, j);
-        if (c == 0) save_piece(vr[i], ok, a.kvq + vrow * a.dim, a.kvs + vrow * blocks, j);
+        if (kRows > 1 || c == 0) save_piece(vr[i], ok && c == 0, a.kvq + vrow * a.dim, a.kvs + vrow * blocks, j);
     }
-    hh = wave_sum(hh);
-    kk = wave_sum(kk);
-    hwk = wave_sum(hwk);
-    if (lane == 0) {
-        part[w][0] = hh;
-        part[w][1] = kk;
-        part[w][2] = hwk;
-    }
-    __syncthreads();
-    float shh = 0.f, skk = 0.f, shwk = 0.f;
-#pragma unroll
-    for (int v = 0; v < kWaves; ++v) {
-        shh += part[v][0];
-        skk += part[v][1];
-        shwk += part[v][2];
-    }
-    const float rstd = rsqrtf(shh * a.inv_dim + a.eps) * rsqrtf(skk * a.inv_dim + a.eps);
-    const float d = shwk * rstd * a.rsqrt_dim;
-    if (threadIdx.x == 0) a.dot[tc] = d;
+    row_sums<L>(sum, part);
+    const float rstd = rsqrtf(sum[0] * a.inv_dim + a.eps) * rsqrtf(sum[1] * a.inv_dim + a.eps);
+    const float d = sum[2] * rstd * a.rsqrt_dim;
+    if (live && lane == 0) a.dot[tc] = d;
     const float gate = (a.mask && a.mask[t] == 0) ? 0.f : gate_of(d);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const int j = threadIdx.x + kThreads * i;
-        if (j < chunks) __builtin_nontemporal_store(residual(hr[i], vr[i], gate), out + j);
+        const int j = lane + L * i;
+        if (live && j < chunks) __builtin_nontemporal_store(residual(hr[i], vr[i], gate), out + j);
     }
+}
+
+template <int L, int P>
+int launch_output(const CkptArgs& a, hipStream_t stream, const char* what) {
+    constexpr int kRows = L < kThreads ? kThreads / L : 1;
+    hipLaunchKernelGGL((gate_output_ckpt_kernel<L, P>), group_grid((a.T * a.hc + kRows - 1) / kRows), dim3(kRows * L), 0, stream,
+                       a);
+    return check_launch(what);
 }
 
 // what is wrong with a checkpoint's rows, or null
@@ -227,11 +245,17 @@ extern "C" int engram_gate_output_ckpt(const uint16_t* x, const uint16_t* kv, in
     a.T = T;
     a.hc = hc;
     a.dim = dim;
-    const dim3 grid = group_grid(T * hc), block(kThreads);
-    const int pieces = (dim / 8 + kThreads - 1) / kThreads;
-    if (pieces == 1) hipLaunchKernelGGL(gate_output_ckpt_kernel<1>, grid, block, 0, as_stream(stream), a);
-    else if (pieces == 2) hipLaunchKernelGGL(gate_output_ckpt_kernel<2>, grid, block, 0, as_stream(stream), a);
-    else if (pieces == 3) hipLaunchKernelGGL(gate_output_ckpt_kernel<3>, grid, block, 0, as_stream(stream), a);
-    else hipLaunchKernelGGL(gate_output_ckpt_kernel<4>, grid, block, 0, as_stream(stream), a);
-    return check_launch(what);
+    // As many threads a row as it has pieces, up to a wave of two each, so that no thread idles and no barrier is met: 8,192 x 4
+    // x 256 17 us, of 512 32, of 1,024 56 (a workgroup a row 60, 63 and 75; but 64 x 4 x 1,024 4.7 against 4.0).  Past 1,024 a
+    // workgroup of one to three pieces a thread: of 2,048 108 us (a wave a row 124), of 5,120 268 (640 threads 330), of 8,192
+    // 430 (1,024 threads 625).
+    hipStream_t s = as_stream(stream);
+    if (dim <= 128) return launch_output<16, 1>(a, s, what);
+    if (dim <= 256) return launch_output<32, 1>(a, s, what);
+    if (dim <= 512) return launch_output<64, 1>(a, s, what);
+    if (dim <= 1024) return launch_output<64, 2>(a, s, what);
+    if (dim <= 2048) return launch_output<256, 1>(a, s, what);
+    if (dim <= 4096) return launch_output<256, 2>(a, s, what);
+    if (dim <= 6144) return launch_output<256, 3>(a, s, what);
+    return launch_output<512, 2>(a, s, what);
 }

@@ -213,3 +213,19 @@ def test_output_with_checkpoints_in_place(gpu_device, T, hc, dim):
     assert o2 is stream and torch.equal(o2, out) and torch.equal(d2, dot)
     for t, a, b in zip(held, c, c2):
         assert torch.equal(a, b) and (t[T] == 9).all()
+
+
+@pytest.mark.parametrize("dim", [8, 24, 120, 128, 136, 248, 256, 264, 512, 520, 1016, 1024, 1032, 2048, 2056, 4096, 4104, 6144, 6152,
+                                 8192])
+@pytest.mark.parametrize("T,hc", [(1, 1), (3, 3), (67, 2), (130, 5)])
+def test_output_with_checkpoints_at_every_width(gpu_device, T, hc, dim):
+    """A group of lanes, a wave or a workgroup a row: what is kept bit for bit, the dot within its bound, the output as the
+    residual gives it from that dot."""
+    x, kv, q, k, mask, _ = _gate_case(T, hc, dim, gpu_device, extra=16)
+    out, dot, c = g.engram_gate_output_ckpt(x, kv, q, k, EPS, mask)
+    rows = kv[:, :(hc + 1) * dim].contiguous().view(T, hc + 1, dim)
+    for got, want in zip(c, (*g.engram_ckpt_save(x), *g.engram_ckpt_save(rows))):
+        assert torch.equal(got, want)
+    want, tol = _dot_tolerance(x, rows[:, :hc], q, k)
+    assert ((dot.double() - want).abs() <= tol).all()
+    assert torch.equal(out, g.engram_gate_residual(x, kv[:, hc * dim:(hc + 1) * dim], dot, mask))

@@ -133,10 +133,12 @@ def test_fused_products_of_any_size(library, bits, T, K, hc, dim):
 @pytest.mark.parametrize("T,hc,dim", [(1, 1, 8), (8192, 4, 5120), (1 << 22, 4, 1024), (1 << 31, 1, 8), (1 << 30, 3, 8),
                                       (1 << 24, 64, 8), (7, 64, 8192)])
 def test_outputs_and_gradients_of_any_size(library, T, hc, dim):
-    """A workgroup of the output has a token's copy."""
+    """A token's copy of the output has 16, 32 or 64 threads up to 1,024 columns, then a workgroup."""
     status, launches = _output(library, T, hc, dim)
     assert status == 0 and len(launches) == 1 and _fits(launches)
-    assert _threads(launches[0]) >= T * hc * 256
+    x, y, _, bx, _, _ = launches[0]
+    a_row = 16 if dim <= 128 else 32 if dim <= 256 else 64 if dim <= 1024 else bx
+    assert x * y >= -(-T * hc // (bx // a_row))
     status, launches = _grad(library, T, hc, dim)
     assert status == 0 and len(launches) == 2 and _fits(launches)
 

@@ -16,13 +16,15 @@
 // HBM-bound: per token (3 hc + 1) rows of dim are read and 2 hc + 1 written, every one once.  A workgroup holds a
 // whole token, one 16-byte piece of every row per thread: the rows stay in registers between the sums that need all
 // of a row and the outputs that need the sums, and the sum over tokens of dq and dk stays in registers (in LDS for four
-// copies of more than 5,120 columns) over all of the workgroup's tokens.  The next token's rows are asked for as this one's are used up, so loads are in flight over
-// the barrier (one per token: the sums of the waves, in two LDS buffers taken in turn).  A second launch adds the
-// workgroups' sums in their order, so the same call gives the same bits.
+// copies of more than 5,120 columns) over all of the workgroup's tokens.  The next token's rows are asked for as this one's
+// are used up, so loads are in flight over the barrier (one per token: the sums of the waves, in two LDS buffers taken in
+// turn).  A second launch adds the workgroups' sums in their order, so the same call gives the same bits.
 //
 // 8,192 tokens, both launches: 4 copies of 5,120 335 us (5.5 TB/s of the bytes above), of 2,048 146 (5.0), of 1,024 84
 // (4.4), of 256 41 (2.2, bound by the tokens' chains of barrier and sums), of 8,192 633 (4.7); 2 of 5,120 193 (5.2), 1 of
-// 5,120 125 (4.7); 3 of 2,048 184 (3.1, the kernel for any count of copies, which takes a barrier a copy).
+// 5,120 125 (4.7); 3 of 2,048 184 (3.1, the kernel for any count of copies, which takes a barrier a copy).  From checkpoints:
+// 4 copies of 5,120 318 us (4.7 TB/s: fewer bytes for the same arithmetic), of 2,048 127, of 1,024 74, of 256 45, of 8,192 485;
+// 2 of 5,120 188, 1 of 5,120 129; 3 of 2,048 164.
 #include <type_traits>
 
 #include "mx.h"

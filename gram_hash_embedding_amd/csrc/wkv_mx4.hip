@@ -92,6 +92,10 @@ __device__ inline f32x4 mfma(const i32x4& w, int sw, const AFrag<kA8>& a, int sa
 // two waves of a 256 x 128 tile read the same weights, at 64 bytes of a row a load), so as few and as long runs as the registers
 // allow; a few tokens are bound by the weights' latency, so as many steps in flight as they allow.
 //
+// 1,536 x 25,600, us with 8-bit / 4-bit rows: 1 token 5.9 / 5.8, 256 11.2 / 9.8, 8,192 231 / 173, 65,536 1,798 / 1,349 (2.9 / 3.8
+// PFLOP/s); 6,144 x 25,600: 8,192 tokens 805 / 532 (3.2 / 4.8, the instruction alone 4.1 / 6.9).  Fused, 4 x 5,120: 256 18.3 /
+// 16.8, 8,192 275 / 210, 65,536 2,178 / 1,636.
+//
 // LDS rows: the 16-byte piece c of a row at slot c ^ (row / 2) % 8: neighbouring lanes' pieces lie in different banks.
 constexpr int kBufferWord3 = 0x00020000;
 constexpr int kWaitLgkmcnt0 = 0xC07F;
@@ -423,6 +427,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // largest exponent is 2, so the shared scale's code is the field less 2, or 0 where that is below E8M0's range (fields 0, of
 // zeros and subnormals, to 2).  v_cvt_scalef32_pk_fp4_bf16 divides by the scale, rounds to nearest even and saturates at 6 --
 // checked on every bf16 pattern.  A block with an infinity or a NaN, which E2M1 has not, takes the NaN scale 0xFF and zeros.
+// HBM-bound: 65,536 x 1,536 49 us (5.3 TB/s); 256 rows 2.5.
 __global__ __launch_bounds__(256) void mx4_quant_kernel(const uint16_t* x, int64_t rows, int K, int64_t rows4, uint8_t* q,
                                                         uint8_t* scale) {
     const int64_t gid = group_index() * 256 + threadIdx.x;

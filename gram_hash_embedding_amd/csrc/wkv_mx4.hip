@@ -42,6 +42,7 @@ struct Mx4Args {
     uint16_t* kv;        // [M, ld_out] bf16: the columns from n_key on
     int64_t M, M4, ld_out;
     int N, steps;        // columns, K / 128
+    int group, across;   // the tiles' order: groups of so many tile rows (across: tile columns), each walked along the other axis
     // the fused gate: columns below n_key are keys, reduced against the stream and not stored
     const uint16_t* x;   // [M, hc, dim] bf16
     const uint16_t* q;   // [hc, dim] bf16
@@ -102,7 +103,6 @@ constexpr int kWaitLgkmcnt0 = 0xC07F;
 constexpr int wait_vmcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | 0x0F70; }
 constexpr int kNonTemporal = 2;  // cache-policy operand of a load: streamed past L2
 constexpr int kXcds = 8;
-constexpr int kGroupM = 8;  // tile rows that an XCD walks together
 
 __device__ inline i32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t at) {
     const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
@@ -135,21 +135,19 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r = lane & 15;
     const int S = p.steps;
-    // the workgroup's tile: an XCD (workgroups % 8) takes a contiguous run of the order, kGroupM tile rows deep
+    // the workgroup's tile: an XCD (workgroups % 8) takes a contiguous run of the order
     int64_t m0;
     int n0;
     {
-        const int64_t n = static_cast<int64_t>(tiles_m) * tiles_n;
-        const int64_t pid = group_index(), xcd = pid % kXcds, per = n / kXcds, rem = n % kXcds;
+        const uint32_t n = static_cast<uint32_t>(tiles_m) * static_cast<uint32_t>(tiles_n);
+        const uint32_t pid = static_cast<uint32_t>(group_index()), xcd = pid % kXcds, per = n / kXcds, rem = n % kXcds;
         if (pid >= n) return;
-        const int64_t at = xcd * per + min(xcd, rem) + pid / kXcds;
-        const int64_t in_group = static_cast<int64_t>(kGroupM) * tiles_n;
-        const int64_t group = at / in_group;
-        const int first = static_cast<int>(group) * kGroupM;
-        const int deep = min(tiles_m - first, kGroupM);
-        const int left = static_cast<int>(at - group * in_group);
-        m0 = static_cast<int64_t>(first + left % deep) * BM;
-        n0 = left / deep * BN;
+        const uint32_t at = xcd * per + min(xcd, rem) + pid / kXcds;
+        const uint32_t outer = p.across ? tiles_n : tiles_m, inner = p.across ? tiles_m : tiles_n, depth = p.group;
+        const uint32_t group = at / (depth * inner), first = group * depth, deep = min(outer - first, depth);
+        const uint32_t left = at - first * inner, i = left / deep, o = first + left - i * deep;
+        m0 = static_cast<int64_t>(p.across ? i : o) * BM;
+        n0 = static_cast<int>(p.across ? o : i) * BN;
     }
     const int row_bytes = S * (kA8 ? 128 : 64);
     const int valid_bytes = static_cast<int>(min<int64_t>(BM, p.M - m0)) * row_bytes;
@@ -473,10 +471,23 @@ __global__ __launch_bounds__(256) void mx4_pack_kernel(const uint8_t* q, const u
     }
 }
 
+// The order: eight tile rows together along the columns (16 +1 %, 4 +7 %), which reads the rows into the L2s once and the
+// weights once for every eight; or, of a plain product whose weights an XCD's L2 (4 MB) holds an eighth of, that eighth along
+// the rows, which reads the weights once and the rows eight times, where that is less: 65,536 x 1,536 x 25,600 with 4-bit rows
+// 1,350 us (1,400 the other way, 1.4 GB of reads instead of 0.4), 8,192 173 (178), with 8-bit rows 237 (238), 8,192 x 512 x 8,192
+// 34 (40).  Where it is more, 65,536 x 1,536 x 2,560 147 (140); where an eighth is too large, 8,192 x 6,144 x 25,600 575 (558);
+// fused, whose stream's rows it scatters, 8,192 225 (219).
+constexpr int kGroupM = 8;
+constexpr int64_t kHeld = 3 << 20;
+
 template <bool kA8, int MI, int NW, int kSets, bool kGate>
-int launch_tiles(const Mx4Args& p, hipStream_t stream, const char* what) {
+int launch_tiles(Mx4Args p, hipStream_t stream, const char* what) {
     const int64_t tiles_m = (p.M + 16 * MI - 1) / (16 * MI);
     const int tiles_n = (p.N + 64 * NW - 1) / (64 * NW);
+    const int eighth = (tiles_n + kXcds - 1) / kXcds;
+    const int64_t row_bytes = p.steps * (kA8 ? 128ll : 64ll), weights = static_cast<int64_t>(tiles_n) * NW * p.steps * kRecord;
+    p.across = !kGate && weights <= kXcds * kHeld && (kXcds - 1) * p.M * row_bytes < (tiles_m / kGroupM - 1) * weights;
+    p.group = p.across ? eighth : kGroupM;
     hipLaunchKernelGGL((mx4_tile_kernel<kA8, MI, NW, kSets, kGate>), group_grid(tiles_m * tiles_n), dim3(64 * NW), 0,
                        stream, p, static_cast<int>(tiles_m), tiles_n);
     return check_launch(what);
@@ -506,7 +517,7 @@ const char* bad_shape(int64_t T, int32_t a_bits, int32_t K, int32_t N) {
     if (a_bits != 4 && a_bits != 8) return "a_bits must be 4 or 8";
     if (K < kStepCols || K % kStepCols != 0 || K > kMaxK) return "K must be a multiple of 128 in [128, 2^20]";
     if (N < 8 || N % 8 != 0 || N > kMaxN) return "the columns must be a multiple of 8 in [8, 2^22]";
-    if (T > 1ll << 34 || T > (1ll << 48) / N) return "too many tokens";
+    if (T > 1ll << 34 || T > (1ll << 41) / N) return "too many tokens";
     return nullptr;
 }
 

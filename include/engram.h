@@ -580,7 +580,7 @@ int engram_mx4_pack_weight(const uint8_t* q, const uint8_t* scale, int32_t Nout,
  * a_scale  MX scales of a (T rows); 16-byte aligned
  * w        the packed weights (engram_mx4_pack_weight's); 16-byte aligned
  * kv       uint16 [T, Nout] bf16 bits, out: the hc keys then the value, as engram_wkv; 16-byte aligned
- * Limits: 0 <= T <= 2^34, T * Nout <= 2^48; K a multiple of 128 in [128, 2^20]; Nout a multiple of 8 in [8, 2^22].
+ * Limits: 0 <= T <= 2^34, T * Nout <= 2^41; K a multiple of 128 in [128, 2^20]; Nout a multiple of 8 in [8, 2^22].
  */
 int engram_wkv_mx4(const uint8_t* a, const uint8_t* a_scale, int32_t a_bits, const uint8_t* w, uint16_t* kv, int64_t T,
                    int32_t K, int32_t Nout, void* stream);

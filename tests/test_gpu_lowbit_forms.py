@@ -13,10 +13,12 @@ pytestmark = pytest.mark.gpu
 WIDE = [(500, 128, 25600), (385, 256, 25592), (513, 384, 25544), (400, 640, 25600), (2305, 896, 5400), (12300, 128, 1000),
         (384, 384, 25600), (65, 128, 25600), (129, 640, 25544), (250, 1536, 25600), (700, 256, 8200), (64, 256, 25600),
         (40, 896, 25592), (33, 128, 32776), (200, 384, 9000), (17, 1536, 25600), (32, 640, 25544), (1, 384, 25600)]
+# an eighth of the columns along all rows, rather than eight tile rows along the columns
+ALONG_ROWS = [(3000, 384, 25544), (4100, 128, 8200), (2200, 640, 25592), (9001, 256, 6400), (2050, 1536, 25600), (20000, 128, 2312)]
 
 
 @pytest.mark.parametrize("bits", [4, 8])
-@pytest.mark.parametrize("T,K,N", WIDE)
+@pytest.mark.parametrize("T,K,N", WIDE + ALONG_ROWS)
 def test_tiles_in_whole_numbers(gpu_device, T, K, N, bits):
     """Exact sums, as of the small products: multiples of a quarter whose sums stay below 2^22 quarters."""
     gen = _gen("wide", T, K, N, bits)

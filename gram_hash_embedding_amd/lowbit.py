@@ -127,7 +127,7 @@ def _operands(on, a, a_scale, w):
     K = 128 * steps
     if row != K and (row != K // 2 or a.dtype is not u8):
         raise ValueError(f"a must be [T, K={K}] (MX fp8) or [T, K/2] (MX fp4), got {tuple(a.shape)}")
-    if a_scale.numel() != _scale_bytes(T, K):
+    if a_scale.numel() != steps * ((T + 3) // 4 * 16):  # _scale_bytes
         raise ValueError("a_scale must be the MX scale array of a")
     return ap, on.ptr(a_scale, "a_scale", u8), 8 if row == K else 4, wp, T, K, 64 * groups
 

@@ -20,13 +20,15 @@ import ctypes
 from . import _check, lib
 
 torch = None  # imported by the first call, as in the rest of the package
+_current_device = _raw_stream = None
 
 
 def _load():
-    global torch
+    global torch, _current_device, _raw_stream
     import torch as t
 
     torch = t
+    _current_device, _raw_stream = t._C._cuda_getDevice, t._C._cuda_getCurrentRawStream
 
 
 BF16, F32 = 0, 1  # ENGRAM_BF16, ENGRAM_F32
@@ -68,18 +70,21 @@ class _On:
             if not like.is_cuda:
                 raise ValueError(f"{name} must be a GPU tensor")
             self.index = like.get_device()
-            if self.index != torch._C._cuda_getDevice():
+            if self.index != _current_device():
                 raise ValueError(f"{name} is on GPU {self.index}, the current device is {torch.cuda.current_device()}")
-        current = torch._C._cuda_getCurrentRawStream(self.index)
+        current = _raw_stream(self.index)
         self.handle, self.side = current, None
         if stream is not None and stream.cuda_stream != current:
             self.handle, self.side = stream.cuda_stream, stream
 
     def ptr(self, t, name, dtype, ndim=None):
         """Address of a contiguous tensor of the call's device."""
-        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == self.index and t.is_contiguous() and
-                (ndim is None or t.dim() == ndim)):
-            return t.data_ptr()
+        try:
+            if (t.dtype is dtype and t.get_device() == self.index and t.is_contiguous() and
+                    (ndim is None or t.dim() == ndim)):
+                return t.data_ptr()
+        except AttributeError:  # no tensor
+            pass
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if not t.is_cuda:

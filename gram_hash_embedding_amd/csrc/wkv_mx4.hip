@@ -89,9 +89,10 @@ __device__ inline f32x4 mfma(const i32x4& w, int sw, const AFrag<kA8>& a, int sa
 // and first loads run under another's matrix instructions.  A wave has all tokens and 64 columns, MI x 4 blocks of 16 x 16.  The
 // token rows come through LDS, 128 bytes of each (128 columns in 8 bits, 256 in 4) a stage, by direct-to-LDS loads (rows past M
 // are outside their resource and read as zero); the weights go from memory to the registers, kSets steps ahead, each read by one
-// wave only.  What bounds large products is the path of the loads through the CU's address unit (busy 84 % of the clocks where
-// two waves of a 256 x 128 tile read the same weights, at 64 bytes of a row a load), so as few and as long runs as the registers
-// allow; a few tokens are bound by the weights' latency, so as many steps in flight as they allow.
+// wave only.  Large products: matrix instructions, stores and loads add up (of 65,536 x 1,536 x 25,600 without stores 80 % of the
+// time, without any load 75 %; tiles of 256 x 128 whose waves share weights, at 64 bytes of a row a load, kept the CU's address
+// unit busy for 84 % of the clocks and took 17 % more), so as few bytes and as long runs as the registers allow.  A few tokens are
+// bound by the weights' way from HBM, so as many steps in flight as they allow (more than four measured no faster).
 //
 // 1,536 x 25,600, us with 8-bit / 4-bit rows: 1 token 5.9 / 5.9, 256 12.1 / 10.2, 8,192 237 / 174, 65,536 1,861 / 1,355 (2.8 /
 // 3.8 PFLOP/s); 6,144 x 25,600: 8,192 tokens 832 / 564 (3.1 / 4.6, the instruction alone 4.1 / 6.9).  Fused, 4 x 5,120: 256 19.1

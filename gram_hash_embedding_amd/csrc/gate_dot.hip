@@ -398,7 +398,8 @@ __global__ __launch_bounds__(kThreads) void gate_residual_kernel(ResArgs a) {
     for (int u = 0; u < P; ++u) {
         const int64_t i = base + u * kThreads;
         if (i < a.pieces) {
-            h[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a.x) + i);  // read once
+            const u32x4* at = reinterpret_cast<const u32x4*>(a.x) + i;  // read once; a short launch's are still in the caches
+            h[u] = P == 1 ? *at : __builtin_nontemporal_load(at);
             v[u] = *reinterpret_cast<const u32x4*>(a.value + t * a.ld_value + 8ll * j);    // shared by the copies
             d[u] = a.dot[t * a.hc + c];
             live[u] = !a.mask || a.mask[t] != 0;

@@ -276,7 +276,7 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         for (int q = 0; q < 2 * MI; ++q)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, mine + q * 1024, 16,
                                                      xo + static_cast<uint32_t>(8 * q * x_bytes) + (q & 1 ? xp ^ 64u : xp), 0, 0,
-                                                     kNonTemporal);
+                                                     kEarly ? 0 : kNonTemporal);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int n = nw + 16 * j + 4 * g;

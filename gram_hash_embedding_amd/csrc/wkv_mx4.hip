@@ -127,7 +127,8 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
     constexpr int kStages = kSets > 1 ? kSets / kSub + 1 : 2;
     constexpr int kRing = kStages * kStageBytes;
     constexpr int kWaveBytes = BM * 128;                    // a wave's part of the tile as bf16, behind the last step
-    // the gate's stream rows have room beside the stages (two workgroups a CU): they are loaded ahead of the steps
+    // the gate's stream rows have room beside the stages (two workgroups a CU): they are loaded ahead of the steps, and kept in
+    // the caches for the residual that follows (past them where there are many: 8,192 tokens and their residual 327 us, 334 not)
     constexpr bool kEarly = kGate && kRing + NW * kWaveBytes <= 80 * 1024;
     constexpr int kParts = kEarly ? kRing : 0;
     constexpr int kLds = kParts + NW * kWaveBytes > kRing ? kParts + NW * kWaveBytes : kRing;

@@ -112,6 +112,19 @@ __device__ inline f32x4 mfma(const i32x4& w, int sw, const AFrag<kA8>& a, int sa
 constexpr int kBufferWord3 = 0x00020000;
 constexpr int kWaitLgkmcnt0 = 0xC07F;
 constexpr int wait_vmcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | 0x0F70; }
+// until at most n of the wave's loads are outstanding (a constant once unrolled; even, up to 14)
+__device__ __forceinline__ void wait_loads(int n) {
+    switch (n) {
+        case 14: return __builtin_amdgcn_s_waitcnt(wait_vmcnt(14));
+        case 12: return __builtin_amdgcn_s_waitcnt(wait_vmcnt(12));
+        case 10: return __builtin_amdgcn_s_waitcnt(wait_vmcnt(10));
+        case 8: return __builtin_amdgcn_s_waitcnt(wait_vmcnt(8));
+        case 6: return __builtin_amdgcn_s_waitcnt(wait_vmcnt(6));
+        case 4: return __builtin_amdgcn_s_waitcnt(wait_vmcnt(4));
+        case 2: return __builtin_amdgcn_s_waitcnt(wait_vmcnt(2));
+        default: return __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
+    }
+}
 constexpr int kNonTemporal = 2;  // cache-policy operand of a load: streamed past L2
 constexpr int kXcds = 8;
 
@@ -277,7 +290,14 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
     const bool keys = kGate && n0 < p.n_key;
     u32x2 qw[4], kw[4];  // q and k of the lane's columns
     // the stream's rows of the wave's tokens and columns (rows past M: zeros), and the weights
-    auto load_stream = [&]() {
+    auto load_stream = [&]() {  // (the weights first: the rows are waited for one by one)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = nw + 16 * j + 4 * g;
+            qw[j] = *reinterpret_cast<const u32x2*>(p.q + n);
+            kw[j] = *reinterpret_cast<const u32x2*>(p.k + n);
+        }
+        fence();
         const int64_t x_bytes = static_cast<int64_t>(p.n_key) * 2;
         const int x_rows = static_cast<int>(min<int64_t>(BM, p.M - m0));
         const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
@@ -288,12 +308,6 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, mine + q * 1024, 16,
                                                      xo + static_cast<uint32_t>(8 * q * x_bytes) + (q & 1 ? xp ^ 64u : xp), 0, 0,
                                                      kEarly ? 0 : kNonTemporal);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = nw + 16 * j + 4 * g;
-            qw[j] = *reinterpret_cast<const u32x2*>(p.q + n);
-            kw[j] = *reinterpret_cast<const u32x2*>(p.k + n);
-        }
     };
 #pragma unroll
     for (int t = 0; t < kStages; ++t)
@@ -378,11 +392,13 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         // then has 64 tokens' (8,192 x 1,536 x 4 x 5,120 204 us with 4-bit rows, 263 with 8-bit ones; 216 and 284 by shuffles).
         constexpr int kRes = MI >= 4 ? MI / 4 : MI;
         float res[kRes][3], part4[3][4];
-        fence();
-        __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));  // the wave's own rows
-        fence();
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
+            if (!kEarly || i == 0) {  // the wave's own rows, the later ones left in flight (8,192 tokens 203 -> 196 us)
+                fence();
+                wait_loads(kEarly ? 0 : 2 * (MI - 1 - i));
+                fence();
+            }
             float hwk = 0.f, kk = 0.f, hh = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

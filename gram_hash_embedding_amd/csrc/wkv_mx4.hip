@@ -125,7 +125,7 @@ __device__ __forceinline__ void wait_loads(int n) {
         default: return __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
     }
 }
-constexpr int kNonTemporal = 2;  // cache-policy operand of a load: streamed past L2
+constexpr int kNonTemporal = 2;  // cache-policy operand of a load or store: streamed past L2
 constexpr int kXcds = 8;
 
 __device__ inline i32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t at) {
@@ -362,19 +362,26 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
                               static_cast<uint32_t>(r * 128 + (((4 + (g >> 1)) ^ key) << 4) + (g & 1) * 8)};
     auto quad_at = [&](int i, int j) { return mine + i * 2048 + (quad[j >> 1] ^ ((j & 1) << 5)); };
     if (!keys) {
+        // 16 rows at a time, so that their stores go out under the next ones' rounding (-2 %), by a resource that ends with row M
+        // and an offset past it behind column N: no comparison a store (-2 %)
+        const int n = nw + 8 * (lane & 7);
+        const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
+            p.kv + m0 * p.ld_out, 0, static_cast<int>(min<int64_t>(BM, p.M - m0) * p.ld_out * 2), kBufferWord3);
+        const uint32_t row_out = static_cast<uint32_t>(p.ld_out) * 2;
+        const uint32_t so = n < p.N ? line_row * row_out + static_cast<uint32_t>(n - p.n_key) * 2 : 0x80000000u;
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < MI; ++i) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<u32x2*>(quad_at(i, j)) =
                     u32x2{pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3])};
-        const int n = nw + 8 * (lane & 7);
-        uint16_t* out = p.kv + (m0 + line_row) * p.ld_out + (n - p.n_key);
+            fence();
 #pragma unroll
-        for (int q = 0; q < 2 * MI; ++q) {
-            const int t = 8 * q + line_row;
-            const u32x4 v = *reinterpret_cast<const u32x4*>(mine + t * 128 + (((lane & 7) ^ ((t >> 1) & 7)) << 4));
-            if (m0 + t < p.M && n < p.N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out + 8 * q * p.ld_out));
+            for (int q = 2 * i; q < 2 * i + 2; ++q) {
+                const int t = 8 * q + line_row;
+                const u32x4 v = *reinterpret_cast<const u32x4*>(mine + t * 128 + (((lane & 7) ^ ((t >> 1) & 7)) << 4));
+                __builtin_amdgcn_raw_buffer_store_b128(v, ro, so + static_cast<uint32_t>(8 * q) * row_out, 0, kNonTemporal);
+            }
         }
         return;
     }
@@ -636,8 +643,8 @@ extern "C" int engram_wkv_mx4_gate(const uint8_t* a, const uint8_t* a_scale, int
     const int N = (hc + 1) * dim;
     if (const char* bad = bad_shape(T, a_bits, K, N)) return fail(ENGRAM_EINVAL, "%s: %s", what, bad);
     if (T > (1ll << 31) / hc) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
-    if (ld_value < dim || ld_value % 8 != 0)
-        return fail(ENGRAM_EINVAL, "%s: ld_value=%lld must be >= dim and a multiple of 8", what, (long long)ld_value);
+    if (ld_value < dim || ld_value % 8 != 0 || ld_value > kMaxN)
+        return fail(ENGRAM_EINVAL, "%s: ld_value=%lld must be a multiple of 8 in [dim, 2^22]", what, (long long)ld_value);
     const int64_t need = engram_wkv_gate_workspace_bytes(T, hc, dim);
     if (workspace_bytes < need)
         return fail(ENGRAM_ERANGE, "%s: workspace of %lld bytes, %lld needed", what, (long long)workspace_bytes,

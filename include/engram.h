@@ -601,7 +601,7 @@ int engram_wkv_mx4(const uint8_t* a, const uint8_t* a_scale, int32_t a_bits, con
  * workspace  at least engram_wkv_gate_workspace_bytes(T, hc, dim) bytes, 16-byte aligned, caller-owned scratch (no
  *            initialisation needed); two calls in flight at once must not share it
  * Limits: as engram_wkv_mx4; 1 <= hc <= 64; T * hc <= 2^31; dim >= 256 and dim % 256 == 0; (hc+1)*dim <= 2^22;
- * ld_value >= dim, ld_value % 8 == 0.  Too small a workspace -> ENGRAM_ERANGE.
+ * dim <= ld_value <= 2^22, ld_value % 8 == 0.  Too small a workspace -> ENGRAM_ERANGE.
  */
 int engram_wkv_mx4_gate(const uint8_t* a, const uint8_t* a_scale, int32_t a_bits, const uint8_t* w, const uint16_t* x,
                         const uint16_t* q_weight, const uint16_t* k_weight, float eps, uint16_t* value, int64_t ld_value,

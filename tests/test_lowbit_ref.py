@@ -134,7 +134,7 @@ def test_wkv_mx4_validation(args, status, msg):
 @pytest.mark.parametrize("args,status,msg", [
     (dict(T=-1), 1, "T < 0"), (dict(bits=0), 1, "a_bits"), (dict(hc=0), 1, "hc=0"), (dict(hc=65), 1, "hc=65"),
     (dict(dim=128), 1, "dim=128"), (dict(dim=300), 1, "dim=300"), (dict(hc=64, dim=1 << 17), 1, "exceeds"),
-    (dict(K=96), 1, "K must"), (dict(ld=248), 1, "ld_value"), (dict(ld=260), 1, "ld_value"), (dict(wn=16), 2, "workspace"),
+    (dict(K=96), 1, "K must"), (dict(ld=248), 1, "ld_value"), (dict(ld=260), 1, "ld_value"), (dict(ld=(1 << 22) + 8), 1, "ld_value"), (dict(wn=16), 2, "workspace"),
     (dict(a=None), 1, "null"), (dict(x=None), 1, "null"), (dict(q=None), 1, "null"), (dict(value=None), 1, "null"),
     (dict(dot=None), 1, "null"), (dict(ws=None), 1, "null"), (dict(x=ODD), 1, "misaligned"), (dict(value=ODD), 1, "misaligned"),
     (dict(dot=ctypes.c_void_p(0x100001)), 1, "misaligned"), (dict(T=0, a=None), 0, "")])

@@ -104,9 +104,9 @@ __device__ inline f32x4 mfma(const i32x4& w, int sw, const AFrag<kA8>& a, int sa
 // unit busy for 84 % of the clocks and took 17 % more), so as few bytes and as long runs as the registers allow.  A few tokens are
 // bound by the weights' way from HBM, so as many steps in flight as they allow (more than four measured no faster).
 //
-// 1,536 x 25,600, us with 8-bit / 4-bit rows: 1 token 5.9 / 5.9, 256 12.1 / 10.2, 8,192 237 / 174, 65,536 1,861 / 1,355 (2.8 /
-// 3.8 PFLOP/s); 6,144 x 25,600: 8,192 tokens 832 / 564 (3.1 / 4.6, the instruction alone 4.1 / 6.9).  Fused, 4 x 5,120: 256 19.1
-// / 16.9, 8,192 289 / 220, 65,536 2,226 / 1,668.
+// 1,536 x 25,600, us with 8-bit / 4-bit rows: 1 token 5.9 / 5.8, 256 11.8 / 9.7, 8,192 229 / 162, 65,536 1,786 / 1,267 (2.9 /
+// 4.1 PFLOP/s); 6,144 x 25,600: 8,192 tokens 804 / 536 (3.2 / 4.8, the instruction alone 4.1 / 6.9).  Fused, 4 x 5,120: 256 20.6
+// / 17.8, 8,192 262 / 197, 65,536 2,024 / 1,514.
 //
 // LDS rows: the 16-byte piece c of a row at slot c ^ (row / 2) % 8: neighbouring lanes' pieces lie in different banks.
 constexpr int kBufferWord3 = 0x00020000;
@@ -525,7 +525,7 @@ __global__ __launch_bounds__(256) void mx4_pack_kernel(const uint8_t* q, const u
 // The order: eight tile rows together along the columns (16 +1 %, 4 +7 %), which reads the rows into the L2s once and the
 // weights once for every eight; or, of a plain product whose weights an XCD's L2 (4 MB) holds an eighth of, that eighth along
 // the rows, which reads the weights once and the rows eight times, where that is less: 65,536 x 1,536 x 25,600 with 4-bit rows
-// 1,350 us (1,400 the other way, 1.39 GB of reads instead of 0.47), 8,192 173 (178), with 8-bit rows 237 (238), 8,192 x 512 x 8,192
+// 1,350 us (1,400 the other way, 1.39 GB of reads instead of 0.47), 8,192 174 (179), with 8-bit rows 237 (238), 8,192 x 512 x 8,192
 // 34 (40).  Where it is more, 65,536 x 1,536 x 2,560 147 (140); where an eighth is too large, 8,192 x 6,144 x 25,600 575 (558);
 // fused, whose stream's rows it scatters, 8,192 225 (219).
 constexpr int kGroupM = 8;

@@ -198,8 +198,8 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
             const int s = stage * kSub + u / kScaleRows;
             const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
                 const_cast<uint8_t*>(p.as + (static_cast<int64_t>(s) * p.M4 + m0) * 4), 0, s < S ? scale_bytes : 0, kBufferWord3);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, st + kScales + u * 4, 4, static_cast<uint32_t>((u % kScaleRows + lane) * 4), 0,
-                                                     0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, st + kScales + u * 4, 4,
+                                                     static_cast<uint32_t>((u % kScaleRows + lane) * 4), 0, 0, 0);
         }
     };
     const int group = min(n0 / kGroupRows + wave, (p.N + kGroupRows - 1) / kGroupRows - 1);  // (columns past N are not stored)
@@ -522,7 +522,7 @@ __global__ __launch_bounds__(256) void mx4_pack_kernel(const uint8_t* q, const u
     }
 }
 
-// The order: eight tile rows together along the columns (16 +1 %, 4 +7 %), which reads the rows into the L2s once and the
+// The order: eight tile rows together along the columns (4 or 16: -1 to +1.5 %), which reads the rows into the L2s once and the
 // weights once for every eight; or, of a plain product whose weights an XCD's L2 (4 MB) holds an eighth of, that eighth along
 // the rows, which reads the weights once and the rows eight times, where that is less: 65,536 x 1,536 x 25,600 with 4-bit rows
 // 1,350 us (1,400 the other way, 1.39 GB of reads instead of 0.47), 8,192 174 (179), with 8-bit rows 237 (238), 8,192 x 512 x 8,192

@@ -105,8 +105,8 @@ __device__ inline f32x4 mfma(const i32x4& w, int sw, const AFrag<kA8>& a, int sa
 // bound by the weights' way from HBM, so as many steps in flight as they allow (more than four measured no faster).
 //
 // 1,536 x 25,600, us with 8-bit / 4-bit rows: 1 token 5.9 / 5.8, 256 11.8 / 9.7, 8,192 229 / 162, 65,536 1,786 / 1,267 (2.9 /
-// 4.1 PFLOP/s); 6,144 x 25,600: 8,192 tokens 804 / 536 (3.2 / 4.8, the instruction alone 4.1 / 6.9).  Fused, 4 x 5,120: 256 20.6
-// / 17.8, 8,192 262 / 197, 65,536 2,024 / 1,514.
+// 4.1 PFLOP/s); 6,144 x 25,600: 8,192 tokens 804 / 536 (3.2 / 4.8, the instruction alone 4.1 / 6.9).  Fused, 4 x 5,120: 256 19.4
+// / 16.8, 8,192 262 / 197, 65,536 2,024 / 1,514.
 //
 // LDS rows: the 16-byte piece c of a row at slot c ^ (row / 2) % 8: neighbouring lanes' pieces lie in different banks.
 constexpr int kBufferWord3 = 0x00020000;
@@ -150,9 +150,11 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
     constexpr int kStages = kSets > 1 ? kSets / kSub + 1 : 2;
     constexpr int kRing = kStages * kStageBytes;
     constexpr int kWaveBytes = BM * 128;                    // a wave's part of the tile as bf16, behind the last step
-    // the gate's stream rows have room beside the stages (two workgroups a CU): they are loaded ahead of the steps, and kept in
-    // the caches for the residual that follows (past them where there are many: 8,192 tokens and their residual 327 us, 334 not)
-    constexpr bool kEarly = kGate && kRing + NW * kWaveBytes <= 80 * 1024;
+    // The gate's stream rows are loaded ahead of the steps where they are few (16 tokens 9.9 us, 10.0 behind them), else behind
+    // them (256 tokens and their residual 22.7 us, 22.8 ahead).  Up to 64 tokens a tile they stay in the caches for the residual
+    // that follows (256 tokens 22.7, past them 23.5); where there are many they go past them (8,192 tokens 327, 334).
+    constexpr bool kEarly = kGate && MI <= 2;
+    constexpr int kStreamPolicy = MI <= 4 ? 0 : kNonTemporal;
     constexpr int kParts = kEarly ? kRing : 0;
     constexpr int kLds = kParts + NW * kWaveBytes > kRing ? kParts + NW * kWaveBytes : kRing;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
@@ -307,7 +309,7 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         for (int q = 0; q < 2 * MI; ++q)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, mine + q * 1024, 16,
                                                      xo + static_cast<uint32_t>(8 * q * x_bytes) + (q & 1 ? xp ^ 64u : xp), 0, 0,
-                                                     kEarly ? 0 : kNonTemporal);
+                                                     kStreamPolicy);
     };
 #pragma unroll
     for (int t = 0; t < kStages; ++t)

@@ -67,10 +67,11 @@ class LayerWeights:
 @dataclasses.dataclass
 class LayerCheckpoint:
     """What EngramForward.layer keeps of a layer for its gradient under `checkpoint=True` (tensors of its own: several calls'
-    checkpoints may live at once).  The rows that the projection read are not kept: they are gathered again."""
+    checkpoints may live at once).  The rows that the projection read are not kept: they are gathered again, by the ids."""
 
     rows: GateCheckpoint           # the stream, the keys and the value in 8 bits
     dot: "torch.Tensor"            # float32 [T, hc]
+    ids: "Optional[torch.Tensor]" = None  # [B, L, 1, C]: the layer's, as `hash` gives them in a buffer that its next call fills
 
 
 @dataclasses.dataclass
@@ -164,6 +165,10 @@ class EngramForward:
 
     def gather(self, e: int, hash_ids, events=None, packed=False):
         """Layer e's rows bf16 [T, C, D] (this object's buffer) from its table, or its packed copy."""
+        return self._gather(e, hash_ids, e, events, packed)
+
+    def _gather(self, e, hash_ids, at, events, packed):
+        """`gather` by the ids hash_ids[:, :, at]."""
         import torch
 
         lw = self.layers[e]
@@ -173,10 +178,10 @@ class EngramForward:
             if lw.packed is None:
                 raise ValueError(f"layer {e} has no packed table")
             self._timed(events, "gather_dequant_packed", lambda: engram_gather_dequant_packed(
-                hash_ids, lw.packed, lw.block_size, lw.row_start, layer=e, out=a))
+                hash_ids, lw.packed, lw.block_size, lw.row_start, layer=at, out=a))
         else:
             self._timed(events, "gather_dequant", lambda: engram_gather_dequant(
-                hash_ids, lw.weight, lw.scale, lw.block_size, lw.row_start, layer=e, out=a))
+                hash_ids, lw.weight, lw.scale, lw.block_size, lw.row_start, layer=at, out=a))
         return a
 
     def _mx_rows(self, e, hash_ids, events, packed, a, gather_mx):
@@ -311,7 +316,8 @@ class EngramForward:
             out = self._buf(("out", e), tuple(x.shape), torch.bfloat16, dev)
             _, dot, rows = self._timed(events, "gate_output_ckpt", lambda: engram_gate_output_ckpt(
                 x, kv, lw.q_weight, lw.k_weight, self.eps, token_mask, out=out))
-            return LayerCheckpoint(rows, dot), out
+            ids = hash_ids[:, :, e:e + 1].clone(memory_format=torch.contiguous_format)
+            return LayerCheckpoint(rows, dot, ids), out
         x3 = x.reshape(T, x.shape[-2], x.shape[-1])
         dot = self._buf(("dot", e), (T, x3.shape[1]), torch.float32, dev)
         if fused:
@@ -339,18 +345,22 @@ class EngramForward:
                  dx=None, checkpoint=None, packed=False):
         """LayerGrads of layer e from `dout`, the gradient of the output stream of `layer(e, hash_ids, x, token_mask=...,
         output=True)`, and what that call returned: a, kv and dot -- or, of a call with checkpoint=True, its LayerCheckpoint
-        (x, kv and dot are then not read, and `a` is gathered again, from the packed table with `packed`, unless given).
+        (hash_ids, x, kv and dot are then not read, and `a` is gathered again, from the packed table with `packed`, unless
+        given).
         `dx` (dout itself is allowed) receives the stream's gradient; by default it is a new tensor."""
         import torch
 
         lw = self.layers[e]
+        at = e  # the layer's place in the ids
+        if checkpoint is not None and checkpoint.ids is not None:
+            hash_ids, at = checkpoint.ids, 0
         T = hash_ids.shape[0] * hash_ids.shape[1]
         dev = hash_ids.device
         if dout is None:
             raise ValueError("backward needs dout")
         hc, dim = dout.shape[-2], dout.shape[-1]
         if checkpoint is not None and a is None:
-            a = self.gather(e, hash_ids, events, packed)
+            a = self._gather(e, hash_ids, at, events, packed)
         D, N = lw.weight.shape[1], lw.wkv.shape[0]
         K, n = self.C * D, T * self.C
         ws = self._buf("backward_workspace", (max(16, engram_gate_output_backward_workspace_bytes(T, hc, dim),
@@ -378,7 +388,7 @@ class EngramForward:
         self._timed(events, "wkv_backward", lambda: engram_wkv_backward(dkv, a.view(T, K), lw.wkv, da=da, dw=dw,
                                                                         workspace=ws))
         self._timed(events, "embed_grad_rows", lambda: engram_embed_grad_rows(
-            hash_ids, da, lw.weight.shape[0], row_start=lw.row_start, layer=e, unique=ids, rows=rows, count=count,
+            hash_ids, da, lw.weight.shape[0], row_start=lw.row_start, layer=at, unique=ids, rows=rows, count=count,
             workspace=ws))
         return LayerGrads(dx, dw, dq, dk, ids, rows, count)
 

@@ -20,6 +20,7 @@
 
 #include "common.h"
 #include "mx.h"
+#include "mx4_rows.h"
 
 namespace engram {
 namespace {
@@ -139,11 +140,12 @@ __device__ inline int load4(__amdgpu_buffer_rsrc_t r, uint32_t at) {
 template <bool kA8, int MI, int NW, int kSets, bool kGate>
 __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int tiles_n) {
     constexpr int BM = 16 * MI, BN = 64 * NW;
-    constexpr int kSub = kA8 ? 1 : 2;                       // steps of a stage
+    using Rows = Mx4Rows<kA8, BM, NW>;
+    constexpr int kSub = Rows::kSub;                        // steps of a stage
     constexpr int kScales = BM * 128;                       // a stage: its rows, then a word per row and step
     constexpr int kScaleRows = BM > 64 ? BM : 64;           // (a load of them writes 64 words)
     constexpr int kStageBytes = kScales + kSub * kScaleRows * 4;
-    constexpr int kRowLoads = (BM + 8 * NW - 1) / (8 * NW);  // per wave and stage: 8 rows each
+    constexpr int kRowLoads = Rows::kLoads;                 // per wave and stage
     constexpr int kScaleLoads = (kSub * kScaleRows + BN - 1) / BN;  // 64 rows of a step each
     constexpr int kLoads = kRowLoads + kScaleLoads;
     constexpr int kWLoads = 5;
@@ -176,14 +178,10 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         m0 = static_cast<int64_t>(p.across ? i : o) * BM;
         n0 = static_cast<int>(p.across ? o : i) * BN;
     }
-    const int row_bytes = S * (kA8 ? 128 : 64);
+    const int row_bytes = Rows::row_bytes(S);
     const int valid_bytes = static_cast<int>(min<int64_t>(BM, p.M - m0)) * row_bytes;
-    // row loads: load q of the wave fills 1 KB, rows 8 (kRowLoads wave + q) on, lane l slot l % 8 of row l / 8; the key of an odd
-    // group of 8 rows is that of an even one plus 4
-    const int row0 = wave * kRowLoads * 8 % BM;  // (with fewer rows than the waves load, some load the same)
-    const int at_row = row0 + (lane >> 3);
-    const uint32_t piece = static_cast<uint32_t>(((lane & 7) ^ ((at_row >> 1) & 7)) << 4);
-    const uint32_t voff[2] = {at_row * row_bytes + piece, at_row * row_bytes + (piece ^ 64u)};
+    const int row0 = Rows::first(wave);  // load q of the wave fills 1 KB, rows row0 + 8 q on
+    const uint32_t voff[2] = {Rows::offset(row0, lane, false, row_bytes), Rows::offset(row0, lane, true, row_bytes)};
     const int scale_bytes = static_cast<int>(min<int64_t>(BM, p.M4 - m0)) * 4;
     // load q (0 .. kLoads - 1) of a stage into the one at `slot`: the rows', then their scales; past the last step nothing is
     // fetched (zeros are written)
@@ -191,10 +189,10 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
         uint8_t* st = lds + slot;
         if (q < kRowLoads) {
             const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<uint8_t*>(p.a + m0 * row_bytes), 0, stage * kSub < S ? valid_bytes : 0, kBufferWord3);
+                const_cast<uint8_t*>(p.a + m0 * row_bytes + Rows::begin(stage)), 0, Rows::bytes(stage, S, valid_bytes),
+                kBufferWord3);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, st + (row0 + 8 * q) * 128, 16,
-                                                     voff[q & 1] + static_cast<uint32_t>(q * 8 * row_bytes),
-                                                     stage * 128, 0, 0);
+                                                     voff[q & 1] + Rows::load_rows(q, row_bytes), 0, 0, 0);
         } else {
             const int u = (wave + NW * (q - kRowLoads)) * 64 % (kSub * kScaleRows);  // (some waves load the same here too)
             const int s = stage * kSub + u / kScaleRows;

@@ -223,8 +223,8 @@ def engram_gate_output_ckpt(x, kv, q_weight, k_weight, eps, token_mask=None, out
                             stream=None):
     """(out, dot, GateCheckpoint): engram_gate_output of x bf16 [T, hc, dim] (or [B, L, hc, dim]) and kv [T, >= (hc+1)*dim],
     with x, the keys and the value kept in 8 bits (engram_ckpt_save's, of their rows of dim) for
-    engram_gate_output_backward_ckpt.  out (x's shape; x itself is allowed), dot (float32 [T, hc]) and `checkpoint` are
-    allocated if not given."""
+    engram_gate_output_backward_ckpt.  out (x's shape; x itself is allowed), dot (float32 [T, hc]) and `checkpoint`, or those
+    of its tensors that are None, are allocated if not given."""
     on = _t._On(stream, x, "x")
     torch = _t.torch
     bf, f32 = torch.bfloat16, torch.float32
@@ -248,14 +248,14 @@ def engram_gate_output_ckpt(x, kv, q_weight, k_weight, eps, token_mask=None, out
 
 
 def _checkpoint(on, given, T, hc, dim):
-    """(GateCheckpoint, its addresses): the given one, checked, or a new one."""
+    """(GateCheckpoint, its addresses): the given one's tensors, checked, and new ones where it has none."""
     i8, u8, nb = _t.torch.int8, _t.torch.uint8, (dim + 31) // 32
     x, xs, kv, kvs = given if given is not None else (None, None, None, None)
     x, p0 = _out(on, x, "checkpoint.x", (T, hc, dim), i8)
     xs, p1 = _out(on, xs, "checkpoint.x_scale", (T, hc, nb), u8)
     kv, p2 = _out(on, kv, "checkpoint.kv", (T, hc + 1, dim), i8)
     kvs, p3 = _out(on, kvs, "checkpoint.kv_scale", (T, hc + 1, nb), u8)
-    return (given if given is not None else GateCheckpoint(x, xs, kv, kvs)), (p0, p1, p2, p3)
+    return GateCheckpoint(x, xs, kv, kvs), (p0, p1, p2, p3)
 
 
 def engram_gate_output_backward_ckpt(checkpoint, q_weight, k_weight, eps, dot, dout, token_mask=None, dx=None, dkv=None,

@@ -102,7 +102,7 @@ __global__ __launch_bounds__(L < kThreads ? kThreads : L) void gate_output_ckpt_
     __shared__ float part[(L + 63) / 64][3];
     constexpr int kRows = L < kThreads ? kThreads / L : 1;  // of a workgroup
     const int64_t n = a.T * a.hc, groups = (n + kRows - 1) / kRows;
-    const int64_t group = part_of_group(group_index(), groups, (a.hc + kRows - 1) / kRows);
+    const int64_t group = part_of_group(group_index<kRows * L>(), groups, (a.hc + kRows - 1) / kRows);
     if (group >= groups) return;
     const int lane = kRows == 1 ? threadIdx.x : threadIdx.x % L;
     const int64_t at = kRows == 1 ? group : group * kRows + threadIdx.x / L;  // token * hc + copy
@@ -167,8 +167,8 @@ __global__ __launch_bounds__(L < kThreads ? kThreads : L) void gate_output_ckpt_
 template <int L, int P>
 int launch_output(const CkptArgs& a, hipStream_t stream, const char* what) {
     constexpr int kRows = L < kThreads ? kThreads / L : 1;
-    hipLaunchKernelGGL((gate_output_ckpt_kernel<L, P>), group_grid((a.T * a.hc + kRows - 1) / kRows), dim3(kRows * L), 0, stream,
-                       a);
+    hipLaunchKernelGGL((gate_output_ckpt_kernel<L, P>), group_grid((a.T * a.hc + kRows - 1) / kRows, kRows * L), dim3(kRows * L),
+                       0, stream, a);
     return check_launch(what);
 }
 
@@ -220,7 +220,7 @@ extern "C" int engram_gate_output_ckpt(const uint16_t* x, const uint16_t* kv, in
         return fail(ENGRAM_EINVAL, "%s: dim=%d must be a multiple of 8 in [8, 8192]", what, dim);
     if (ld_kv < static_cast<int64_t>(hc + 1) * dim || ld_kv % 8 != 0)
         return fail(ENGRAM_EINVAL, "%s: ld_kv=%lld must be >= (hc+1)*dim and a multiple of 8", what, (long long)ld_kv);
-    if (T > (1ll << 38) / hc) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
+    if (T > (1ll << 37) / hc) return fail(ENGRAM_EINVAL, "%s: too many tokens", what);
     if (T == 0) return ENGRAM_OK;
     if (!x || !kv || !q_weight || !k_weight || !out || !dot || !x_q || !x_scale || !kv_q || !kv_scale)
         return fail(ENGRAM_EINVAL, "%s: null pointer", what);

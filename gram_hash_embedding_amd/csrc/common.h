@@ -18,14 +18,17 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
-// A grid of `groups` workgroups (at most kMostGroups) of up to 256 threads, along x as far as its threads stay below 2^32
-// and then along y, and a workgroup's index in it, which can be groups or more.
-constexpr int64_t kMaxGroupsX = 1ll << 23, kMostGroups = kMaxGroupsX * 65535;
-inline dim3 group_grid(int64_t groups) {
-    const int64_t x = groups < kMaxGroupsX ? groups : kMaxGroupsX;
+// A grid of `groups` workgroups (at most 65,535 times kMaxThreadsX / threads) of up to `threads` threads, along x as far as its
+// threads stay below 2^32 and then along y, and a workgroup's index in it, which can be groups or more.
+constexpr int64_t kMaxThreadsX = 1ll << 31;
+inline dim3 group_grid(int64_t groups, int threads = 256) {
+    const int64_t most = kMaxThreadsX / threads, x = groups < most ? groups : most;
     return dim3(static_cast<unsigned>(x), static_cast<unsigned>((groups + x - 1) / x));
 }
-__device__ inline int64_t group_index() { return blockIdx.y * kMaxGroupsX + blockIdx.x; }
+template <int kThreads = 256>
+__device__ inline int64_t group_index() {
+    return blockIdx.y * (kMaxThreadsX / kThreads) + blockIdx.x;
+}
 
 // The part of the work, of `parts`, that workgroup `group` of as many does where `run` parts in a row share data: workgroups go
 // to the 8 XCDs in turn, so those that are 8 apart take a run's parts, and its data is read into one L2.

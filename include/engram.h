@@ -828,7 +828,7 @@ int engram_ckpt_load(const int8_t* q, const uint8_t* scale, int64_t rows, int32_
  * dot       float32 [T, hc], out (kept for the gradient); 4-byte aligned
  * x_q       int8 [T, hc, dim], out; 8-byte aligned;     x_scale   uint8 [T, hc, ceil(dim/32)], out
  * kv_q      int8 [T, hc+1, dim], out; 8-byte aligned;   kv_scale  uint8 [T, hc+1, ceil(dim/32)], out
- * Limits: T * hc <= 2^38; 1 <= hc <= 64; 8 <= dim <= 8192 and dim % 8 == 0.
+ * Limits: T * hc <= 2^37; 1 <= hc <= 64; 8 <= dim <= 8192 and dim % 8 == 0.
  */
 int engram_gate_output_ckpt(const uint16_t* x, const uint16_t* kv, int64_t ld_kv, const uint16_t* q_weight,
                             const uint16_t* k_weight, float eps, const uint8_t* token_mask, uint16_t* out, float* dot,

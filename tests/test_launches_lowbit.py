@@ -143,6 +143,19 @@ def test_outputs_and_gradients_of_any_size(library, T, hc, dim):
     assert status == 0 and len(launches) == 2 and _fits(launches)
 
 
+@pytest.mark.parametrize("dim", [8, 256, 1024, 1032, 6144, 6152, 8192])
+@pytest.mark.parametrize("T,hc", [(1 << 22, 1), ((1 << 22) + 1, 1), (1 << 23, 1), ((1 << 23) + 3, 3), (1 << 31, 64)])
+def test_outputs_of_workgroups_of_any_width(library, T, hc, dim):
+    """Past 6,144 columns a workgroup has 512 threads: its rows of the grid are half as long.  The limit itself: as many rows as
+    no memory holds."""
+    status, launches = _output(library, T, hc, dim)
+    assert status == 0 and len(launches) == 1 and _fits(launches)
+    x, y, _, bx, _, _ = launches[0]
+    a_row = 16 if dim <= 128 else 32 if dim <= 256 else 64 if dim <= 1024 else bx
+    assert 0 <= x * y - -(-T * hc // (bx // a_row)) < x
+    assert _output(library, (1 << 37) // hc + 1, hc, dim) == (1, [])
+
+
 CALLS = {
     "quantisation": lambda lib, f: _quant(lib, 251, 1536, f),
     "packing": lambda lib, f: _pack(lib, 25600, 1536, f),

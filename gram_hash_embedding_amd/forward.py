@@ -304,7 +304,7 @@ class EngramForward:
         import torch
 
         lw = self.layers[e]
-        T = hash_ids.shape[0] * hash_ids.shape[1]
+        T, K = hash_ids.shape[0] * hash_ids.shape[1], lw.wkv.shape[1]
         dev = hash_ids.device
         if checkpoint and (fused or not output):
             raise ValueError("a checkpoint is of the layer's output, from the unfused projection")
@@ -312,7 +312,7 @@ class EngramForward:
             a = self.gather(e, hash_ids, events, packed)
         if checkpoint:
             kv = self._buf("kv", (T, lw.wkv.shape[0]), torch.bfloat16, dev)
-            self._timed(events, "wkv", lambda: engram_wkv(a.view(T, -1), lw.wkv, out=kv))
+            self._timed(events, "wkv", lambda: engram_wkv(a.view(T, K), lw.wkv, out=kv))
             out = self._buf(("out", e), tuple(x.shape), torch.bfloat16, dev)
             _, dot, rows = self._timed(events, "gate_output_ckpt", lambda: engram_gate_output_ckpt(
                 x, kv, lw.q_weight, lw.k_weight, self.eps, token_mask, out=out))
@@ -325,14 +325,14 @@ class EngramForward:
             value = self._buf(("value", e), (T, dim), torch.bfloat16, dev)
             ws = self._buf("workspace", (engram_wkv_gate_workspace_bytes(T, hc, dim),), torch.uint8, dev)
             self._timed(events, "wkv_gate", lambda: engram_wkv_gate(
-                a.view(T, -1), lw.wkv, x3, lw.q_weight, lw.k_weight, self.eps, value=value, dot=dot, workspace=ws))
+                a.view(T, K), lw.wkv, x3, lw.q_weight, lw.k_weight, self.eps, value=value, dot=dot, workspace=ws))
             if output:
                 out = self._buf(("out", e), tuple(x.shape), torch.bfloat16, dev)
                 self._timed(events, "gate_residual", lambda: engram_gate_residual(x, value, dot, token_mask, out=out))
                 return a, value, dot, out
             return a, value, dot
         kv = self._buf(("kv", e), (T, lw.wkv.shape[0]), torch.bfloat16, dev)
-        self._timed(events, "wkv", lambda: engram_wkv(a.view(T, -1), lw.wkv, out=kv))
+        self._timed(events, "wkv", lambda: engram_wkv(a.view(T, K), lw.wkv, out=kv))
         if output:
             out = self._buf(("out", e), tuple(x.shape), torch.bfloat16, dev)
             self._timed(events, "gate_output", lambda: engram_gate_output(
@@ -445,7 +445,7 @@ class EngramForward:
         ws = self._buf("workspace", (self.E * engram_wkv_gate_workspace_bytes(T, hc, dim),), torch.uint8, dev)
         L = self.layers
         self._timed(events, "wkv_gate_layers", lambda: engram_wkv_gate_layers(
-            [r.view(T, -1) for r in rows], [lw.wkv for lw in L], x3, [lw.q_weight for lw in L],
+            [r.view(T, lw.wkv.shape[1]) for r, lw in zip(rows, L)], [lw.wkv for lw in L], x3, [lw.q_weight for lw in L],
             [lw.k_weight for lw in L], self.eps, value=values, dot=dots, workspace=ws))
         if not output:
             return dots

@@ -1,5 +1,5 @@
-"""Training steps with 8-bit checkpoints as a loop runs them: the ids as `hash` and `hash_gather` return them, and several
-micro-batches between their forwards and their backwards."""
+"""Training steps with 8-bit checkpoints as a loop runs them: the ids as `hash` and `hash_gather` return them, several
+micro-batches between their forwards and their backwards, and batches without tokens."""
 import dataclasses
 
 import pytest
@@ -45,3 +45,26 @@ def test_micro_batches_with_the_ids_of_hash(gpu_device, gathered):
             want = fwd.backward(e, own, xl, a, kvl, ck[e].dot, dout)
             for p, r in zip(got, [want.dx, *want.tensors(), want.row_ids, want.row_count]):
                 assert torch.equal(p, r), e
+
+
+@pytest.mark.parametrize("shape", [(1, 0), (0, 7)])
+def test_a_batch_without_tokens(gpu_device, shape):
+    """Every form of the path takes one: nothing is kept, the weights' gradients are zeros and no row is reached."""
+    cfg = dataclasses.replace(CFG, head_dim=64)
+    wl = sw.build(cfg, device=gpu_device, packed=True)
+    fwd, hc, dim = wl.fwd, cfg.hc_mult, cfg.dim
+    for lw in fwd.layers:
+        lw.wkv_mx4 = g.engram_mx4_pack_weight(*g.engram_mx4_quant(lw.wkv))
+    tokens = torch.empty(shape, dtype=torch.int64, device=gpu_device)
+    x = torch.empty((*shape, hc, dim), dtype=torch.bfloat16, device=gpu_device)
+    for kw in (dict(), dict(fused=True), dict(hash_gather=True), dict(fused=True, all_layers=True), dict(fp4=True),
+               dict(fp4=True, fused=True), dict(fp4=True, a_bits=4), dict(fp4=True, fused=True, gather_mx=True)):
+        for t in fwd.step(tokens, 0, x, output=True, **kw):
+            assert t.shape == x.shape, kw
+    ids = fwd.hash(tokens, 0)
+    a, kv, dot, out = fwd.layer(0, ids, x, output=True)
+    ck, got = fwd.layer(0, ids, x, output=True, checkpoint=True)
+    assert out.shape == got.shape == x.shape and ck.rows.x.shape == (0, hc, dim) and ck.rows.kv.shape == (0, hc + 1, dim)
+    for grads in (fwd.backward(0, ids, x, a, kv, dot, x), fwd.backward(0, None, dout=x, checkpoint=ck)):
+        assert grads.dx.shape == x.shape and int(grads.row_count) == 0 and grads.row_ids.numel() == grads.rows.numel() == 0
+        assert not grads.dwkv.any() and not grads.dq.any() and not grads.dk.any()

@@ -1,5 +1,5 @@
-// Pieces of the gate shared by its kernels (gate_dot.hip, checkpoint.hip): sums over a wave, the gate of a dot, and the
-// residual.
+// Pieces of the gate shared by its kernels (gate_dot.hip, gate_grad.hip, checkpoint.hip, wkv_mx4.hip): pairs of bf16, sums over a
+// wave, the gate of a dot, and the residual.
 #pragma once
 
 #include "common.h"

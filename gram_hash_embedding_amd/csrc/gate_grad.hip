@@ -27,6 +27,7 @@
 // 2 of 5,120 188, 1 of 5,120 129; 3 of 2,048 164.
 #include <type_traits>
 
+#include "gate.h"
 #include "mx.h"
 #include "rows.h"
 
@@ -57,12 +58,6 @@ struct GateGradArgs {
     int hc, dim;
     float eps, inv_dim, rsqrt_dim;
 };
-
-__device__ inline float wave_sum(float v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-    return v;
-}
 
 // Where the rows of the stream (copy c of token t) and of the keys and the value (row c of token t, the value's being hc)
 // come from: eight consecutive elements of one, as they lie in memory until they are widened.

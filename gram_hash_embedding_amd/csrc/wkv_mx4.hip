@@ -19,6 +19,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "gate.h"
 #include "mx.h"
 #include "mx4_rows.h"
 
@@ -52,13 +53,7 @@ struct Mx4Args {
     int n_key;
 };
 
-__device__ inline uint32_t pack_bf16(float lo, float hi) {
-    const bf16x2 v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};  // to nearest even
-    return __builtin_bit_cast(uint32_t, v);
-}
 __device__ inline bf16x2 as_pair(uint32_t w) { return __builtin_bit_cast(bf16x2, w); }
-__device__ inline float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ inline float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // c + a.lo * b.lo + a.hi * b.hi over packed bf16 pairs, fp32 accumulation
 __device__ inline float dot2_bf16(uint32_t a, uint32_t b, float c) {
@@ -374,7 +369,7 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<u32x2*>(quad_at(i, j)) =
-                    u32x2{pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3])};
+                    u32x2{pack2_bf16(acc[i][j][0], acc[i][j][1]), pack2_bf16(acc[i][j][2], acc[i][j][3])};
             fence();
 #pragma unroll
             for (int q = 2 * i; q < 2 * i + 2; ++q) {
@@ -410,7 +405,7 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 // the product is a bf16 tensor before it is used, as the other forms of the projection round it
-                const uint32_t k01 = pack_bf16(acc[i][j][0], acc[i][j][1]), k23 = pack_bf16(acc[i][j][2], acc[i][j][3]);
+                const uint32_t k01 = pack2_bf16(acc[i][j][0], acc[i][j][1]), k23 = pack2_bf16(acc[i][j][2], acc[i][j][3]);
                 const u32x2 x = *reinterpret_cast<const u32x2*>(quad_at(i, j));
                 const uint32_t x01 = x[0], x23 = x[1];
                 hwk += lo_bf16(x01) * wq[j][0] * lo_bf16(k01);

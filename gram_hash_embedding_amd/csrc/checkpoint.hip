@@ -8,7 +8,7 @@
 //                              rows it has in registers, instead of a second pass that reads them (gate_grad.hip reads them)
 //
 // All three are bound by HBM: 32,768 x 5,120 saved in 92 us (5.6 TB/s), loaded in 86 (5.9); the output of 8,192 x 4 x 5,120 268
-// (5.5).  Keeping the same rows by engram_ckpt_save behind engram_gate_output would read them again: 754 MB, some 110 us.
+// (5.5).  engram_gate_output and then engram_ckpt_save, which reads the same 754 MB again, take 213 and 201.
 #include "gate.h"
 #include "mx.h"
 

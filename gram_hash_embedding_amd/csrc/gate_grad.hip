@@ -23,8 +23,8 @@
 // 8,192 tokens, both launches: 4 copies of 5,120 335 us (5.5 TB/s of the bytes above), of 2,048 146 (5.0), of 1,024 84
 // (4.4), of 256 41 (2.2, bound by the tokens' chains of barrier and sums), of 8,192 633 (4.7); 2 of 5,120 193 (5.2), 1 of
 // 5,120 125 (4.7); 3 of 2,048 184 (3.1, the kernel for any count of copies, which takes a barrier a copy).  From checkpoints:
-// 4 copies of 5,120 318 us (4.7 TB/s: fewer bytes for the same arithmetic), of 2,048 127, of 1,024 74, of 256 45, of 8,192 485;
-// 2 of 5,120 188, 1 of 5,120 129; 3 of 2,048 164.
+// 4 copies of 5,120 318 us (4.7 TB/s: fewer bytes for the same arithmetic), of 2,048 127, of 1,024 75, of 256 44, of 8,192 484;
+// 2 of 5,120 188, 1 of 5,120 128; 3 of 2,048 164.
 #include <type_traits>
 
 #include "gate.h"

@@ -356,8 +356,10 @@ __global__ __launch_bounds__(kMainThreads, 1) void wkv_kernel(WkvArgs p) {
         uint8_t* sw = lds + stage * kStageBytes + kABytes + wave * 64 * 128;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            // the row offset goes into the VGPR offset: a raw buffer's range check covers the VGPR and
-            // immediate offsets but not the SGPR offset, which carries only the slab's column
+            // the row offset goes into the VGPR offset, the SGPR offset carries only the slab's column: whether
+            // a raw buffer's range check counts the latter (gfx950 does: it compares the VGPR and immediate
+            // offsets with the size less the SGPR offset, or with nothing where that is more) or not (as the
+            // compiler describes it), rows past the last are out of range and a valid row's pieces are not
             // (row bases are multiples of 128 bytes: the XOR flips the piece's swizzle bit only)
             const uint32_t flip = (q & 1) ? (4u << 4) : 0u;
             const uint32_t qrows = static_cast<uint32_t>(q * 8 * row_bytes);

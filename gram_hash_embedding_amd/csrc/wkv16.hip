@@ -145,8 +145,8 @@ __device__ __forceinline__ void wkv16_body(const W16Args& p) {
 
     // ---- slab loads (loader waves): wave w fills rows [64w, 64w+64) of the A and of the W slab, 8 rows per
     // instruction, lane l at slot (l & 7) of row base + 8q + (l >> 3), fetching the piece the swizzle puts
-    // there.  Rows past M or N fall outside their resource and read as zero; the row offset sits in the
-    // range-checked VGPR operand, the SGPR operand carries only the slab's column.
+    // there.  Rows past M or N fall outside their resource and read as zero: the row offset sits in the VGPR
+    // operand, so that they do whether or not the range check counts the SGPR operand, the slab's column.
     const int ld_r = lane >> 3, ld_slot = lane & 7;
     const uint32_t vo_piece = static_cast<uint32_t>(ld_r * row_bytes + ((ld_slot ^ (ld_r >> 1)) << 4));
     const uint32_t vo_rows = vo_piece + static_cast<uint32_t>(wave * 64 * row_bytes);

@@ -100,9 +100,10 @@ __device__ inline f32x4 mfma(const i32x4& w, int sw, const AFrag<kA8>& a, int sa
 // unit busy for 84 % of the clocks and took 17 % more), so as few bytes and as long runs as the registers allow.  A few tokens are
 // bound by the weights' way from HBM, so as many steps in flight as they allow (more than four measured no faster).
 //
-// 1,536 x 25,600, us with 8-bit / 4-bit rows: 1 token 5.9 / 5.8, 256 11.8 / 9.7, 8,192 229 / 162, 65,536 1,786 / 1,267 (2.9 /
-// 4.1 PFLOP/s); 6,144 x 25,600: 8,192 tokens 804 / 536 (3.2 / 4.8, the instruction alone 4.1 / 6.9).  Fused, 4 x 5,120: 256 19.4
-// / 16.8, 8,192 262 / 197, 65,536 2,024 / 1,514.
+// 1,536 x 25,600, us with 8-bit / 4-bit rows: 1 token 6.9 / 6.8 with the weights from HBM and 5.9 / 5.8 where the Infinity Cache
+// holds them, 256 16.4 / 14.9 and 11.9 / 9.8, 8,192 231 / 166, 65,536 1,834 / 1,291 (2.8 / 4.0 PFLOP/s); 6,144 x 25,600: 8,192
+// tokens 819 / 538 (3.1 / 4.8, the instruction alone 4.1 / 6.9).  Fused, 4 x 5,120: 256 20.9 / 19.5 and 19.0 / 17.6, 8,192 266 /
+// 199, 65,536 2,064 / 1,540.
 //
 // LDS rows: the 16-byte piece c of a row at slot c ^ (row / 2) % 8: neighbouring lanes' pieces lie in different banks.
 constexpr int kBufferWord3 = 0x00020000;
@@ -147,9 +148,9 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
     constexpr int kStages = kSets > 1 ? kSets / kSub + 1 : 2;
     constexpr int kRing = kStages * kStageBytes;
     constexpr int kWaveBytes = BM * 128;                    // a wave's part of the tile as bf16, behind the last step
-    // The gate's stream rows are loaded ahead of the steps where they are few (16 tokens 9.9 us, 10.0 behind them), else behind
-    // them (256 tokens and their residual 22.7 us, 22.8 ahead).  Up to 64 tokens a tile they stay in the caches for the residual
-    // that follows (256 tokens 22.7, past them 23.5); where there are many they go past them (8,192 tokens 327, 334).
+    // The gate's stream rows are loaded ahead of the steps where they are few (16 tokens 9.9 us, 10.3 behind them), else behind
+    // them (256 tokens and their residual 23.3 us, 23.5 ahead).  Up to 64 tokens a tile they stay in the caches for the residual
+    // that follows (256 tokens 23.3, past them 24.0); where there are many they go past them (8,192 tokens 320, 330).
     constexpr bool kEarly = kGate && MI <= 2;
     constexpr int kStreamPolicy = MI <= 4 ? 0 : kNonTemporal;
     constexpr int kParts = kEarly ? kRing : 0;
@@ -391,12 +392,12 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& p, int tiles_m, int
                 wq[j][2 * e + 1] = hi_bf16(qw[j][e]) * hi_bf16(kw[j][e]);
             }
         // The sums over the four lanes of a token by swaps of lanes between registers, of four times 16 tokens together: a register
-        // then has 64 tokens' (8,192 x 1,536 x 4 x 5,120 204 us with 4-bit rows, 263 with 8-bit ones; 216 and 284 by shuffles).
+        // then has 64 tokens' (8,192 x 1,536 x 4 x 5,120: 5 % less time with 4-bit rows, 7 % with 8-bit ones, than by shuffles).
         constexpr int kRes = MI >= 4 ? MI / 4 : MI;
         float res[kRes][3], part4[3][4];
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            if (!kEarly || i == 0) {  // the wave's own rows, the later ones left in flight (8,192 tokens 203 -> 196 us)
+            if (!kEarly || i == 0) {  // the wave's own rows, the later ones left in flight (8,192 tokens: -3 %)
                 fence();
                 wait_loads(kEarly ? 0 : 2 * (MI - 1 - i));
                 fence();
@@ -520,9 +521,9 @@ __global__ __launch_bounds__(256) void mx4_pack_kernel(const uint8_t* q, const u
 // The order: eight tile rows together along the columns (4 or 16: -1 to +1.5 %), which reads the rows into the L2s once and the
 // weights once for every eight; or, of a plain product whose weights an XCD's L2 (4 MB) holds an eighth of, that eighth along
 // the rows, which reads the weights once and the rows eight times, where that is less: 65,536 x 1,536 x 25,600 with 4-bit rows
-// 1,350 us (1,400 the other way, 1.39 GB of reads instead of 0.47), 8,192 174 (179), with 8-bit rows 237 (238), 8,192 x 512 x 8,192
-// 34 (40).  Where it is more, 65,536 x 1,536 x 2,560 147 (140); where an eighth is too large, 8,192 x 6,144 x 25,600 575 (558);
-// fused, whose stream's rows it scatters, 8,192 225 (219).
+// 1,292 us (1,331 the other way, 1.39 GB of reads instead of 0.47), 8,192 165 (171), with 8-bit rows 233 (232), 8,192 x 512 x 8,192
+// 32 (37).  Where it is more, 65,536 x 1,536 x 2,560 139 (135); where an eighth is too large, 8,192 x 6,144 x 25,600 571 (550);
+// fused, whose stream's rows it scatters, 8,192 201 (200).
 constexpr int kGroupM = 8;
 constexpr int64_t kHeld = 3 << 20;
 
@@ -542,7 +543,7 @@ int launch_tiles(Mx4Args p, hipStream_t stream, const char* what) {
 // The tile: 128 tokens where that makes one and a half tiles or more for every CU; 64, then 32, where it makes one for half of
 // them and is more than half filled; else 16, by two waves.  A small tile has more steps of weights in flight, and few tiles
 // take the latency of their chain of steps; many are bound by what they read.  8-bit rows of 1,536 columns, us at 16 / 32 / 64
-// / 128 tokens a tile: 1 x 25,600 5.8 / 6.1 / 7.7 / 11.4; 64 x 25,600 8.3 / 7.0 / 8.3 / 11.8; 128 13.0 / 9.4 / 8.4 / 12.2; and
+// / 128 tokens a tile (the weights in the Infinity Cache): 1 x 25,600 5.8 / 6.1 / 7.7 / 11.4; 64 x 25,600 8.3 / 7.0 / 8.3 / 11.8; 128 13.0 / 9.4 / 8.4 / 12.2; and
 // at 16 / 64 / 128: 256 20.6 / 12.1 / 12.5; 384 28.6 / 18.3 / 19.4; 512 36 / 22.7 / 19.8; 1,024 x 2,560 10.4 / 8.1 / 12.0.
 template <bool kA8, bool kGate>
 int launch(const Mx4Args& p, hipStream_t stream, const char* what) {

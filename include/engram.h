@@ -326,7 +326,7 @@ int engram_gate_dot(const uint16_t* x, const uint16_t* kv, int64_t ld_kv, const 
  *   shared by its hc copies).  The product and the sum are rounded separately (no
  *   fused multiply-add), then the sum is rounded to bf16 to nearest even, so a
  *   masked token's output equals x bit for bit (x = -0 with value >= +0 gives +0,
- *   by IEEE addition).
+ *   by IEEE addition; a value that is an infinity or a NaN gives NaN, as zero times it is).
  *
  * x          uint16 [T, hc, dim] bf16 bits; 16-byte aligned
  * kv         uint16 bf16 bits, row stride ld_kv >= (hc+1)*dim: keys in columns
@@ -492,7 +492,8 @@ int engram_gather_mx_packed(const int64_t* hash_ids, int64_t T, int64_t id_token
  * engram_wkv_mx -- the projection on MX fp8 operands:
  *   kv[t,o] = bf16( sum over 32-column blocks b of
  *                   2^(a_scale[t,b]-127) * 2^(w_scale[o,b]-127) * sum_{k in b} e4m3(a[t,k]) * e4m3(w[o,k]) )
- * with fp32 accumulation and one bf16 rounding (round to nearest even).
+ * with the matrix core's accumulation (in fp32, but up to 2^-12 of the sum of the products' magnitudes may be lost) and one
+ * bf16 rounding (round to nearest even).
  *
  * a        uint8 [T, K] E4M3FN bytes; 16-byte aligned
  * a_scale  MX scales of a (T rows), layout above; 16-byte aligned
@@ -573,8 +574,9 @@ int engram_mx4_pack_weight(const uint8_t* q, const uint8_t* scale, int32_t Nout,
  * engram_wkv_mx4 -- the projection on MX fp4 weights:
  *   kv[t,o] = bf16( sum over 32-column blocks b of
  *                   2^(a_scale[t,b]-127) * 2^(w_scale[o,b]-127) * sum_{k in b} a[t,k] * w[o,k] )
- * with fp32 accumulation in ascending order of 128-column steps, and one bf16 rounding: an output's bits depend on its
- * row and weights alone, not on the other rows of the call.
+ * with the matrix core's accumulation in ascending order of 128-column steps, and one bf16 rounding: an output's bits depend on
+ * its row and weights alone, not on the other rows of the call.  The matrix core adds a step's products to its fp32 sums less
+ * exactly than fp32 additions would where elements are E4M3: up to 2^-12 of the sum of their magnitudes may be lost.
  *
  * a        uint8 [T, K] E4M3FN bytes (a_bits 8) or [T, K/2] E2M1 pairs (a_bits 4); 16-byte aligned
  * a_scale  MX scales of a (T rows); 16-byte aligned
